@@ -420,6 +420,63 @@ int nvfp4_moe_forward_noalloc(const uint16_t* x, const int32_t* topk_ids, const 
 int nvfp4_route_topk(const float* logits, int64_t T, int64_t E, int64_t topk,
                      int32_t* topk_ids, float* topk_weights, hipStream_t stream);
 
+/* ------------------------------------------------------------------------ *
+ * nvfp4_gated_forward - a gated feed-forward block in bf16: both projections,
+ * the activation and the product (the dense or shared expert beside the
+ * routed ones; its weights are not quantized and may be trained):
+ *
+ *   gate = x @ w13[:, :I], up = x @ w13[:, I:]        float32 sums
+ *   act  = bf16(silu(gate) * up), silu(z) = z / (1 + exp(-z)), float32 from
+ *          the unrounded sums, one rounding
+ *
+ *   x        (T, H) bf16
+ *   w13      (H, 2I) bf16, the math layout [gate | up] along the columns (one
+ *            matrix of nvfp4_quantize_weights' input), 2 H I elements
+ *   act      (T, I) bf16 out
+ *   gate_up  NULL, or (T, 2I) bf16 out: [bf16(gate) | bf16(up)], what
+ *            nvfp4_gated_backward takes
+ *   H % 16 == 0, I % 16 == 0, T <= 2^24, H <= 2^20, I <= 2^20, else
+ *   NVFP4_ESHAPE; every pointer 16-byte aligned. Outputs overlap no input and
+ *   each other. T == 0 enqueues nothing.
+ * Results are deterministic: the order of every sum depends on the sizes
+ * alone. A row of x affects no other row of the outputs, whatever its values.
+ *
+ * Workspace: nvfp4_gated_workspace(T, H, I) bytes, 256-byte aligned: partial
+ * sums of small batches, whose few tiles have H cut into chunks. It returns 0
+ * for invalid sizes.
+ * ------------------------------------------------------------------------ */
+size_t nvfp4_gated_workspace(int64_t T, int64_t H, int64_t I);
+int nvfp4_gated_forward(const uint16_t* x, const uint16_t* w13, int64_t T, int64_t H, int64_t I,
+                        uint16_t* act, uint16_t* gate_up,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_gated_backward - the gradients of nvfp4_gated_forward:
+ *
+ *   s = 1 / (1 + exp(-gate))
+ *   dgate = d_act * up * s * (1 + gate * (1 - s)),  dup = d_act * gate * s
+ *   dx    = bf16([dgate | dup] @ w13^T),  dw13 = bf16(x^T @ [dgate | dup])
+ *
+ *   d_act    (T, I) bf16, the gradient of act
+ *   x, w13   as in the forward
+ *   gate_up  (T, 2I) bf16, the forward's
+ *   dx       (T, H) bf16 out, or NULL (not computed; w13 may then be NULL)
+ *   dw13     (H, 2I) bf16 out, or NULL (not computed; x may then be NULL)
+ * dgate and dup are float32 from the saved bf16 gate | up and enter the two
+ * products rounded to bf16; the products are summed in float32 and rounded
+ * once. Sizes, alignment, overlap and determinism as in the forward. With
+ * T == 0, dw13 is zero. Both outputs NULL: NVFP4_EINVAL.
+ *
+ * Workspace: nvfp4_gated_backward_workspace(T, H, I) bytes, 256-byte aligned
+ * ([dgate | dup], and partial sums where the tiles are few); 0 for invalid
+ * sizes.
+ * ------------------------------------------------------------------------ */
+size_t nvfp4_gated_backward_workspace(int64_t T, int64_t H, int64_t I);
+int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_t* w13,
+                         const uint16_t* gate_up, int64_t T, int64_t H, int64_t I,
+                         uint16_t* dx, uint16_t* dw13,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

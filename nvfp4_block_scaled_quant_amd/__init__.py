@@ -17,6 +17,8 @@ mirror the C ABI in include/nvfp4moe.h:
                 x_gs=None, gate_up_tap=None) -> y   (w13_alpha (E,) or per half (E, 2))
     moe_forward_noalloc(...)         -> y     the same without a workspace
     route_topk(logits, topk)         -> (topk_ids, topk_weights)
+    gated_forward(x, w13)            -> act               bf16 gated feed-forward block
+    gated_backward(d_act, x, w13, gate_up) -> (dx, dw13)  its gradients
 
 The library must be built in-tree first (``python -m
 nvfp4_block_scaled_quant_amd.build``); importing this package without it
@@ -58,6 +60,10 @@ _SIGS = {
                                      _int),
     "nvfp4_moe_forward_ex": ([_vp] * 9 + [_i64] * 5 + [_vp, _vp, _sz, _vp, _vp, _vp], _int),
     "nvfp4_route_topk": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp], _int),
+    "nvfp4_gated_workspace": ([_i64, _i64, _i64], _sz),
+    "nvfp4_gated_forward": ([_vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp], _int),
+    "nvfp4_gated_backward_workspace": ([_i64, _i64, _i64], _sz),
+    "nvfp4_gated_backward": ([_vp] * 4 + [_i64] * 3 + [_vp, _vp, _vp, _sz, _vp], _int),
     "nvfp4_moe_forward_noalloc": ([_vp] * 9 + [_i64] * 5 + [_vp, _vp, _vp, _vp], _int),
 }
 
@@ -396,6 +402,80 @@ def moe_forward_noalloc(x, topk_ids, topk_weights, w13, w13_sf, w13_alpha, w2, w
         _ptr(w2), _ptr(w2_sf), _ptr(w2_alpha), T, H, I, E, topk, _ptr(y), _stream(), ev,
         ctypes.byref(opts) if opts is not None else None), "nvfp4_moe_forward_noalloc")
     return y
+
+
+def _on(device):
+    """Makes the operands' device the current one for a call (the library
+    launches on the current device) and names its current stream."""
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else _NO_GUARD
+
+
+class _NoGuard:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_NO_GUARD = _NoGuard()
+
+
+def _gated_sizes(x, w13, dev):
+    if w13.shape[0] != x.shape[1] or w13.shape[1] % 2:
+        raise ValueError(f"w13 must be (H, 2I) with H = {x.shape[1]}, got {tuple(w13.shape)}")
+    H, I = x.shape[1], w13.shape[1] // 2
+    if H % 16 or I % 16 or H == 0 or I == 0:
+        raise ValueError("gated: H and I must be positive multiples of 16")
+    return x.shape[0], H, I
+
+
+def gated_forward(x, w13, act=None, gate_up=None, workspace=None):
+    """act = silu(x @ w13[:, :I]) * (x @ w13[:, I:]) in one pass: x bf16
+    (T, H), w13 bf16 (H, 2I) = [gate | up] -> act bf16 (T, I). gate_up: None,
+    or a bf16 (T, 2I) tensor that receives the rounded gate | up values that
+    gated_backward takes."""
+    _need(x, torch.bfloat16, "x", 2)
+    dev = x.device
+    _need(w13, torch.bfloat16, "w13", 2, dev)
+    T, H, I = _gated_sizes(x, w13, dev)
+    with _on(dev):
+        act = _out(act, (T, I), torch.bfloat16, dev, "act")
+        if gate_up is not None:
+            _out(gate_up, (T, 2 * I), torch.bfloat16, dev, "gate_up")
+        ws = _workspace(workspace, _lib.nvfp4_gated_workspace(T, H, I), dev)
+        _check(_lib.nvfp4_gated_forward(_ptr(x), _ptr(w13), T, H, I, _ptr(act), _ptr(gate_up),
+                                        _ptr(ws), _nbytes(ws), _stream()), "nvfp4_gated_forward")
+    return act
+
+
+def gated_backward(d_act, x, w13, gate_up, dx=None, dw13=None, need_dx=True, need_dw13=True,
+                   workspace=None):
+    """Gradients of gated_forward: d_act bf16 (T, I), the forward's x, w13 and
+    gate_up -> (dx bf16 (T, H), dw13 bf16 (H, 2I)). need_dx / need_dw13 =
+    False skips that product and returns None in its place."""
+    _need(x, torch.bfloat16, "x", 2)
+    dev = x.device
+    _need(w13, torch.bfloat16, "w13", 2, dev)
+    T, H, I = _gated_sizes(x, w13, dev)
+    _need(d_act, torch.bfloat16, "d_act", 2, dev)
+    _need(gate_up, torch.bfloat16, "gate_up", 2, dev)
+    if d_act.shape != (T, I) or gate_up.shape != (T, 2 * I):
+        raise ValueError("gated_backward: inconsistent shapes")
+    if not (need_dx or need_dw13):
+        raise ValueError("gated_backward: nothing to compute")
+    if (dx is not None and not need_dx) or (dw13 is not None and not need_dw13):
+        raise ValueError("gated_backward: an output is given for a gradient that is not computed")
+    with _on(dev):
+        if need_dx:
+            dx = _out(dx, (T, H), torch.bfloat16, dev, "dx")
+        if need_dw13:
+            dw13 = _out(dw13, (H, 2 * I), torch.bfloat16, dev, "dw13")
+        ws = _workspace(workspace, _lib.nvfp4_gated_backward_workspace(T, H, I), dev)
+        _check(_lib.nvfp4_gated_backward(_ptr(d_act), _ptr(x), _ptr(w13), _ptr(gate_up), T, H, I,
+                                         _ptr(dx), _ptr(dw13), _ptr(ws), _nbytes(ws), _stream()),
+               "nvfp4_gated_backward")
+    return dx, dw13
 
 
 class _Hip:

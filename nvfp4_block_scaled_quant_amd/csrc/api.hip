@@ -530,4 +530,128 @@ int nvfp4_route_topk(const float* logits, int64_t T, int64_t E, int64_t topk, in
     return hip_status(launch_route_topk(logits, T, (int)E, (int)topk, topk_ids, topk_weights, stream));
 }
 
+// ---------------------------------------------------------------------------
+namespace {
+
+bool gated_shape_ok(int64_t T, int64_t H, int64_t I) {
+    if (T < 0 || H <= 0 || I <= 0 || H % 16 || I % 16) return false;
+    return T <= (int64_t)1 << 24 && H <= (int64_t)1 << 20 && I <= (int64_t)1 << 20;
+}
+
+// the three products' plans; workspace: dgu, then the backward's partial sums
+GatedPlan gated_fwd_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(T, I, kGatedBN / 2, 2 * I, H); }
+GatedPlan gated_dx_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(T, H, kGatedBN, H, 2 * I); }
+GatedPlan gated_dw_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(H, 2 * I, kGatedBN, 2 * I, T); }
+
+size_t gated_partial_bytes(const GatedPlan& g, int64_t rows, int64_t cols) {
+    return g.ksplit > 1 ? align_up((size_t)g.ksplit * (size_t)rows * (size_t)cols * 4) : 0;
+}
+
+}  // namespace
+
+size_t nvfp4_gated_workspace(int64_t T, int64_t H, int64_t I) {
+    if (!gated_shape_ok(T, H, I)) return 0;
+    const size_t n = T > 0 ? gated_partial_bytes(gated_fwd_plan(T, H, I), T, 2 * I) : 0;
+    return n ? n : kAlign;
+}
+
+int nvfp4_gated_forward(const uint16_t* x, const uint16_t* w13, int64_t T, int64_t H, int64_t I, uint16_t* act,
+                        uint16_t* gate_up, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (T < 0 || H <= 0 || I <= 0) return NVFP4_EINVAL;
+    if (!gated_shape_ok(T, H, I)) return NVFP4_ESHAPE;
+    if (T == 0) return NVFP4_OK;
+    if (!x || !w13 || !act) return NVFP4_EINVAL;
+    if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(act, 16) || !aligned(gate_up, 16)) return NVFP4_EINVAL;
+    if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < nvfp4_gated_workspace(T, H, I))
+        return NVFP4_EWORKSPACE;
+    int dv = check_device();
+    if (dv) return dv;
+    const GatedPlan plan = gated_fwd_plan(T, H, I);
+    GatedGemm p = {};
+    p.a = x;
+    p.lda = H;
+    p.b = w13;
+    p.ldb = 2 * I;
+    p.M = T;
+    p.K = H;
+    p.ncols = I;
+    p.tile_cols = kGatedBN / 2;
+    p.I = I;
+    p.out = act;
+    p.gate_up = gate_up;
+    p.ksplit = plan.ksplit;
+    p.partial = static_cast<float*>(workspace);
+    NVFP4_TRY(launch_gated(p, kGatedFwd, plan.mi, stream));
+    if (plan.ksplit > 1) NVFP4_TRY(launch_gated_reduce(p, stream));
+    return NVFP4_OK;
+}
+
+size_t nvfp4_gated_backward_workspace(int64_t T, int64_t H, int64_t I) {
+    if (!gated_shape_ok(T, H, I)) return 0;
+    if (T == 0) return kAlign;
+    return align_up((size_t)T * (size_t)I * 4) + gated_partial_bytes(gated_dx_plan(T, H, I), T, H) +
+           gated_partial_bytes(gated_dw_plan(T, H, I), H, 2 * I);
+}
+
+int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_t* w13, const uint16_t* gate_up,
+                         int64_t T, int64_t H, int64_t I, uint16_t* dx, uint16_t* dw13, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream) {
+    if (T < 0 || H <= 0 || I <= 0) return NVFP4_EINVAL;
+    if (!gated_shape_ok(T, H, I)) return NVFP4_ESHAPE;
+    if (!dx && !dw13) return NVFP4_EINVAL;
+    if (!aligned(dx, 16) || !aligned(dw13, 16)) return NVFP4_EINVAL;
+    if (T > 0) {
+        if (!d_act || !gate_up || (dx && !w13) || (dw13 && !x)) return NVFP4_EINVAL;
+        if (!aligned(d_act, 16) || !aligned(x, 16) || !aligned(w13, 16) || !aligned(gate_up, 16)) return NVFP4_EINVAL;
+        if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < nvfp4_gated_backward_workspace(T, H, I))
+            return NVFP4_EWORKSPACE;
+    } else if (!dw13) {
+        return NVFP4_OK;
+    }
+    int dv = check_device();
+    if (dv) return dv;
+    if (T == 0) {
+        NVFP4_TRY(launch_zero_bytes(dw13, H * I * 4, stream));
+        return NVFP4_OK;
+    }
+    const GatedPlan px = gated_dx_plan(T, H, I), pw = gated_dw_plan(T, H, I);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint16_t* dgu = reinterpret_cast<uint16_t*>(ws);
+    ws += align_up((size_t)T * (size_t)I * 4);
+    GatedGemm gx = {}, gw = {};
+    gx.a = dgu;
+    gx.lda = 2 * I;
+    gx.b = w13;
+    gx.ldb = 2 * I;
+    gx.M = T;
+    gx.K = 2 * I;
+    gx.ncols = H;
+    gx.tile_cols = kGatedBN;
+    gx.out = dx;
+    gx.ksplit = px.ksplit;
+    gx.partial = reinterpret_cast<float*>(ws);
+    ws += gated_partial_bytes(px, T, H);
+    gw.a = x;
+    gw.lda = H;
+    gw.b = dgu;
+    gw.ldb = 2 * I;
+    gw.M = H;
+    gw.K = T;
+    gw.ncols = 2 * I;
+    gw.tile_cols = kGatedBN;
+    gw.out = dw13;
+    gw.ksplit = pw.ksplit;
+    gw.partial = reinterpret_cast<float*>(ws);
+    NVFP4_TRY(launch_gated_dgu(d_act, gate_up, T, I, dgu, stream));
+    if (dx) {
+        NVFP4_TRY(launch_gated(gx, kGatedDx, px.mi, stream));
+        if (px.ksplit > 1) NVFP4_TRY(launch_gated_sum(gx.partial, px.ksplit, T * H, dx, stream));
+    }
+    if (dw13) {
+        NVFP4_TRY(launch_gated(gw, kGatedDw, pw.mi, stream));
+        if (pw.ksplit > 1) NVFP4_TRY(launch_gated_sum(gw.partial, pw.ksplit, H * 2 * I, dw13, stream));
+    }
+    return NVFP4_OK;
+}
+
 }  // extern "C"

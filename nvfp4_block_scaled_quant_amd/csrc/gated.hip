@@ -1,0 +1,541 @@
+// Gated feed-forward block in bf16: act = silu(x Wg) * (x Wu) with
+// w13 = [Wg | Wu] (H, 2I), and its backward pass. The dense (or shared) expert
+// beside the routed ones: its weights stay in bf16 and may be trained.
+//
+//   forward   g = x Wg, u = x Wu (float32 sums), act = bf16(g / (1 + e^-g) * u),
+//             optionally gate_up = [bf16(g) | bf16(u)] for the backward pass
+//   backward  s = 1 / (1 + e^-g);  dg = d u s (1 + g (1 - s));  du = d g s
+//             dx = [dg | du] w13^T,  dw13 = x^T [dg | du]
+//
+// All three products run through one tile routine (below) on
+// v_mfma_f32_32x32x16_bf16. The two directions a reduction can lie in are
+// handled at the LDS read: an operand whose rows are contiguous along K
+// (x in the forward; [dg | du] and w13 in dx) is staged as rows of 64 bytes and
+// read with 16-byte loads; one whose rows are contiguous along M or N (w13 in
+// the forward; both operands of dw13) is staged as K rows and read with the
+// transposing LDS load (ds_read_b64_tr_b16: 16 lanes read 4 K rows of 16
+// columns and each lane receives the 4 K values of its column). Nothing is
+// transposed in memory and no weight is repacked, which training could not
+// keep up to date for free.
+//
+// Tile. A work-group of 8 waves (two per SIMD) computes 64 MI x 256 outputs;
+// wave w owns rows 32 MI (w / 4) .. and columns 64 (w % 4) .. +64. In the
+// forward a wave's 64 columns are 32 gate columns and the matching 32 up
+// columns, so both projections of an output meet in one lane and the
+// activation and the product are its epilogue. Stages of 32 K elements move
+// from memory to LDS by buffer loads that write LDS directly; a ring of
+// stages keeps several in flight. Every load is issued with either an offset
+// inside the operand or one beyond the buffer (which reads zeros): K tails,
+// rows beyond M and columns beyond N are zeros in both operands, so nothing
+// else (a NaN beside the tile) enters a sum.
+//
+// Few tiles: K is cut into chunks that fill the GPU, each work-group writes
+// float32 partial sums, and a second kernel adds them in chunk order (the
+// result does not depend on scheduling) before the one rounding.
+#include <type_traits>
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef short short8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) short4_t lds_short4;
+
+constexpr int NT = 512;                     // 8 waves
+constexpr int KS = 32;                      // K elements per stage
+constexpr int BN = kGatedBN;                // tile columns
+constexpr int B_BYTES = BN * KS * 2;        // 16 KB
+constexpr uint32_t kRsrcWord3 = 0x00020000u;
+constexpr uint32_t kBeyond = 0x80000000u;   // an offset outside every buffer: reads zeros
+constexpr int kWaves = NT / 64;
+
+template <int MI> constexpr int kABytes = 64 * MI * KS * 2;
+template <int MI> constexpr int kStage = kABytes<MI> + B_BYTES;
+// ring depth: what 128 KB hold, in powers of two
+template <int MI> constexpr int kStages = 4;
+template <int MI> constexpr int kLds = kStages<MI> * kStage<MI>;
+
+constexpr int waitcnt_imm(int vm, int lgkm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4) | (lgkm << 8); }
+
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A buffer whose valid offsets are the ones the callers form (all below 2^31);
+// kBeyond lies outside.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, 0x7FFFFFFF, kRsrcWord3);
+}
+
+// silu(g) * u in float32. e = e^-|g| is at most 1, so neither sign overflows.
+__device__ __forceinline__ float sigmoid_f32(float g) {
+    const float e = exp_split(-__builtin_fabsf(g));
+    return (g >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
+}
+__device__ __forceinline__ float silu_mul(float g, float u) { return g * sigmoid_f32(g) * u; }
+
+// Transposing LDS load. The restrict argument gives the access alias
+// information; without any, the compiler drains every outstanding load into
+// LDS before it (the waits that order them are the main loop's own).
+__device__ __forceinline__ short4_t lds_read_tr(lds_short4* __restrict__ q) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(q);
+}
+
+// 4 x 4 transpose inside each quad of lanes: lane m of a quad gives v[r] = row
+// r of column m and receives row m of columns 0..3.
+__device__ __forceinline__ void quad_transpose(float (&v)[4], int lane) {
+    const bool odd = lane & 1, upper = lane & 2;
+    auto swap1 = [](float x) {       // quad_perm(1,0,3,2)
+        return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0xB1, 0xF, 0xF, false));
+    };
+    auto swap2 = [](float x) {       // quad_perm(2,3,0,1)
+        return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x4E, 0xF, 0xF, false));
+    };
+    const float a = swap1(odd ? v[0] : v[1]), b = swap1(odd ? v[2] : v[3]);
+    if (odd) { v[0] = a; v[2] = b; } else { v[1] = a; v[3] = b; }
+    const float c = swap2(upper ? v[0] : v[2]), d = swap2(upper ? v[1] : v[3]);
+    if (upper) { v[0] = c; v[1] = d; } else { v[2] = c; v[3] = d; }
+}
+
+// Work-group b -> tile (m, n) and K chunk. Work-groups go to the eight XCDs
+// round-robin, so XCD b % 8 gets a contiguous range of tile numbers, and tile
+// numbers run over blocks of 4 row tiles, so that an XCD's tiles share
+// operand rows in its L2.
+struct TileId { int m, n, chunk; };
+__device__ __forceinline__ TileId map_tile(int b, int total, int mt, int ntn) {
+    const int x = b & 7, q = total >> 3, rem = total & 7;
+    const int id = x * q + min(x, rem) + (b >> 3);
+    const int tiles = mt * ntn;
+    const int chunk = id / tiles, t = id - chunk * tiles;
+    constexpr int GM = 4;
+    const int g = t / (GM * ntn), r = t - g * GM * ntn;
+    const int gm = min(GM, mt - g * GM);
+    return {g * GM + r % gm, r / gm, chunk};
+}
+
+// One operand of a tile. KSTRIDED = false: `rows` rows (from base), each
+// contiguous along K, ld elements apart; true: K rows, contiguous along the
+// tile's W columns (column ranges given per 8-column chunk by `off`).
+//
+// LDS layout of a stage. K-contiguous: rows of 64 bytes, 16-byte chunk c of
+// row r stored at c ^ ((r >> 2) & 3), so the 16 rows a 16-lane group reads
+// cover all 64 banks. K-strided: 32 K rows of 2 W bytes; 16-byte chunk c of
+// row k at c ^ swz(k), so the 4 K rows x 64 bytes that 32 lanes of a
+// transposing load read cover all banks.
+template <int W> __device__ __forceinline__ int kstrided_swz(int k) {
+    return W >= 128 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
+}
+
+template <int MODE, int MI>
+__device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_t* smem) {
+    constexpr bool A_KS = MODE == kGatedDw;              // A contiguous along M
+    constexpr bool B_KS = MODE != kGatedDx;              // B contiguous along N
+    constexpr int AW = 64 * MI;                          // tile rows
+    constexpr int NS = kStages<MI>;
+    constexpr int STAGE = kStage<MI>;
+    constexpr int NA = MI == 4 ? 2 : 1, NB = 2, NL = NA + NB;   // loads per wave and stage
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ntn = (int)((p.ncols + p.tile_cols - 1) / p.tile_cols);
+    const int mt = (int)((p.M + AW - 1) / AW);
+    const TileId id = map_tile(block, mt * ntn * p.ksplit, mt, ntn);
+    const int64_t m0 = (int64_t)id.m * AW, n0 = (int64_t)id.n * p.tile_cols;
+    const int rows = (int)min((int64_t)AW, p.M - m0);
+
+    // K range of this work-group, in stages; kend bounds every load
+    const int nk_all = (int)((p.K + KS - 1) / KS);
+    const int kper = (nk_all + p.ksplit - 1) / p.ksplit;
+    const int kb = id.chunk * kper;
+    const int nk = min(nk_all, kb + kper) - kb;
+    const int kend = (int)min(p.K, (int64_t)(kb + nk) * KS);
+
+    // ---- per-lane load offsets (bytes from the stage's base) and K position ----
+    const uint16_t* abase = p.a + (A_KS ? m0 : m0 * p.lda);
+    const uint16_t* bbase = p.b + (MODE == kGatedDx ? n0 * p.ldb : MODE == kGatedDw ? n0 : 0);
+    uint32_t a_off[2], b_off[2];
+    int a_k[2], b_k[2];
+#pragma unroll
+    for (int t = 0; t < NA; ++t) {
+        // (64-row tiles have 4 KB of A: waves 4..7 load what waves 0..3 do)
+        const int u = MI == 4 ? 2 * wave + t : MI == 2 ? wave : (wave & 3);
+        if (A_KS) {
+            constexpr int CH = AW / 8;                   // chunks per K row
+            const int k = u * (64 / CH) + lane / CH, pc = lane % CH;
+            const int c = pc ^ kstrided_swz<AW>(k);
+            a_k[t] = k;
+            a_off[t] = 8 * c < rows ? (uint32_t)(k * p.lda * 2 + 16 * c) : kBeyond;
+        } else {
+            const int r = 16 * u + (lane >> 2);
+            const int c = (lane & 3) ^ ((r >> 2) & 3);
+            a_k[t] = 8 * c;
+            a_off[t] = r < rows ? (uint32_t)(r * p.lda * 2 + 16 * c) : kBeyond;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NB; ++t) {
+        const int u = 2 * wave + t;
+        if (B_KS) {
+            const int k = 2 * u + (lane >> 5), pc = lane & 31;
+            const int c = pc ^ kstrided_swz<BN>(k);
+            b_k[t] = k;
+            int64_t col;
+            bool ok;
+            if (MODE == kGatedFwd) {                     // chunk c: 4 chunks gate, 4 chunks up per wave
+                const int64_t a = n0 + 32 * (c >> 3) + 8 * (c & 3);
+                ok = a < p.I;
+                col = (c & 4) ? p.I + a : a;
+            } else {
+                col = 8 * c;
+                ok = n0 + col < p.ncols;
+            }
+            b_off[t] = ok ? (uint32_t)((k * p.ldb + col) * 2) : kBeyond;
+        } else {
+            const int r = 16 * u + (lane >> 2);
+            const int c = (lane & 3) ^ ((r >> 2) & 3);
+            b_k[t] = 8 * c;
+            b_off[t] = n0 + r < p.ncols ? (uint32_t)(r * p.ldb * 2 + 16 * c) : kBeyond;
+        }
+    }
+    const int64_t a_step = A_KS ? (int64_t)KS * p.lda : KS;       // elements per stage
+    const int64_t b_step = B_KS ? (int64_t)KS * p.ldb : KS;
+
+    auto issue = [&](int r, int st) {
+        const int k0 = (kb + r) * KS;
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(abase + (int64_t)(kb + r) * a_step);
+        const __amdgpu_buffer_rsrc_t rb = make_rsrc(bbase + (int64_t)(kb + r) * b_step);
+        uint8_t* base = smem + st * STAGE;
+#pragma unroll
+        for (int t = 0; t < NA; ++t) {
+            const int u = MI == 4 ? 2 * wave + t : MI == 2 ? wave : (wave & 3);
+            const uint32_t off = k0 + a_k[t] < kend ? a_off[t] : kBeyond;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + u * 1024), 16, off, 0, 0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < NB; ++t) {
+            const uint32_t off = k0 + b_k[t] < kend ? b_off[t] : kBeyond;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(base + kABytes<MI> + (2 * wave + t) * 1024), 16,
+                                                     off, 0, 0, 0);
+        }
+    };
+
+    // ---- fragments ---------------------------------------------------------------
+    // Lane l serves row / column l % 32 and, of a 16-element substep, K values
+    // 8 h .. 8 h + 7 with h = l / 32, in both operands.
+    const int wm = wave >> 2, wn = wave & 3;
+    const int l32 = lane & 31, h = lane >> 5;
+    const int tk = 8 * h + ((lane & 15) >> 2);                     // transposing loads: K row
+    const int tc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);      // chunk inside a 32-column block
+    uint32_t fa_off[MI], fb_off[2], fc_a, fc_b;
+    fc_a = (uint32_t)(16 * (h ^ ((l32 >> 2) & 3)));                // K-contiguous: chunk of substep 0
+    fc_b = fc_a;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+        fa_off[i] = A_KS ? (uint32_t)(tk * AW * 2 + 16 * ((4 * (wm * MI + i) + tc) ^ kstrided_swz<AW>(tk)) + 8 * (lane & 1))
+                         : (uint32_t)((wm * 32 * MI + 32 * i + l32) * 64);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        fb_off[j] = kABytes<MI> +
+                    (B_KS ? (uint32_t)(tk * BN * 2 + 16 * ((4 * (wn * 2 + j) + tc) ^ kstrided_swz<BN>(tk)) + 8 * (lane & 1))
+                          : (uint32_t)((wn * 64 + 32 * j + l32) * 64));
+
+    auto read_tr = [&](uint32_t off, int ldw, int s) -> bf16x8_t {
+        const uint8_t* q = smem + off + s * 16 * ldw;
+        const short4_t lo = lds_read_tr((lds_short4*)q);
+        const short4_t hi = lds_read_tr((lds_short4*)(q + 4 * ldw));
+        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    auto read_row = [&](uint32_t off, uint32_t fc, int s) -> bf16x8_t {
+        return *reinterpret_cast<const bf16x8_t*>(smem + off + (fc ^ (uint32_t)(32 * s)));
+    };
+    bf16x8_t fa[2][MI], fb[2][2];
+    auto read = [&](int st, int s, int d) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            fa[d][i] = A_KS ? read_tr(st * STAGE + fa_off[i], AW * 2, s) : read_row(st * STAGE + fa_off[i], fc_a, s);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            fb[d][j] = B_KS ? read_tr(st * STAGE + fb_off[j], BN * 2, s) : read_row(st * STAGE + fb_off[j], fc_b, s);
+    };
+
+    float16_t acc[MI][2];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    auto mfma = [&](int d) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[d][i], fb[d][j], acc[i][j], 0, 0, 0);
+    };
+
+    // ---- main loop ------------------------------------------------------------------
+    // Step r: substep 0's fragments are in registers. Substep 1's are read
+    // under substep 0's MFMAs; then this wave's loads of stage r + 1 are
+    // waited for (those of the NS - 2 later stages stay in flight), the
+    // barrier makes everyone's visible and says that everyone has read stage
+    // r, whose buffer stage r + NS refills. Loads past the last stage read
+    // zeros, so the count of outstanding loads is the same in every step.
+#pragma unroll
+    for (int s = 0; s < NS; ++s) issue(s, s);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 1) * NL, 0));
+    lds_barrier();
+    read(0, 0, 0);
+    auto step = [&](int r, int st) {
+        read(st, 1, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        mfma(0);
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 2) * NL, 0));
+        lds_barrier();
+        issue(r + NS, st);
+        read(st + 1 == NS ? 0 : st + 1, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        mfma(1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    int r = 0;
+    for (; r + NS <= nk; r += NS) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) step(r + s, s);
+    }
+    for (int s = 0; r + s < nk; ++s) step(r + s, s);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));      // no load into LDS outlives the work-group
+
+    // ---- epilogue -------------------------------------------------------------------
+    // acc[i][j][r] = D[row 32 i + 8 (r / 4) + 4 h + r % 4][column 32 j + l32] of
+    // the wave's part; after a transpose inside each quad of lanes, lane 4 c +
+    // m holds columns 4 c .. 4 c + 3 of row m of each group of four rows
+    const int m4 = lane & 3, c4 = l32 & ~3;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int local = wm * 32 * MI + 32 * i + 8 * g + 4 * h + m4;
+            const int64_t row = m0 + local;
+            float v[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[j][k] = acc[i][j][4 * g + k];
+                quad_transpose(v[j], lane);
+            }
+            if (MODE == kGatedFwd) {
+                const int64_t col = n0 + wn * 32 + c4;       // I % 16 == 0: four columns are in or out together
+                if (local >= rows || col >= p.I) continue;
+                if (p.ksplit > 1) {
+                    float* dst = p.partial + ((int64_t)id.chunk * p.M + row) * 2 * p.I + col;
+                    *reinterpret_cast<float4_t*>(dst) = (float4_t){v[0][0], v[0][1], v[0][2], v[0][3]};
+                    *reinterpret_cast<float4_t*>(dst + p.I) = (float4_t){v[1][0], v[1][1], v[1][2], v[1][3]};
+                    continue;
+                }
+                float a[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) a[k] = silu_mul(v[0][k], v[1][k]);
+                *reinterpret_cast<u32x2*>(p.out + row * p.I + col) =
+                    (u32x2){pack_bf16x2_rne(a[0], a[1]), pack_bf16x2_rne(a[2], a[3])};
+                if (p.gate_up) {
+                    uint16_t* gu = p.gate_up + row * 2 * p.I + col;
+                    *reinterpret_cast<u32x2*>(gu) =
+                        (u32x2){pack_bf16x2_rne(v[0][0], v[0][1]), pack_bf16x2_rne(v[0][2], v[0][3])};
+                    *reinterpret_cast<u32x2*>(gu + p.I) =
+                        (u32x2){pack_bf16x2_rne(v[1][0], v[1][1]), pack_bf16x2_rne(v[1][2], v[1][3])};
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t col = n0 + wn * 64 + 32 * j + c4;
+                    if (local >= rows || col >= p.ncols) continue;
+                    if (p.ksplit > 1)
+                        *reinterpret_cast<float4_t*>(p.partial + ((int64_t)id.chunk * p.M + row) * p.ncols + col) =
+                            (float4_t){v[j][0], v[j][1], v[j][2], v[j][3]};
+                    else
+                        *reinterpret_cast<u32x2*>(p.out + row * p.ncols + col) =
+                            (u32x2){pack_bf16x2_rne(v[j][0], v[j][1]), pack_bf16x2_rne(v[j][2], v[j][3])};
+                }
+            }
+        }
+    }
+}
+
+template <int MODE, int MI>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void gated_kernel(GatedGemm p) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    gated_tile<MODE, MI>(p, blockIdx.x, smem);
+}
+
+// Partial sums of the forward, in chunk order, then the epilogue of the tile
+// routine. One thread per 4 columns.
+__global__ __launch_bounds__(256) void gated_reduce_kernel(GatedGemm p) {
+    const int64_t I4 = p.I / 4, n = p.M * I4, plane = p.M * 2 * p.I;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
+        const int64_t row = t / I4, col = 4 * (t - row * I4);
+        const float* src = p.partial + row * 2 * p.I + col;
+        float4_t g = *reinterpret_cast<const float4_t*>(src), u = *reinterpret_cast<const float4_t*>(src + p.I);
+#pragma unroll 8
+        for (int c = 1; c < p.ksplit; ++c) {
+            g += *reinterpret_cast<const float4_t*>(src + c * plane);
+            u += *reinterpret_cast<const float4_t*>(src + c * plane + p.I);
+        }
+        float a[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[k] = silu_mul(g[k], u[k]);
+        *reinterpret_cast<u32x2*>(p.out + row * p.I + col) =
+            (u32x2){pack_bf16x2_rne(a[0], a[1]), pack_bf16x2_rne(a[2], a[3])};
+        if (p.gate_up) {
+            uint16_t* gu = p.gate_up + row * 2 * p.I + col;
+            *reinterpret_cast<u32x2*>(gu) = (u32x2){pack_bf16x2_rne(g[0], g[1]), pack_bf16x2_rne(g[2], g[3])};
+            *reinterpret_cast<u32x2*>(gu + p.I) = (u32x2){pack_bf16x2_rne(u[0], u[1]), pack_bf16x2_rne(u[2], u[3])};
+        }
+    }
+}
+
+// out = bf16(sum of the chunks' partial sums, in chunk order), 4 columns a thread.
+__global__ __launch_bounds__(256) void gated_sum_kernel(const float* __restrict__ partial, int ksplit, int64_t n4,
+                                                        uint16_t* __restrict__ out) {
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n4; t += (int64_t)gridDim.x * 256) {
+        const float4_t* src = reinterpret_cast<const float4_t*>(partial) + t;
+        float4_t v = src[0];
+#pragma unroll 8
+        for (int c = 1; c < ksplit; ++c) v += src[c * n4];
+        *reinterpret_cast<u32x2*>(out + 4 * t) = (u32x2){pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
+    }
+}
+
+// [dg | du] from the saved bf16 gate | up and d_act. It is rounded to bf16,
+// the matrix cores' operand type: independent relative errors of at most 2^-9
+// per element, which a sum over them carries as one such error, the size of
+// the outputs' own rounding. 8 columns a thread: 3 reads and 2 writes of 16
+// bytes, nothing to reuse, bound by memory.
+__global__ __launch_bounds__(256) void gated_dgu_kernel(const uint16_t* __restrict__ d_act,
+                                                        const uint16_t* __restrict__ gate_up, int64_t T, int64_t I,
+                                                        uint16_t* __restrict__ dgu) {
+    const int64_t I8 = I / 8, n = T * I8;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
+        const int64_t row = t / I8, col = 8 * (t - row * I8);
+        const u32x4 d = *reinterpret_cast<const u32x4*>(d_act + row * I + col);
+        const u32x4 g = *reinterpret_cast<const u32x4*>(gate_up + row * 2 * I + col);
+        const u32x4 u = *reinterpret_cast<const u32x4*>(gate_up + row * 2 * I + I + col);
+        u32x4 og, ou;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float dg[2], du[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const float dv = bf16_to_f32((d[k] >> (16 * b)) & 0xFFFFu), gv = bf16_to_f32((g[k] >> (16 * b)) & 0xFFFFu);
+                const float uv = bf16_to_f32((u[k] >> (16 * b)) & 0xFFFFu);
+                // 1 - s = sigmoid(-g): formed without cancellation
+                const float e = exp_split(-__builtin_fabsf(gv)), q = __builtin_amdgcn_rcpf(1.0f + e);
+                const float s = gv >= 0.0f ? q : e * q, s1 = gv >= 0.0f ? e * q : q;
+                du[b] = dv * (gv * s);
+                dg[b] = dv * uv * (s * (1.0f + gv * s1));
+            }
+            og[k] = pack_bf16x2_rne(dg[0], dg[1]);
+            ou[k] = pack_bf16x2_rne(du[0], du[1]);
+        }
+        *reinterpret_cast<u32x4*>(dgu + row * 2 * I + col) = og;
+        *reinterpret_cast<u32x4*>(dgu + row * 2 * I + I + col) = ou;
+    }
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(u32x4* p, int64_t n) {
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256)
+        p[t] = (u32x4){0u, 0u, 0u, 0u};
+}
+
+unsigned grid_for(int64_t n) {
+    const int64_t g = (n + 255) / 256;
+    return (unsigned)(g < 1 ? 1 : g < 2048 ? g : 2048);
+}
+
+template <int MODE, int MI>
+hipError_t launch_tiles(const GatedGemm& p, hipStream_t s) {
+    const int64_t grid = (p.M + 64 * MI - 1) / (64 * MI) * ((p.ncols + p.tile_cols - 1) / p.tile_cols) * p.ksplit;
+    static std::atomic<int> lds_set[kMaxDevices];
+    hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&gated_kernel<MODE, MI>), kLds<MI>, lds_set);
+    if (e != hipSuccess) return e;
+    gated_kernel<MODE, MI><<<(unsigned)grid, NT, kLds<MI>, s>>>(p);
+    return hipGetLastError();
+}
+
+template <int MODE>
+hipError_t launch_mode(const GatedGemm& p, int mi, hipStream_t s) {
+    switch (mi) {
+        case 1: return launch_tiles<MODE, 1>(p, s);
+        case 2: return launch_tiles<MODE, 2>(p, s);
+        default: return launch_tiles<MODE, 4>(p, s);
+    }
+}
+
+}  // namespace
+
+// Tile height and K chunks of a product M x cols x K (cols / tile_cols column
+// tiles): the pair with the smallest estimate of rounds x stages of one
+// work-group, plus the partial sums' traffic.
+GatedPlan gated_plan(int64_t M, int64_t ncols, int64_t tile_cols, int64_t outcols, int64_t K) {
+    const int64_t nk = (K + KS - 1) / KS, ntn = (ncols + tile_cols - 1) / tile_cols;
+    GatedPlan best = {4, 1};
+    double best_t = 1e30;
+    for (int mi = 4; mi >= 1; mi /= 2) {
+        const int64_t tiles = (M + 64 * mi - 1) / (64 * mi) * ntn;
+        // microseconds of one stage of a tile (matrix cores, or its loads)
+        const double stage = mi == 4 ? 0.60 : mi == 2 ? 0.34 : 0.25;
+        for (int64_t ks = 1; ks <= 32 && ks <= nk; ++ks) {
+            const int64_t per = (nk + ks - 1) / ks;
+            if ((nk + per - 1) / per != ks) continue;        // no empty chunk
+            if (ks > 1 && tiles * ks > 512) break;
+            const int64_t rounds = (tiles * ks + 255) / 256;
+            double t = rounds * (per * stage + 3.0);
+            if (ks > 1) t += 3.0 + (double)ks * M * outcols * 4 * 2 / 4e6;
+            if (t < best_t) {
+                best_t = t;
+                best = {mi, (int)ks};
+            }
+        }
+    }
+    return best;
+}
+
+hipError_t launch_gated(const GatedGemm& p, int mode, int mi, hipStream_t s) {
+    switch (mode) {
+        case kGatedFwd: return launch_mode<kGatedFwd>(p, mi, s);
+        case kGatedDx: return launch_mode<kGatedDx>(p, mi, s);
+        default: return launch_mode<kGatedDw>(p, mi, s);
+    }
+}
+
+hipError_t launch_gated_reduce(const GatedGemm& p, hipStream_t s) {
+    gated_reduce_kernel<<<grid_for(p.M * p.I / 4), 256, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_gated_sum(const float* partial, int ksplit, int64_t n, uint16_t* out, hipStream_t s) {
+    gated_sum_kernel<<<grid_for(n / 4), 256, 0, s>>>(partial, ksplit, n / 4, out);
+    return hipGetLastError();
+}
+
+hipError_t launch_gated_dgu(const uint16_t* d_act, const uint16_t* gate_up, int64_t T, int64_t I, uint16_t* dgu,
+                            hipStream_t s) {
+    gated_dgu_kernel<<<grid_for(T * I / 8), 256, 0, s>>>(d_act, gate_up, T, I, dgu);
+    return hipGetLastError();
+}
+
+hipError_t launch_zero_bytes(void* p, int64_t bytes, hipStream_t s) {
+    zero_kernel<<<grid_for(bytes / 16), 256, 0, s>>>(static_cast<u32x4*>(p), bytes / 16);
+    return hipGetLastError();
+}
+
+}  // namespace nvfp4

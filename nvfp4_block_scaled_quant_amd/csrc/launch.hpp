@@ -245,4 +245,35 @@ __host__ __device__ inline int64_t skinny_lds_bytes(int64_t K) {
 }
 hipError_t launch_skinny(const GemmParams& p, hipStream_t s);
 
+// Gated feed-forward block in bf16 (gated.hip). One product C = A B of a tile
+// routine: M rows, `ncols` columns in tiles of tile_cols, reduction length K.
+//   kGatedFwd  A = x (T, H), B = w13 (H, 2I): M = T, K = H, ncols = I act
+//              columns (tile_cols = 128: as many gate as up columns a tile)
+//   kGatedDx   A = dgu (T, 2I), B = w13 (H, 2I): M = T, K = 2I, ncols = H
+//   kGatedDw   A = x (T, H), B = dgu (T, 2I): M = H, K = T, ncols = 2I
+enum GatedMode { kGatedFwd = 0, kGatedDx = 1, kGatedDw = 2 };
+constexpr int kGatedBN = 256;
+struct GatedGemm {
+    const uint16_t* a;
+    const uint16_t* b;
+    int64_t lda, ldb;
+    int64_t M, K, ncols, tile_cols, I;
+    uint16_t* out;             // act (T, I), dx (T, H) or dw13 (H, 2I)
+    uint16_t* gate_up;         // forward: null, or (T, 2I)
+    int ksplit;                // > 1: chunk c writes partial[c] instead (rows as
+    float* partial;            // out's; forward: (T, 2I))
+};
+struct GatedPlan { int mi, ksplit; };   // tiles of 64 mi rows, K chunks
+GatedPlan gated_plan(int64_t M, int64_t ncols, int64_t tile_cols, int64_t outcols, int64_t K);
+hipError_t launch_gated(const GatedGemm& p, int mode, int mi, hipStream_t s);
+// forward with ksplit > 1: sums, activation and stores
+hipError_t launch_gated_reduce(const GatedGemm& p, hipStream_t s);
+// out = bf16(sum over chunks of partial[c][0 .. n)), n % 4 == 0
+hipError_t launch_gated_sum(const float* partial, int ksplit, int64_t n, uint16_t* out, hipStream_t s);
+// gradients of gate | up (T, 2I), bf16
+hipError_t launch_gated_dgu(const uint16_t* d_act, const uint16_t* gate_up, int64_t T, int64_t I, uint16_t* dgu,
+                            hipStream_t s);
+// zero `bytes` bytes (a multiple of 16, 16-byte aligned)
+hipError_t launch_zero_bytes(void* p, int64_t bytes, hipStream_t s);
+
 }  // namespace nvfp4
