@@ -208,23 +208,29 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
     const int64_t a_step = A_KS ? (int64_t)KS * p.lda : KS;       // elements per stage
     const int64_t b_step = B_KS ? (int64_t)KS * p.ldb : KS;
 
-    auto issue = [&](int r, int st) {
-        const int k0 = (kb + r) * KS;
-        const __amdgpu_buffer_rsrc_t ra = make_rsrc(abase + (int64_t)(kb + r) * a_step);
-        const __amdgpu_buffer_rsrc_t rb = make_rsrc(bbase + (int64_t)(kb + r) * b_step);
+    // running state of the refills: the next stage's bases and how many K
+    // elements are left from there
+    const uint16_t* pa = abase + (int64_t)kb * a_step;
+    const uint16_t* pb = bbase + (int64_t)kb * b_step;
+    int left = kend - kb * KS;
+    auto issue = [&](int st) {
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(pa), rb = make_rsrc(pb);
         uint8_t* base = smem + st * STAGE;
 #pragma unroll
         for (int t = 0; t < NA; ++t) {
             const int u = MI == 4 ? 2 * wave + t : MI == 2 ? wave : (wave & 3);
-            const uint32_t off = k0 + a_k[t] < kend ? a_off[t] : kBeyond;
+            const uint32_t off = a_k[t] < left ? a_off[t] : kBeyond;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + u * 1024), 16, off, 0, 0, 0);
         }
 #pragma unroll
         for (int t = 0; t < NB; ++t) {
-            const uint32_t off = k0 + b_k[t] < kend ? b_off[t] : kBeyond;
+            const uint32_t off = b_k[t] < left ? b_off[t] : kBeyond;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(base + kABytes<MI> + (2 * wave + t) * 1024), 16,
                                                      off, 0, 0, 0);
         }
+        pa += a_step;
+        pb += b_step;
+        left -= KS;
     };
 
     // ---- fragments ---------------------------------------------------------------
@@ -259,11 +265,11 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
     bf16x8_t fa[2][MI], fb[2][2];
     auto read = [&](int st, int s, int d) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
-            fa[d][i] = A_KS ? read_tr(st * STAGE + fa_off[i], AW * 2, s) : read_row(st * STAGE + fa_off[i], fc_a, s);
-#pragma unroll
         for (int j = 0; j < 2; ++j)
             fb[d][j] = B_KS ? read_tr(st * STAGE + fb_off[j], BN * 2, s) : read_row(st * STAGE + fb_off[j], fc_b, s);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            fa[d][i] = A_KS ? read_tr(st * STAGE + fa_off[i], AW * 2, s) : read_row(st * STAGE + fa_off[i], fc_a, s);
     };
 
     float16_t acc[MI][2];
@@ -289,29 +295,45 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
     // r, whose buffer stage r + NS refills. Loads past the last stage read
     // zeros, so the count of outstanding loads is the same in every step.
 #pragma unroll
-    for (int s = 0; s < NS; ++s) issue(s, s);
+    for (int s = 0; s < NS; ++s) issue(s);
     __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 1) * NL, 0));
     lds_barrier();
     read(0, 0, 0);
-    auto step = [&](int r, int st) {
+    // LDS reads of one substep, spread over its first MFMAs (one instruction
+    // group each), so that the matrix core starts at once and the reads land
+    // under the rest
+    constexpr int NR = (A_KS ? 2 : 1) * MI + (B_KS ? 2 : 1) * 2;
+    constexpr int NM = 2 * MI;                                   // MFMAs of a substep
+    constexpr int SPREAD = NM > 2 ? NM - 2 : 1;
+    constexpr int PER = (NR + SPREAD - 1) / SPREAD;
+    auto step = [&](int st) {
         read(st, 1, 1);
-        __builtin_amdgcn_sched_barrier(0);
         mfma(0);
+#pragma unroll
+        for (int k = 0; k < NM; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);       // one MFMA
+            __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);     // its share of the LDS reads
+        }
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 2) * NL, 0));
         lds_barrier();
-        issue(r + NS, st);
         read(st + 1 == NS ? 0 : st + 1, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
+        issue(st);
         mfma(1);
+#pragma unroll
+        for (int k = 0; k < NM; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);       // one load into LDS
+        }
         __builtin_amdgcn_sched_barrier(0);
     };
     int r = 0;
     for (; r + NS <= nk; r += NS) {
 #pragma unroll
-        for (int s = 0; s < NS; ++s) step(r + s, s);
+        for (int s = 0; s < NS; ++s) step(s);
     }
-    for (int s = 0; r + s < nk; ++s) step(r + s, s);
+    for (int s = 0; r + s < nk; ++s) step(s);
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));      // no load into LDS outlives the work-group
 
     // ---- epilogue -------------------------------------------------------------------
