@@ -421,6 +421,47 @@ int nvfp4_route_topk(const float* logits, int64_t T, int64_t E, int64_t topk,
                      int32_t* topk_ids, float* topk_weights, hipStream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * nvfp4_gemm_lora - nvfp4_gemm with the low-rank adapters of many requests
+ * added to its rows (one shared projection, each row with the adapter of its
+ * request):
+ *
+ *   out[m][n] = bf16( (a_gs[0] * b_alpha[0]) * sum_k deqA[m][k] * deqB[k][n]
+ *                     + scale[a] * sum_{r < rank[a]} (sum_k x[m][k] lora_a[a][r][k])
+ *                                                    * lora_b[a][n][r] )
+ *   with a = adapter_ids[m]; rows whose id is outside [0, L) get the first
+ *   term alone. One rounding; the sums are float32, and the shrunk row
+ *   scale * x A^T enters the second product as the sum of two bf16 values
+ *   (2^-17 relative).
+ *
+ *   aq, asf, a_gs, bq, bsf, b_alpha, M, N, K, out   as nvfp4_gemm
+ *   x            (M, K) bf16, what aq was quantized from
+ *   lora_a       (L, R, K) bf16, lora_b (L, N, R) bf16 (the usual down and up
+ *                matrices of each adapter)
+ *   lora_scale   (L) float32
+ *   lora_rank    (L) int32, or NULL: every adapter has rank R. Adapter a is its
+ *                first rank[a] ranks (values outside [0, R] are taken as the
+ *                nearest); what is stored beyond them is not used.
+ *   adapter_ids  (M) int32
+ *   x, lora_a, lora_b 16-byte aligned; R % 8 == 0, 8 <= R <= 256, 1 <= L <=
+ *   65535, M <= 2^22, K % 16 == 0, N % 16 == 0 and nvfp4_gemm's limits, else
+ *   NVFP4_ESHAPE.
+ * A row depends on its own x, aq and adapter and on no other: NaN in one
+ * request's row or adapter stays in that request's rows. Deterministic: the
+ * order of every sum depends on the sizes alone, not on the ids.
+ *
+ * Workspace: nvfp4_gemm_lora_workspace(M, N, K, L, R) bytes, 256-byte
+ * aligned (nvfp4_gemm's, and the shrunk rows); 0 for invalid sizes. M == 0
+ * enqueues nothing.
+ * ------------------------------------------------------------------------ */
+size_t nvfp4_gemm_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
+int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs,
+                    const uint8_t* bq, const uint8_t* bsf, const float* b_alpha,
+                    const uint16_t* x, const uint16_t* lora_a, const uint16_t* lora_b,
+                    const float* lora_scale, const int32_t* lora_rank, const int32_t* adapter_ids,
+                    int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, uint16_t* out,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * nvfp4_gated_forward - a gated feed-forward block in bf16: both projections,
  * the activation and the product (the dense or shared expert beside the
  * routed ones; its weights are not quantized and may be trained):

@@ -17,6 +17,8 @@ mirror the C ABI in include/nvfp4moe.h:
                 x_gs=None, gate_up_tap=None) -> y   (w13_alpha (E,) or per half (E, 2))
     moe_forward_noalloc(...)         -> y     the same without a workspace
     route_topk(logits, topk)         -> (topk_ids, topk_weights)
+    gemm_lora(aq, asf, a_gs, bq_t, bsf_t, b_alpha, x, lora_a, lora_b, lora_scale,
+              adapter_ids)           -> out (bf16)        gemm + per-row adapters
     gated_forward(x, w13)            -> act               bf16 gated feed-forward block
     gated_backward(d_act, x, w13, gate_up) -> (dx, dw13)  its gradients
 
@@ -60,6 +62,8 @@ _SIGS = {
                                      _int),
     "nvfp4_moe_forward_ex": ([_vp] * 9 + [_i64] * 5 + [_vp, _vp, _sz, _vp, _vp, _vp], _int),
     "nvfp4_route_topk": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp], _int),
+    "nvfp4_gemm_lora_workspace": ([_i64] * 5, _sz),
+    "nvfp4_gemm_lora": ([_vp] * 12 + [_i64] * 5 + [_vp, _vp, _sz, _vp], _int),
     "nvfp4_gated_workspace": ([_i64, _i64, _i64], _sz),
     "nvfp4_gated_forward": ([_vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp], _int),
     "nvfp4_gated_backward_workspace": ([_i64, _i64, _i64], _sz),
@@ -419,6 +423,52 @@ class _NoGuard:
 
 
 _NO_GUARD = _NoGuard()
+
+
+def gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, adapter_ids,
+              lora_rank=None, out=None, workspace=None):
+    """gemm with the low-rank adapter of each row's request added before the
+    one rounding: out[m] += lora_scale[a] * (x[m] @ lora_a[a].T) @ lora_b[a].T
+    with a = adapter_ids[m] (int32; rows with an id outside [0, L) have none).
+    x: the bf16 (M, K) activation that aq was quantized from; lora_a bf16
+    (L, R, K), lora_b bf16 (L, N, R), R a multiple of 8 up to 256; lora_scale
+    float32 (L,); lora_rank: None, or int32 (L,): adapter a uses its first
+    lora_rank[a] ranks."""
+    _need(x, torch.bfloat16, "x", 2)
+    dev = x.device
+    for t, n, d, nd in ((aq, "aq", torch.uint8, 2), (asf, "asf", torch.uint8, 2),
+                        (bq, "bq", torch.uint8, 4), (bsf, "bsf", torch.uint8, 4),
+                        (a_gs, "a_gs", torch.float32, None), (b_alpha, "b_alpha", torch.float32, None),
+                        (lora_a, "lora_a", torch.bfloat16, 3), (lora_b, "lora_b", torch.bfloat16, 3),
+                        (lora_scale, "lora_scale", torch.float32, 1),
+                        (adapter_ids, "adapter_ids", torch.int32, 1)):
+        _need(t, d, n, nd, dev)
+    if a_gs.numel() < 1 or b_alpha.numel() < 1:
+        raise ValueError("gemm_lora: a_gs and b_alpha must hold one float32 each")
+    M, K = x.shape
+    N = bq.shape[0] * 16
+    L, R = lora_a.shape[0], lora_a.shape[1]
+    if K % 16 or K == 0 or N == 0:
+        raise ValueError("gemm_lora: K must be a positive multiple of 16 and N positive")
+    if R % 8 or not 8 <= R <= 256 or L < 1:
+        raise ValueError("gemm_lora: R must be a multiple of 8 from 8 to 256, and L at least 1")
+    shq, shs = packed_shapes(1, K, N)
+    if (aq.shape != (M, K // 2) or asf.shape != (M, K // 16) or tuple(bq.shape) != shq[1:]
+            or tuple(bsf.shape) != shs[1:] or lora_a.shape != (L, R, K) or lora_b.shape != (L, N, R)
+            or lora_scale.shape != (L,) or adapter_ids.shape != (M,)):
+        raise ValueError("gemm_lora: operand shapes do not match")
+    if lora_rank is not None:
+        _need(lora_rank, torch.int32, "lora_rank", 1, dev)
+        if lora_rank.shape != (L,):
+            raise ValueError("gemm_lora: lora_rank must have shape (L,)")
+    with _on(dev):
+        out = _out(out, (M, N), torch.bfloat16, dev, "out")
+        ws = _workspace(workspace, _lib.nvfp4_gemm_lora_workspace(M, N, K, L, R), dev)
+        _check(_lib.nvfp4_gemm_lora(
+            _ptr(aq), _ptr(asf), _ptr(a_gs), _ptr(bq), _ptr(bsf), _ptr(b_alpha), _ptr(x), _ptr(lora_a),
+            _ptr(lora_b), _ptr(lora_scale), _ptr(lora_rank), _ptr(adapter_ids), M, N, K, L, R, _ptr(out),
+            _ptr(ws), _nbytes(ws), _stream()), "nvfp4_gemm_lora")
+    return out
 
 
 def _gated_sizes(x, w13, dev):

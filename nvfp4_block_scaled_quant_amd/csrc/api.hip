@@ -533,6 +533,67 @@ int nvfp4_route_topk(const float* logits, int64_t T, int64_t E, int64_t topk, in
 // ---------------------------------------------------------------------------
 namespace {
 
+bool lora_shape_ok(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+    if (M < 0 || N <= 0 || K <= 0 || L <= 0 || R <= 0 || K % 16 || N % 16 || R % 8) return false;
+    if (R > kLoraMaxRank || L > 65535 || M > (int64_t)1 << 22) return false;
+    return M * pitch_h(K) < 0x7FFFFFFF && N * pitch_q(K) < 0x7FFFFFFF;
+}
+
+}  // namespace
+
+// nvfp4_gemm's workspace, then the partial sums of the shrunk rows
+size_t nvfp4_gemm_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+    if (!lora_shape_ok(M, N, K, L, R)) return 0;
+    return align_up(nvfp4_gemm_workspace(M, N, K)) + (size_t)lora_planes(M > 0 ? M : 1, K, L, R) * (size_t)M * (size_t)R * 4;
+}
+
+int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, const uint8_t* bq, const uint8_t* bsf,
+                    const float* b_alpha, const uint16_t* x, const uint16_t* lora_a, const uint16_t* lora_b,
+                    const float* lora_scale, const int32_t* lora_rank, const int32_t* adapter_ids, int64_t M,
+                    int64_t N, int64_t K, int64_t L, int64_t R, uint16_t* out, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+    if (M < 0 || N <= 0 || K <= 0 || L <= 0 || R <= 0) return NVFP4_EINVAL;
+    if (!lora_shape_ok(M, N, K, L, R)) return NVFP4_ESHAPE;
+    if (M == 0) return NVFP4_OK;
+    if (!aq || !asf || !a_gs || !bq || !bsf || !b_alpha || !out || !x || !lora_a || !lora_b || !lora_scale ||
+        !adapter_ids)
+        return NVFP4_EINVAL;
+    if (!aligned(aq, 8) || !aligned(bq, 16) || !aligned(bsf, 8) || !aligned(out, 8) || !aligned(a_gs, 4) ||
+        !aligned(b_alpha, 4) || !aligned(x, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) ||
+        !aligned(lora_scale, 4) || !aligned(lora_rank, 4) || !aligned(adapter_ids, 4))
+        return NVFP4_EINVAL;
+    if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < nvfp4_gemm_lora_workspace(M, N, K, L, R))
+        return NVFP4_EWORKSPACE;
+    int dv = check_device();
+    if (dv) return dv;
+    uint16_t* ah = static_cast<uint16_t*>(workspace);
+    float* v = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up(nvfp4_gemm_workspace(M, N, K)));
+    const int planes = lora_planes(M, K, L, R);
+    NVFP4_TRY(launch_dequant_rows_f16(aq, asf, M, K, ah, stream));
+    NVFP4_TRY(launch_lora_shrink(x, lora_a, lora_scale, adapter_ids, lora_rank, M, K, L, R, planes, v, stream));
+    GemmParams p = {};
+    p.mode = kGemmLora;
+    p.ah = ah;
+    p.M = M;
+    p.a_rows = M;
+    p.bq = bq;
+    p.bsf = bsf;
+    p.N = N;
+    p.K = K;
+    p.a_gs = a_gs;
+    p.b_alpha = b_alpha;
+    p.out_bf16 = out;
+    p.ksplit = dense_ksplit(M, N, K);
+    p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + gemm_ws_partial_offset(M, K));
+    p.lora = {v, planes, lora_b, adapter_ids, lora_rank, (int)L, (int)R};
+    NVFP4_TRY(launch_gemm(p, stream));
+    if (p.ksplit > 1) NVFP4_TRY(launch_splitk_reduce(p.partial, p.ksplit, M, N, nullptr, nullptr, out, stream));
+    return NVFP4_OK;
+}
+
+// ---------------------------------------------------------------------------
+namespace {
+
 bool gated_shape_ok(int64_t T, int64_t H, int64_t I) {
     if (T < 0 || H <= 0 || I <= 0 || H % 16 || I % 16) return false;
     return T <= (int64_t)1 << 24 && H <= (int64_t)1 << 20 && I <= (int64_t)1 << 20;

@@ -111,6 +111,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, in
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, kRsrcWord3);
 }
 
+// one GEMM over plain rows (not a list of expert tiles)
+template <int MODE> constexpr bool kDense = MODE == kGemmDense || MODE == kGemmLora;
+
 template <int MODE>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void gemm_kernel(GemmParams p) {
@@ -128,7 +131,7 @@ void gemm_kernel(GemmParams p) {
     // steps into its own partial sums): the dense shapes have few tiles, which
     // the XCD order would put on one XCD.
     int tile_idx, nt, chunk = 0;
-    if (MODE == kGemmDense) {
+    if (kDense<MODE>) {
         const int mt = (int)((p.M + dense_tile_rows(p.M, N) - 1) / dense_tile_rows(p.M, N));
         tile_idx = blockIdx.x % mt;
         const int rest = blockIdx.x / mt;
@@ -142,7 +145,7 @@ void gemm_kernel(GemmParams p) {
     }
 
     int expert, row_start, row_count;
-    if (MODE == kGemmDense) {
+    if (kDense<MODE>) {
         expert = 0;
         const int dbm = (int)dense_tile_rows(p.M, N);
         row_start = tile_idx * dbm;
@@ -226,7 +229,7 @@ void gemm_kernel(GemmParams p) {
         // 64-element steps: all of K, or this work-group's chunk [kb, kb + nk)
         // (dense_ksplit makes every chunk non-empty)
         const int nk_all = (int)(ldq / 32);
-        const bool split = MODE == kGemmDense && p.ksplit > 1;
+        const bool split = kDense<MODE> && p.ksplit > 1;
         const int kper = split ? (nk_all + p.ksplit - 1) / p.ksplit : nk_all;
         const int kb = split ? chunk * kper : 0;
         const int nk = split ? min(nk_all, kb + kper) - kb : nk_all;
@@ -580,6 +583,107 @@ void gemm_kernel(GemmParams p) {
             }
         } else if (MODE == kGemmL2) {
             store_f32(p.out_f32, alpha);
+        } else if (MODE == kGemmLora) {
+            // The adapters, on the matrix cores, into the same accumulators:
+            // delta = v B_a^T per 32-row block and adapter that occurs in it,
+            // added to the rows that have the adapter (the others' results
+            // are dropped by a select, not multiplied by zero: a NaN of one
+            // adapter reaches no other row). v is float32 and enters as the
+            // sum of two bf16 values (2^-17 relative), B_a is bf16. K chunk c
+            // takes the partial sums c, c + ksplit, ... of v, so that the
+            // chunks share this work too.
+            typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+            const LoraParams& lo = p.lora;
+            const int ks = p.ksplit > 1 ? p.ksplit : 1;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][j][r] *= alpha;
+                const int local = wm * (32 * MI) + 32 * i + l32;
+                const int64_t row = (int64_t)row_start + local;
+                int id = local < row_count ? lo.ids[row] : -1;
+                if (id >= lo.L) id = -1;
+                uint32_t todo = (uint32_t)__builtin_amdgcn_ballot_w64(id >= 0);   // lanes l, l + 32 hold one row
+                if (chunk >= lo.planes) todo = 0;              // no partial sum of v is this chunk's
+                while (todo) {
+                    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+                    const uint32_t rows = (uint32_t)__builtin_amdgcn_ballot_w64(id == a);
+                    todo &= ~rows;
+                    const int rank = lo.rank ? min(max(lo.rank[a], 0), lo.R) : lo.R;
+                    float16_t d[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) d[j][r] = 0.0f;
+                    for (int r0 = 0; r0 < rank; r0 += 16) {
+                        const int k = r0 + 8 * h;              // this lane's 8 ranks
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                        if (id == a && k < rank) {             // R % 8 == 0: k + 8 <= R
+                            const float* src = lo.v + (int64_t)chunk * p.M * lo.R + row * lo.R + k;
+                            for (int c = chunk; c < lo.planes; c += ks, src += (int64_t)ks * p.M * lo.R) {
+                                const float4_t v0 = *reinterpret_cast<const float4_t*>(src);
+                                const float4_t v1 = *reinterpret_cast<const float4_t*>(src + 4);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    v[e] += v0[e];
+                                    v[4 + e] += v1[e];
+                                }
+                            }
+                        }
+                        u32x4 hi, lw;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            hi[e] = pack_bf16x2_rne(v[2 * e], v[2 * e + 1]);
+                            lw[e] = pack_bf16x2_rne(v[2 * e] - bf16_to_f32(hi[e] & 0xFFFFu),
+                                                    v[2 * e + 1] - bf16_to_f32(hi[e] >> 16));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + l32;
+                            u32x4 b = {0u, 0u, 0u, 0u};
+                            if (col < N && k < rank) {
+                                b = *reinterpret_cast<const u32x4*>(lo.b + ((int64_t)a * N + col) * lo.R + k);
+                                // what lies beyond the rank is not part of the adapter
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if (k + 2 * e >= rank) b[e] = 0u;
+                                    else if (k + 2 * e + 1 >= rank) b[e] &= 0xFFFFu;
+                                }
+                            }
+                            const bf16x8_t fbv = __builtin_bit_cast(bf16x8_t, b);
+                            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, hi), fbv, d[j], 0, 0, 0);
+                            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, lw), fbv, d[j], 0, 0, 0);
+                        }
+                    }
+                    const uint32_t mine = rows >> (4 * h);     // bit 8 (r / 4) + r % 4: this lane's row r
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const bool take = (mine >> (8 * (r >> 2) + (r & 3))) & 1u;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) acc[i][j][r] += take ? d[j][r] : 0.0f;
+                    }
+                }
+            }
+            if (p.ksplit > 1) {
+                store_f32(p.partial + (int64_t)chunk * p.M * N, 1.0f);
+            } else {
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int local = wm * (32 * MI) + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+                        if (local >= row_count) continue;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + l32;
+                            if (col < N) p.out_bf16[((int64_t)row_start + local) * N + col] = (uint16_t)f32_to_bf16_rne(acc[i][j][r]);
+                        }
+                    }
+            }
         } else if (p.ksplit > 1) {
             store_f32(p.partial + (int64_t)chunk * p.M * N, 1.0f);
         } else {
@@ -610,10 +714,10 @@ void gemm_kernel(GemmParams p) {
 template <int MODE>
 hipError_t launch_mode(const GemmParams& p, hipStream_t s) {
     const int64_t ntn = (MODE == kGemmL1) ? (p.I + 127) / 128 : (p.N + BN - 1) / BN;
-    const int64_t mt = (MODE == kGemmDense) ? (p.M + dense_tile_rows(p.M, p.N) - 1) / dense_tile_rows(p.M, p.N)
+    const int64_t mt = kDense<MODE> ? (p.M + dense_tile_rows(p.M, p.N) - 1) / dense_tile_rows(p.M, p.N)
                                             : p.max_tiles;
     // grouped: whole groups of 8 tiles (one per XCD); dense: every (tile, N-tile, K chunk)
-    const int64_t grid = (MODE == kGemmDense) ? mt * ntn * p.ksplit : (mt + 7) / 8 * 8 * ntn;
+    const int64_t grid = kDense<MODE> ? mt * ntn * p.ksplit : (mt + 7) / 8 * 8 * ntn;
     if (grid <= 0) return hipSuccess;
     static std::atomic<int> lds_set[kMaxDevices];
     hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&gemm_kernel<MODE>), LDS_BYTES, lds_set);
@@ -628,7 +732,7 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restr
                                                             int64_t M, int64_t N, const float* __restrict__ a_gs,
                                                             const float* __restrict__ b_alpha,
                                                             uint16_t* __restrict__ out) {
-    const float alpha = a_gs[0] * b_alpha[0];
+    const float alpha = a_gs ? a_gs[0] * b_alpha[0] : 1.0f;
     const int64_t n4 = M * N / 4;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
         const float* src = partial + 4 * i;
@@ -685,6 +789,7 @@ hipError_t launch_gemm(const GemmParams& p, hipStream_t s) {
     if (p.a_rows * pitch_h(p.K) >= 0x7FFFFFFF || p.N * pitch_q(p.K) >= 0x7FFFFFFF) return hipErrorInvalidValue;
     switch (p.mode) {
         case kGemmDense: return launch_mode<kGemmDense>(p, s);
+        case kGemmLora: return launch_mode<kGemmLora>(p, s);
         case kGemmL1: return launch_mode<kGemmL1>(p, s);
         case kGemmL2: return launch_mode<kGemmL2>(p, s);
         default: return hipErrorInvalidValue;

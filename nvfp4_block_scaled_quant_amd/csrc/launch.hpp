@@ -175,7 +175,28 @@ hipError_t launch_route_topk(const float* logits, int64_t T, int E, int k, int32
 hipError_t launch_combine(const float* o2, const int32_t* slot_row, const float* weights,
                           int64_t T, int topk, int64_t H, uint16_t* y, hipStream_t s);
 
-enum GemmMode { kGemmDense = 0, kGemmL1 = 1, kGemmL2 = 2 };
+enum GemmMode { kGemmDense = 0, kGemmL1 = 1, kGemmL2 = 2, kGemmLora = 3 };
+
+// Low-rank adapters of the rows of a dense GEMM (lora.hip). v holds the
+// shrunk rows scale[a] * x A_a^T as `planes` partial sums (planes, M, R)
+// float32, written only for rows that have an adapter and zero from the
+// adapter's rank on; b (L, N, R) bf16.
+struct LoraParams {
+    const float* v;
+    int planes;
+    const uint16_t* b;
+    const int32_t* ids;        // (M): adapter of each row; outside [0, L): none
+    const int32_t* rank;       // (L) or null: R for all
+    int L, R;
+};
+constexpr int64_t kLoraMaxRank = 256;
+constexpr int kLoraRows = 64;     // rows of a shrink tile
+// number of partial sums (K ranges) of the shrink
+int lora_planes(int64_t M, int64_t K, int64_t L, int64_t R);
+// v of LoraParams from x (M, K), a (L, R, K) and scale (L)
+hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const float* scale, const int32_t* ids,
+                              const int32_t* rank, int64_t M, int64_t K, int64_t L, int64_t R, int planes, float* v,
+                              hipStream_t s);
 
 struct GemmParams {
     int mode;
@@ -213,6 +234,9 @@ struct GemmParams {
     // alpha); launch_splitk_reduce then forms out_bf16
     int ksplit;
     float* partial;
+    // kGemmLora: the dense GEMM whose epilogue adds the adapters; partial
+    // sums then hold alpha and the adapters already
+    LoraParams lora;
 };
 
 hipError_t launch_gemm(const GemmParams& p, hipStream_t s);
@@ -231,7 +255,7 @@ __host__ __device__ inline int64_t dense_tile_rows(int64_t M, int64_t N) {
 }
 
 // out[m][n] = bf16((a_gs[0] * b_alpha[0]) * sum over chunks c, in order, of
-// partial[c][m][n]) for (M, N), N % 4 == 0.
+// partial[c][m][n]) for (M, N), N % 4 == 0; a_gs null: without the factor.
 hipError_t launch_splitk_reduce(const float* partial, int ksplit, int64_t M, int64_t N, const float* a_gs,
                                 const float* b_alpha, uint16_t* out, hipStream_t s);
 

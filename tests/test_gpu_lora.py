@@ -1,0 +1,231 @@
+"""The shared NVFP4 projection with low-rank adapters (nvfp4_gemm_lora) against
+its definition in float64.
+
+Tolerance, per element: half a bf16 step of the result (2^-8 relative), the
+float32 sums (n terms: n * 2^-24 of the sum of magnitudes) of the projection and
+of both adapter products, and the 2^-17 of the shrunk row's two-term bf16 form."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+HALF = 2.0 ** -8
+F32 = 2.0 ** -24
+E2M1 = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+def make(nv, M, N, K, L, R, seed, ids=None, ranks=None):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+
+    def normal(shape, std):
+        return (torch.randn(shape, generator=g) * std).to(torch.bfloat16).cuda()
+
+    x = normal((M, K), 1.5)
+    w = normal((1, K, N), 0.02)
+    aq, asf, a_gs = nv.quantize(x)
+    wq, wsf, b_alpha = nv.quantize_weights(w)
+    bq, bsf = nv.prepack_weights(wq, wsf)
+    s = dict(x=x, aq=aq, asf=asf, a_gs=a_gs, wq=wq[0], wsf=wsf[0], b_alpha=b_alpha, bq=bq[0], bsf=bsf[0],
+             lora_a=normal((L, R, K), K ** -0.5), lora_b=normal((L, N, R), 0.05),
+             lora_scale=(torch.rand((L,), generator=g) * 3 - 1).cuda())
+    if ids is None:
+        ids = torch.randint(-1, L + 1, (M,), generator=g)    # L: no adapter either
+    s["adapter_ids"] = torch.as_tensor(ids).to(torch.int32).cuda()
+    s["lora_rank"] = None if ranks is None else torch.as_tensor(ranks).to(torch.int32).cuda()
+    return s
+
+
+def run(nv, s, **kw):
+    return nv.gemm_lora(s["aq"], s["asf"], s["a_gs"], s["bq"], s["bsf"], s["b_alpha"], s["x"], s["lora_a"],
+                        s["lora_b"], s["lora_scale"], s["adapter_ids"], lora_rank=s["lora_rank"], **kw)
+
+
+def dequant(q, sf, dim):
+    """float64 values of packed codes and scales along dimension `dim`."""
+    import torch
+    table = torch.tensor(E2M1 + [-v for v in E2M1], dtype=torch.float64, device=q.device)
+    v = torch.stack((table[(q & 15).long()], table[(q >> 4).long()]), dim + 1)
+    v = v.flatten(dim, dim + 1)
+    return v * sf.view(torch.float8_e4m3fn).double().repeat_interleave(16, dim)
+
+
+def check(s, out):
+    import torch
+    M, N = out.shape
+    K = s["x"].shape[1]
+    L, R = s["lora_a"].shape[:2]
+    a, b = dequant(s["aq"], s["asf"], 1), dequant(s["wq"], s["wsf"], 0)
+    alpha = s["a_gs"].double() * s["b_alpha"].double()
+    ref, mag = alpha * (a @ b), alpha.abs() * (a.abs() @ b.abs())
+    err = (K + 4) * F32 * mag
+    ids = s["adapter_ids"]
+    for i in range(L):
+        rows = (ids == i).nonzero()[:, 0]
+        if not len(rows):
+            continue
+        r = R if s["lora_rank"] is None else max(0, min(R, int(s["lora_rank"][i])))
+        la, lb, sc = s["lora_a"][i, :r].double(), s["lora_b"][i, :, :r].double(), s["lora_scale"][i].double()
+        x = s["x"][rows].double()
+        v, vm = sc * (x @ la.t()), sc.abs() * (x.abs() @ la.abs().t())
+        ref[rows] += v @ lb.t()
+        err[rows] += ((K + 16) * F32 * vm + 2.0 ** -16 * v.abs()) @ lb.abs().t()
+        err[rows] += (2 * R + 4) * F32 * (v.abs() @ lb.abs().t())
+    tol = HALF * ref.abs() + err * (1 + HALF) + 4 * F32 * ref.abs() + 1e-37
+    d = (out.double() - ref).abs()
+    assert bool((d <= tol).all()), float((d / tol).max())
+
+
+# single rows; every row count around the 16-, 64-, 128- and 256-row tiles;
+# K tails (multiples of 16 only); ranks that end inside a 16-rank block and go
+# past a 64-rank one; one adapter and more adapters than rows
+@pytest.mark.parametrize("M,N,K,L,R", [
+    (1, 16, 16, 1, 8), (1, 6144, 7168, 8, 16), (2, 48, 144, 3, 24), (5, 272, 208, 40, 8), (13, 1024, 2048, 16, 64),
+    (16, 512, 1040, 4, 16), (17, 256, 512, 17, 32), (33, 784, 272, 5, 72), (61, 1536, 1024, 32, 32),
+    (64, 512, 4096, 64, 128), (65, 528, 512, 65, 16), (128, 512, 256, 3, 256), (129, 1040, 528, 9, 40),
+    (256, 768, 640, 6, 16), (300, 512, 256, 20, 64), (513, 6144, 512, 2, 16), (1300, 6144, 144, 7, 136),
+    (4093, 4096, 128, 300, 8)])
+def test_random_ids(nv, M, N, K, L, R):
+    import torch
+    s = make(nv, M, N, K, L, R, M + N + K + L + R)
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    run(nv, s, out=out)
+    check(s, out)
+    assert torch.equal(run(nv, s), out)
+
+
+@pytest.mark.parametrize("M", [7, 64, 200, 1500])
+def test_runs_of_rows(nv, M):
+    """Requests as runs of rows, some without an adapter; ranks of their own,
+    0 and beyond R among them."""
+    import torch
+    L, R = 6, 48
+    cuts = sorted(set([0, M] + [int(M * f) for f in (0.1, 0.33, 0.34, 0.7, 0.95)]))
+    ids = torch.full((M,), -1)
+    for n, (a, b) in enumerate(zip(cuts[:-1], cuts[1:])):
+        ids[a:b] = (n * 5) % (L + 1) - 1
+    s = make(nv, M, 528, 1040, L, R, M, ids=ids, ranks=[48, 0, 7, 33, 100, -3])
+    check(s, run(nv, s))
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_no_row_has_an_adapter(nv, M):
+    """Only the shared projection: what nvfp4_gemm gives up to summation order."""
+    import torch
+    s = make(nv, M, 256, 512, 4, 16, M, ids=torch.tensor([-1, 4, 2 ** 30, -2 ** 31]).repeat(M)[:M])
+    check(s, run(nv, s))
+
+
+@pytest.mark.parametrize("M", [9, 64, 100, 700])
+def test_broken_requests_stay_alone(nv, M):
+    """NaN and infinity in one request's adapter, and in what is stored beyond
+    the ranks, reach no other row."""
+    import torch
+    L, R, N, K = 5, 24, 272, 528
+    s = make(nv, M, N, K, L, R, 3 * M, ids=torch.arange(M) % (L + 1) - 1, ranks=[24, 9, 16, 24, 1])
+    out = run(nv, s).clone()
+    check(s, out)
+    for a, r in enumerate([24, 9, 16, 24, 1]):
+        s["lora_a"][a, r:] = float("nan")
+        s["lora_b"][a, :, r:] = float("inf")
+    assert torch.equal(run(nv, s), out)
+    s["lora_a"][3, 5], s["lora_b"][3, ::3] = float("inf"), float("nan")
+    s["x"][1] = float("nan")                          # aq stays: only the adapter's input is broken
+    keep = (s["adapter_ids"] != 3) & (torch.arange(M, device="cuda") != 1)
+    again = run(nv, s)
+    assert torch.equal(again[keep], out[keep])
+    assert bool(again[s["adapter_ids"] == 3][:, ::3].isnan().all())
+
+
+def test_a_request_does_not_depend_on_its_batch_mates_ids(nv):
+    """The same rows beside other ids: rows whose id did not change keep their
+    bits."""
+    import torch
+    s = make(nv, 50, 256, 1024, 8, 16, 4)
+    out = run(nv, s).clone()
+    ids = s["adapter_ids"].clone()
+    ids[10:30] = torch.flip(ids[10:30], (0,))
+    same = ids == s["adapter_ids"]
+    s["adapter_ids"] = ids
+    assert torch.equal(run(nv, s)[same], out[same])
+
+
+@pytest.mark.parametrize("M", [1, 20, 150])
+def test_streams_and_graph(nv, M):
+    import torch
+    N, K, L, R = 512, 1024, 4, 16
+    s = make(nv, M, N, K, L, R, 5)
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty((nv._lib.nvfp4_gemm_lora_workspace(M, N, K, L, R),), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = run(nv, s)
+    torch.cuda.current_stream().wait_stream(side)
+    check(s, other)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(nv, s, out=out, workspace=ws)
+    for seed in (6, 7, 8):
+        t = make(nv, M, N, K, L, R, seed)
+        for k in ("x", "aq", "asf", "a_gs", "bq", "bsf", "b_alpha", "lora_a", "lora_b", "lora_scale", "adapter_ids"):
+            s[k].copy_(t[k])
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(t, out)
+        assert torch.equal(run(nv, t), out)
+
+
+def test_refusals(nv):
+    import torch
+    s = make(nv, 4, 32, 64, 2, 8, 1)
+
+    def bad(exc, **kw):
+        t = dict(s)
+        t.update(kw)
+        with pytest.raises(exc):
+            run(nv, t)
+
+    bad(TypeError, x=s["x"].float())
+    bad(TypeError, lora_a=s["lora_a"].half())
+    bad(TypeError, adapter_ids=s["adapter_ids"].long())
+    bad(TypeError, lora_scale=s["lora_scale"].cpu())
+    bad(ValueError, lora_a=s["lora_a"].transpose(1, 2))
+    bad(ValueError, lora_a=s["lora_a"][:, :, :48].contiguous())
+    bad(ValueError, lora_a=s["lora_a"][:, :4].contiguous(), lora_b=s["lora_b"][:, :, :4].contiguous())   # R % 8
+    bad(ValueError, adapter_ids=s["adapter_ids"][:3].contiguous())
+    bad(ValueError, lora_rank=torch.ones((3,), dtype=torch.int32, device="cuda"))
+    bad(ValueError, lora_a=s["lora_a"][:0], lora_b=s["lora_b"][:0], lora_scale=s["lora_scale"][:0])
+    with pytest.raises(nv.Nvfp4Error):
+        run(nv, s, workspace=torch.empty((16,), dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        run(nv, s, out=torch.empty((4, 48), dtype=torch.bfloat16, device="cuda"))
+
+
+def test_empty_batch(nv):
+    s = make(nv, 4, 32, 64, 2, 8, 1)
+    for k in ("x", "aq", "asf", "adapter_ids"):
+        s[k] = s[k][:0]
+    assert run(nv, s).shape == (0, 32)
+
+
+@pytest.mark.parametrize("T", [1, 37, 300])
+def test_feed_forward_with_adapters(nv, T):
+    """The dense feed-forward as it is used: the gated block in bf16, its
+    output quantized, the shared NVFP4 down projection with each request's
+    adapter, beside the routed experts' own entry points on one stream."""
+    import torch
+    H, I, L, R = 512, 256, 4, 16
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn((T, H), generator=g).to(torch.bfloat16).cuda()
+    w13 = (torch.randn((H, 2 * I), generator=g) * 0.05).to(torch.bfloat16).cuda()
+    s = make(nv, T, H, I, L, R, T + 9)
+    act = nv.gated_forward(x, w13)
+    s["x"] = act
+    s["aq"], s["asf"], s["a_gs"] = nv.quantize(act)
+    y = run(nv, s)
+    check(s, y)
+    gu = x.double() @ w13.double()
+    ref = gu[:, :I] * torch.sigmoid(gu[:, :I]) * gu[:, I:]
+    assert float((act.double() - ref).norm() / ref.norm()) < HALF
