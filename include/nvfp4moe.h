@@ -443,15 +443,15 @@ int nvfp4_route_topk(const float* logits, int64_t T, int64_t E, int64_t topk,
  *                nearest); what is stored beyond them is not used.
  *   adapter_ids  (M) int32
  *   x, lora_a, lora_b 16-byte aligned; R % 8 == 0, 8 <= R <= 256, 1 <= L <=
- *   65535, M <= 2^22, K % 16 == 0, N % 16 == 0 and nvfp4_gemm's limits, else
+ *   8192, M <= 2^22, K % 16 == 0, N % 16 == 0 and nvfp4_gemm's limits, else
  *   NVFP4_ESHAPE.
  * A row depends on its own x, aq and adapter and on no other: NaN in one
  * request's row or adapter stays in that request's rows. Deterministic: the
  * order of every sum depends on the sizes alone, not on the ids.
  *
  * Workspace: nvfp4_gemm_lora_workspace(M, N, K, L, R) bytes, 256-byte
- * aligned (nvfp4_gemm's, and the shrunk rows); 0 for invalid sizes. M == 0
- * enqueues nothing.
+ * aligned (the shrunk rows, and A in the form that the kernels of the batch
+ * size take); 0 for invalid sizes. M == 0 enqueues nothing.
  * ------------------------------------------------------------------------ */
 size_t nvfp4_gemm_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
 int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs,

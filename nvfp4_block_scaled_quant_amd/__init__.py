@@ -450,8 +450,8 @@ def gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, ad
     L, R = lora_a.shape[0], lora_a.shape[1]
     if K % 16 or K == 0 or N == 0:
         raise ValueError("gemm_lora: K must be a positive multiple of 16 and N positive")
-    if R % 8 or not 8 <= R <= 256 or L < 1:
-        raise ValueError("gemm_lora: R must be a multiple of 8 from 8 to 256, and L at least 1")
+    if R % 8 or not 8 <= R <= 256 or not 1 <= L <= 8192:
+        raise ValueError("gemm_lora: R must be a multiple of 8 from 8 to 256, and L from 1 to 8192")
     shq, shs = packed_shapes(1, K, N)
     if (aq.shape != (M, K // 2) or asf.shape != (M, K // 16) or tuple(bq.shape) != shq[1:]
             or tuple(bsf.shape) != shs[1:] or lora_a.shape != (L, R, K) or lora_b.shape != (L, N, R)

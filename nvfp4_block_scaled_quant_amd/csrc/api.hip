@@ -535,16 +535,40 @@ namespace {
 
 bool lora_shape_ok(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     if (M < 0 || N <= 0 || K <= 0 || L <= 0 || R <= 0 || K % 16 || N % 16 || R % 8) return false;
-    if (R > kLoraMaxRank || L > 65535 || M > (int64_t)1 << 22) return false;
+    if (R > kLoraMaxRank || L > kLoraMaxAdapters || M > (int64_t)1 << 22) return false;
     return M * pitch_h(K) < 0x7FFFFFFF && N * pitch_q(K) < 0x7FFFFFFF;
 }
 
 }  // namespace
 
-// nvfp4_gemm's workspace, then the partial sums of the shrunk rows
+namespace {
+
+// the shrunk rows, then A for streaming, or the tiled GEMM's workspace
+// and the rows' order
+struct LoraLayout {
+    size_t v, aqp, asfp, gemm, perm, sid, total;
+};
+
+LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+    LoraLayout w = {};
+    const int64_t m = M > 0 ? M : 1;
+    w.aqp = align_up((size_t)lora_planes(m, K, L, R) * (size_t)m * (size_t)R * 4);
+    if (lora_streams(m)) {
+        w.asfp = w.aqp + align_up((size_t)lora_stream_aq_bytes(m, K));
+        w.total = w.asfp + align_up((size_t)lora_stream_asf_bytes(m, K));
+    } else {
+        w.gemm = w.aqp;
+        w.perm = w.gemm + align_up(nvfp4_gemm_workspace(m, N, K));
+        w.sid = w.perm + align_up((size_t)m * 4);
+        w.total = w.sid + align_up((size_t)m * 4);
+    }
+    return w;
+}
+
+}  // namespace
+
 size_t nvfp4_gemm_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
-    if (!lora_shape_ok(M, N, K, L, R)) return 0;
-    return align_up(nvfp4_gemm_workspace(M, N, K)) + (size_t)lora_planes(M > 0 ? M : 1, K, L, R) * (size_t)M * (size_t)R * 4;
+    return lora_shape_ok(M, N, K, L, R) ? lora_layout(M, N, K, L, R).total : 0;
 }
 
 int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, const uint8_t* bq, const uint8_t* bsf,
@@ -566,13 +590,37 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
         return NVFP4_EWORKSPACE;
     int dv = check_device();
     if (dv) return dv;
-    uint16_t* ah = static_cast<uint16_t*>(workspace);
-    float* v = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align_up(nvfp4_gemm_workspace(M, N, K)));
-    const int planes = lora_planes(M, K, L, R);
-    NVFP4_TRY(launch_dequant_rows_f16(aq, asf, M, K, ah, stream));
-    NVFP4_TRY(launch_lora_shrink(x, lora_a, lora_scale, adapter_ids, lora_rank, M, K, L, R, planes, v, stream));
+    const LoraLayout w = lora_layout(M, N, K, L, R);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    LoraParams lo = {};
+    lo.x = x;
+    lo.a = lora_a;
+    lo.scale = lora_scale;
+    lo.v = reinterpret_cast<float*>(ws + w.v);
+    lo.planes = lora_planes(M, K, L, R);
+    lo.b = lora_b;
+    lo.ids = adapter_ids;
+    lo.rank = lora_rank;
+    lo.M = M;
+    lo.K = K;
+    lo.N = N;
+    lo.L = (int)L;
+    lo.R = (int)R;
+    if (lora_streams(M)) {
+        NVFP4_TRY(launch_lora_shrink(lo, aq, asf, ws + w.aqp, ws + w.asfp, stream));
+        NVFP4_TRY(launch_lora_stream(lo, ws + w.aqp, ws + w.asfp, bq, bsf, a_gs, b_alpha, out, stream));
+        return NVFP4_OK;
+    }
+    uint16_t* ah = reinterpret_cast<uint16_t*>(ws + w.gemm);
+    int32_t* perm = reinterpret_cast<int32_t*>(ws + w.perm);
+    int32_t* sid = reinterpret_cast<int32_t*>(ws + w.sid);
+    NVFP4_TRY(launch_lora_sort(adapter_ids, M, L, perm, sid, aq, asf, K, ah, stream));
+    lo.perm = perm;
+    lo.ids = sid;
+    NVFP4_TRY(launch_lora_shrink(lo, nullptr, nullptr, nullptr, nullptr, stream));
     GemmParams p = {};
-    p.mode = kGemmLora;
+    p.ksplit = dense_ksplit(M, N, K);
+    p.mode = p.ksplit > 1 ? kGemmDense : kGemmLora;
     p.ah = ah;
     p.M = M;
     p.a_rows = M;
@@ -583,11 +631,10 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
     p.a_gs = a_gs;
     p.b_alpha = b_alpha;
     p.out_bf16 = out;
-    p.ksplit = dense_ksplit(M, N, K);
-    p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + gemm_ws_partial_offset(M, K));
-    p.lora = {v, planes, lora_b, adapter_ids, lora_rank, (int)L, (int)R};
+    p.partial = reinterpret_cast<float*>(ws + w.gemm + gemm_ws_partial_offset(M, K));
+    p.lora = lo;
     NVFP4_TRY(launch_gemm(p, stream));
-    if (p.ksplit > 1) NVFP4_TRY(launch_splitk_reduce(p.partial, p.ksplit, M, N, nullptr, nullptr, out, stream));
+    if (p.ksplit > 1) NVFP4_TRY(launch_lora_reduce(lo, p.partial, p.ksplit, a_gs, b_alpha, out, stream));
     return NVFP4_OK;
 }
 

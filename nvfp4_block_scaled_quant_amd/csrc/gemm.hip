@@ -68,6 +68,7 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "lora.hpp"
 
 namespace nvfp4 {
 
@@ -190,6 +191,7 @@ void gemm_kernel(GemmParams p) {
         auto a_src = [&](int r) -> int64_t {        // A tensor row of tile row r
             int64_t src = row_start + (r < row_count ? r : 0);
             if (MODE == kGemmL1) src = p.a_gather[src] / p.topk;
+            if (MODE == kGemmLora) src = p.lora.perm[src];
             return src;
         };
         auto b_src = [&](int vc) -> int64_t {       // weight row (output column) of virtual column vc
@@ -585,16 +587,14 @@ void gemm_kernel(GemmParams p) {
             store_f32(p.out_f32, alpha);
         } else if (MODE == kGemmLora) {
             // The adapters, on the matrix cores, into the same accumulators:
-            // delta = v B_a^T per 32-row block and adapter that occurs in it,
-            // added to the rows that have the adapter (the others' results
-            // are dropped by a select, not multiplied by zero: a NaN of one
-            // adapter reaches no other row). v is float32 and enters as the
-            // sum of two bf16 values (2^-17 relative), B_a is bf16. K chunk c
-            // takes the partial sums c, c + ksplit, ... of v, so that the
-            // chunks share this work too.
+            // delta = v B_a^T per 32-row block and adapter that occurs in it
+            // (the rows are grouped by adapter: one or two), added to the rows
+            // that have the adapter (the others' results are dropped by a
+            // select, not multiplied by zero: a NaN of one adapter reaches no
+            // other row). v is float32 and enters as the sum of two bf16
+            // values (2^-17 relative), B_a is bf16.
             typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
             const LoraParams& lo = p.lora;
-            const int ks = p.ksplit > 1 ? p.ksplit : 1;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
 #pragma unroll
@@ -602,11 +602,10 @@ void gemm_kernel(GemmParams p) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[i][j][r] *= alpha;
                 const int local = wm * (32 * MI) + 32 * i + l32;
-                const int64_t row = (int64_t)row_start + local;
-                int id = local < row_count ? lo.ids[row] : -1;
-                if (id >= lo.L) id = -1;
+                const bool in = local < row_count;
+                const int id = in ? lo.ids[(int64_t)row_start + local] : -1;
+                const int64_t row = in ? lo.perm[(int64_t)row_start + local] : 0;
                 uint32_t todo = (uint32_t)__builtin_amdgcn_ballot_w64(id >= 0);   // lanes l, l + 32 hold one row
-                if (chunk >= lo.planes) todo = 0;              // no partial sum of v is this chunk's
                 while (todo) {
                     const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
                     const uint32_t rows = (uint32_t)__builtin_amdgcn_ballot_w64(id == a);
@@ -618,43 +617,13 @@ void gemm_kernel(GemmParams p) {
 #pragma unroll
                         for (int r = 0; r < 16; ++r) d[j][r] = 0.0f;
                     for (int r0 = 0; r0 < rank; r0 += 16) {
-                        const int k = r0 + 8 * h;              // this lane's 8 ranks
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-                        if (id == a && k < rank) {             // R % 8 == 0: k + 8 <= R
-                            const float* src = lo.v + (int64_t)chunk * p.M * lo.R + row * lo.R + k;
-                            for (int c = chunk; c < lo.planes; c += ks, src += (int64_t)ks * p.M * lo.R) {
-                                const float4_t v0 = *reinterpret_cast<const float4_t*>(src);
-                                const float4_t v1 = *reinterpret_cast<const float4_t*>(src + 4);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    v[e] += v0[e];
-                                    v[4 + e] += v1[e];
-                                }
-                            }
-                        }
+                        const int k = r0 + 8 * h;              // this lane's 8 ranks (R % 8 == 0: k + 8 <= R)
                         u32x4 hi, lw;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            hi[e] = pack_bf16x2_rne(v[2 * e], v[2 * e + 1]);
-                            lw[e] = pack_bf16x2_rne(v[2 * e] - bf16_to_f32(hi[e] & 0xFFFFu),
-                                                    v[2 * e + 1] - bf16_to_f32(hi[e] >> 16));
-                        }
+                        lora_v_operand(lo, id == a && k < rank, row, k, hi, lw);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + l32;
-                            u32x4 b = {0u, 0u, 0u, 0u};
-                            if (col < N && k < rank) {
-                                b = *reinterpret_cast<const u32x4*>(lo.b + ((int64_t)a * N + col) * lo.R + k);
-                                // what lies beyond the rank is not part of the adapter
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if (k + 2 * e >= rank) b[e] = 0u;
-                                    else if (k + 2 * e + 1 >= rank) b[e] &= 0xFFFFu;
-                                }
-                            }
-                            const bf16x8_t fbv = __builtin_bit_cast(bf16x8_t, b);
+                            const bf16x8_t fbv = __builtin_bit_cast(bf16x8_t, lora_b_operand(lo, col < N, a, col, k, rank));
                             d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, hi), fbv, d[j], 0, 0, 0);
                             d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, lw), fbv, d[j], 0, 0, 0);
                         }
@@ -667,22 +636,17 @@ void gemm_kernel(GemmParams p) {
                         for (int j = 0; j < 2; ++j) acc[i][j][r] += take ? d[j][r] : 0.0f;
                     }
                 }
-            }
-            if (p.ksplit > 1) {
-                store_f32(p.partial + (int64_t)chunk * p.M * N, 1.0f);
-            } else {
 #pragma unroll
-                for (int i = 0; i < MI; ++i)
+                for (int r = 0; r < 16; ++r) {
+                    const int lr = wm * (32 * MI) + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
+                    if (lr >= row_count) continue;
+                    uint16_t* dst = p.out_bf16 + (int64_t)lo.perm[(int64_t)row_start + lr] * N;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int local = wm * (32 * MI) + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-                        if (local >= row_count) continue;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + l32;
-                            if (col < N) p.out_bf16[((int64_t)row_start + local) * N + col] = (uint16_t)f32_to_bf16_rne(acc[i][j][r]);
-                        }
+                    for (int j = 0; j < 2; ++j) {
+                        const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + l32;
+                        if (col < N) dst[col] = (uint16_t)f32_to_bf16_rne(acc[i][j][r]);
                     }
+                }
             }
         } else if (p.ksplit > 1) {
             store_f32(p.partial + (int64_t)chunk * p.M * N, 1.0f);
@@ -732,7 +696,7 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restr
                                                             int64_t M, int64_t N, const float* __restrict__ a_gs,
                                                             const float* __restrict__ b_alpha,
                                                             uint16_t* __restrict__ out) {
-    const float alpha = a_gs ? a_gs[0] * b_alpha[0] : 1.0f;
+    const float alpha = a_gs[0] * b_alpha[0];
     const int64_t n4 = M * N / 4;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
         const float* src = partial + 4 * i;

@@ -180,22 +180,48 @@ enum GemmMode { kGemmDense = 0, kGemmL1 = 1, kGemmL2 = 2, kGemmLora = 3 };
 // Low-rank adapters of the rows of a dense GEMM (lora.hip). v holds the
 // shrunk rows scale[a] * x A_a^T as `planes` partial sums (planes, M, R)
 // float32, written only for rows that have an adapter and zero from the
-// adapter's rank on; b (L, N, R) bf16.
+// adapter's rank on; b (L, N, R) bf16. perm / ids list the rows grouped by
+// adapter: row perm[i] has adapter ids[i] (-1: none); perm null: the rows in
+// order, and ids (M) the caller's (outside [0, L): none).
 struct LoraParams {
-    const float* v;
+    const uint16_t* x;         // (M, K)
+    const uint16_t* a;         // (L, R, K)
+    const float* scale;        // (L)
+    float* v;
     int planes;
     const uint16_t* b;
-    const int32_t* ids;        // (M): adapter of each row; outside [0, L): none
+    const int32_t* perm;
+    const int32_t* ids;
     const int32_t* rank;       // (L) or null: R for all
+    int64_t M, K, N;
     int L, R;
 };
 constexpr int64_t kLoraMaxRank = 256;
-constexpr int kLoraRows = 64;     // rows of a shrink tile
+constexpr int64_t kLoraMaxAdapters = 8192;
+constexpr int kLoraRows = 64;     // rows of a tile of the adapters' kernels
+constexpr int kLoraStreamRows = 32;
+// Whether M rows take the weight-streaming kernel (then A is laid out by
+// launch_lora_shrink) or the tiled GEMM.
+inline bool lora_streams(int64_t M) { return M <= kLoraStreamRows; }
+// bytes of the streaming kernel's A operand: rows padded to 16, K to whole
+// groups of four steps for the scales
+inline int64_t lora_stream_aq_bytes(int64_t M, int64_t K) { return (M + 15) / 16 * 16 * pitch_q(K); }
+inline int64_t lora_stream_asf_bytes(int64_t M, int64_t K) { return (M + 15) / 16 * 16 * pitch_wsf(K); }
 // number of partial sums (K ranges) of the shrink
 int lora_planes(int64_t M, int64_t K, int64_t L, int64_t R);
-// v of LoraParams from x (M, K), a (L, R, K) and scale (L)
-hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const float* scale, const int32_t* ids,
-                              const int32_t* rank, int64_t M, int64_t K, int64_t L, int64_t R, int planes, float* v,
+// Rows by adapter: perm (M), sid (M) from the caller's ids; and, beside it,
+// A's exact f16 form (launch_dequant_rows_f16).
+hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int64_t L, int32_t* perm, int32_t* sid, const uint8_t* aq,
+                            const uint8_t* asf, int64_t K, uint16_t* ah, hipStream_t s);
+// p.v; with aqp not null also A in the streaming kernel's layout.
+hipError_t launch_lora_shrink(const LoraParams& p, const uint8_t* aq, const uint8_t* asf, uint8_t* aqp, uint8_t* asfp,
+                              hipStream_t s);
+// out = bf16(alpha * sum over chunks of partial[c] (M, N) + adapters)
+hipError_t launch_lora_reduce(const LoraParams& p, const float* partial, int ksplit, const float* a_gs,
+                              const float* b_alpha, uint16_t* out, hipStream_t s);
+// out = bf16(alpha * A W + adapters) for lora_streams(M)
+hipError_t launch_lora_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t* asfp, const uint8_t* bq,
+                              const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out,
                               hipStream_t s);
 
 struct GemmParams {
@@ -234,8 +260,8 @@ struct GemmParams {
     // alpha); launch_splitk_reduce then forms out_bf16
     int ksplit;
     float* partial;
-    // kGemmLora: the dense GEMM whose epilogue adds the adapters; partial
-    // sums then hold alpha and the adapters already
+    // kGemmLora: the dense GEMM over the rows grouped by adapter, whose
+    // epilogue adds the adapters (one K chunk)
     LoraParams lora;
 };
 
@@ -255,7 +281,7 @@ __host__ __device__ inline int64_t dense_tile_rows(int64_t M, int64_t N) {
 }
 
 // out[m][n] = bf16((a_gs[0] * b_alpha[0]) * sum over chunks c, in order, of
-// partial[c][m][n]) for (M, N), N % 4 == 0; a_gs null: without the factor.
+// partial[c][m][n]) for (M, N), N % 4 == 0.
 hipError_t launch_splitk_reduce(const float* partial, int ksplit, int64_t M, int64_t N, const float* a_gs,
                                 const float* b_alpha, uint16_t* out, hipStream_t s);
 

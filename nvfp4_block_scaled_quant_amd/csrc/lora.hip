@@ -1,22 +1,29 @@
 // Low-rank adapters of many requests beside one shared NVFP4 projection:
 //   out[m] = bf16(alpha * A[m] W + scale[a] (x[m] A_a^T) B_a^T),  a = ids[m]
-// with A_a (R, K) and B_a (N, R) in bf16. The product with A_a ("shrink", here)
-// gives v[m] = scale[a] x[m] A_a^T in float32; the product with B_a is added in
-// the epilogue of the shared projection (gemm.hip), before its one rounding.
+// with A_a (R, K) and B_a (N, R) in bf16. The product with A_a ("shrink") gives
+// v[m] = scale[a] x[m] A_a^T in float32; the product with B_a ("expand") is added
+// to the projection before its one rounding. Per batch size:
+//   up to 32 rows   shrink (beside it A laid out for streaming), then one kernel
+//                   that streams the weights and adds the adapters
+//   more rows       the rows are listed by adapter (beside it A's f16 form),
+//                   shrink, the tiled GEMM; the expand is in its epilogue, or,
+//                   where K is cut into chunks, in the kernel that adds them
+// A row's arithmetic does not depend on its place in a tile or on the other
+// rows, so results depend neither on scheduling nor on the grouping.
 //
 // Shrink. What has to move is x once and each adapter's A_a once; the
 // arithmetic is small, so the split is made for bytes in flight. A work-group
-// takes one tile of 64 rows, one adapter that occurs in it and one range of K,
-// and gathers the tile's rows that have the adapter, so an adapter is read
-// once per tile however its rows are scattered (a decode batch of 64 rows
-// reads each adapter once; in a prefill batch a tile has one or two). Its 8
-// waves interleave over the range in blocks of 64 K values, read straight from
-// memory into v_mfma_f32_16x16x32_bf16 operands (a lane takes 32 contiguous
-// bytes of a row, so a row's block is one 128-byte line), and join their sums
-// in wave order through LDS. Ranges of K are separate partial sums, added in
-// order by the reader. Nothing depends on scheduling.
+// takes one tile of 64 (listed) rows, one adapter that occurs in it and one
+// range of K, and gathers the rows that have the adapter, so an adapter is read
+// once per tile however its rows are scattered. Its 8 waves interleave over the
+// range in blocks of 64 K values, read straight from memory into
+// v_mfma_f32_16x16x32_bf16 operands (a lane takes 32 contiguous bytes of a row,
+// so a row's block is one 128-byte line), and join their sums in wave order
+// through LDS. Ranges of K are separate partial sums, added in order by the
+// reader.
 #include "common.hpp"
 #include "launch.hpp"
+#include "lora.hpp"
 
 namespace nvfp4 {
 
@@ -29,40 +36,87 @@ constexpr int NW = NT / 64;
 constexpr int kRankBlock = 64;      // ranks of a work-group (4 column blocks of 16)
 constexpr int kSlots = 16;          // work-groups that share a tile's adapters
 
-__global__ __launch_bounds__(NT) void lora_shrink_kernel(const uint16_t* __restrict__ x,
-                                                         const uint16_t* __restrict__ wa,
-                                                         const float* __restrict__ scale,
-                                                         const int32_t* __restrict__ ids,
-                                                         const int32_t* __restrict__ rank, int64_t M, int64_t K,
-                                                         int L, int R, int planes, float* __restrict__ v) {
+// A in the streaming kernel's layout, zero beyond M and K: data per 16-row
+// block and 128-element step as one kilobyte (lane l = 16 q + c holds bytes
+// [16 q, +16) of the step of row c), scales as the packed weights' (per group
+// of four steps: row, pair q, step, two bytes).
+__device__ void lay_out_a(const LoraParams& p, const uint8_t* __restrict__ aq, const uint8_t* __restrict__ asf,
+                          uint8_t* __restrict__ aqp, uint8_t* __restrict__ asfp, int64_t first, int64_t stride) {
+    const int steps = (int)(pitch_q(p.K) / 64), quads = (int)(pitch_wsf(p.K) / 32);
+    const int mt = (int)((p.M + 15) / 16);
+    const int64_t kb = p.K / 2, kg = p.K / 16;
+    const int64_t nd = (int64_t)mt * steps * 64, nsf = (int64_t)mt * quads * 64;
+    for (int64_t i = first; i < nd + nsf; i += stride) {
+        if (i < nd) {
+            const int lane = (int)(i & 63), st = (int)((i >> 6) % steps);
+            const int64_t row = (i >> 6) / steps * 16 + (lane & 15), at = 64 * st + 16 * (lane >> 4);
+            u32x2 lo = {0u, 0u}, hi = {0u, 0u};
+            if (row < p.M && at < kb) lo = *reinterpret_cast<const u32x2*>(aq + row * kb + at);      // K / 2 % 8 == 0
+            if (row < p.M && at + 8 < kb) hi = *reinterpret_cast<const u32x2*>(aq + row * kb + at + 8);
+            *reinterpret_cast<u32x4*>(aqp + 16 * i) = (u32x4){lo[0], lo[1], hi[0], hi[1]};
+        } else {
+            const int64_t j = i - nd;
+            const int t = (int)(j & 63), c = t >> 2, q = t & 3, quad = (int)((j >> 6) % quads);
+            const int64_t row = (j >> 6) / quads * 16 + c;
+            uint32_t w[2] = {0u, 0u};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int64_t g = 8 * (4 * quad + u) + 2 * q + e;
+                    if (row < p.M && g < kg) w[u >> 1] |= (uint32_t)asf[row * kg + g] << (16 * (u & 1) + 8 * e);
+                }
+            *reinterpret_cast<u32x2*>(asfp + 8 * j) = (u32x2){w[0], w[1]};
+        }
+    }
+}
+
+__global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles, int slots, int shrink_blocks,
+                                                         const uint8_t* __restrict__ aq,
+                                                         const uint8_t* __restrict__ asf, uint8_t* __restrict__ aqp,
+                                                         uint8_t* __restrict__ asfp) {
+    if ((int)blockIdx.x >= shrink_blocks) {          // the launch's further work-groups: A's layout
+        lay_out_a(p, aq, asf, aqp, asfp, (int64_t)(blockIdx.x - shrink_blocks) * NT + threadIdx.x,
+                  (int64_t)(gridDim.x - shrink_blocks) * NT);
+        return;
+    }
     __shared__ int list[kLoraRows];
     __shared__ __attribute__((aligned(16))) float red[NW][16][kRankBlock + 4];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, q = lane >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * kLoraRows;
-    const int plane = blockIdx.z % planes, rb = blockIdx.z / planes;
+    const int tile = blockIdx.x % tiles, rest = blockIdx.x / tiles;
+    const int slot = rest % slots, z = rest / slots;
+    const int plane = z % p.planes, rb = z / p.planes;
+    const int64_t m0 = (int64_t)tile * kLoraRows;
     const int rbase = rb * kRankBlock;
+    const int64_t M = p.M, K = p.K;
+    const int L = p.L, R = p.R, planes = p.planes;
+    const uint16_t* __restrict__ x = p.x;
+    const uint16_t* __restrict__ wa = p.a;
+    const int32_t* __restrict__ rank = p.rank;
+    float* __restrict__ v = p.v;
 
-    int id = m0 + lane < M ? ids[m0 + lane] : -1;
+    int id = m0 + lane < M ? p.ids[m0 + lane] : -1;
     if (id >= L) id = -1;
+    const int row_of = m0 + lane < M ? (p.perm ? p.perm[m0 + lane] : (int)(m0 + lane)) : 0;
     uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
     // blocks of 64 K values of this plane, dealt to the waves in turn
     const int nb = (int)((K + 63) / 64), per = (nb + planes - 1) / planes;
     const int b0 = plane * per, b1 = min(nb, b0 + per);
 
     // the tile's adapters in order of first appearance: this work-group takes
-    // numbers y, y + gridDim.y, ...
+    // numbers slot, slot + slots, ...
     for (int d = 0; todo; ++d) {
         const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
         const uint64_t rows = __builtin_amdgcn_ballot_w64(id == a);
         todo &= ~rows;
-        if (d % (int)gridDim.y != (int)blockIdx.y) continue;
+        if (d % slots != slot) continue;
         const int rk = rank ? min(max(rank[a], 0), R) : R;
         const int n = __builtin_popcountll(rows);
-        const float sc = scale[a];
+        const float sc = p.scale[a];
         __syncthreads();                             // the previous adapter's readers are done
-        if (wave == 0 && id == a) list[__builtin_popcountll(rows & ((1ull << lane) - 1))] = lane;
+        if (wave == 0 && id == a) list[__builtin_popcountll(rows & ((1ull << lane) - 1))] = row_of;
         __syncthreads();
 
         const int groups = (n + 15) / 16;            // 16-row groups of the gathered rows
@@ -73,7 +127,7 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(const uint16_t* __restr
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             xok[g] = 16 * g + c < n;
-            xr[g] = x + (m0 + (xok[g] ? list[16 * g + c] : 0)) * K + 16 * q;
+            xr[g] = x + (int64_t)(xok[g] ? list[16 * g + c] : 0) * K + 16 * q;
             aok[g] = 16 * g + c < cols;
             ar[g] = wa + ((int64_t)a * R + rbase + (aok[g] ? 16 * g + c : 0)) * K + 16 * q;
         }
@@ -132,10 +186,326 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(const uint16_t* __restr
                 float sum = red[0][r][col];
 #pragma unroll
                 for (int w = 1; w < NW; ++w) sum += red[w][r][col];
-                v[((int64_t)plane * M + m0 + list[16 * g + r]) * R + rbase + col] = col < cols ? sc * sum : 0.0f;
+                v[((int64_t)plane * M + list[16 * g + r]) * R + rbase + col] = col < cols ? sc * sum : 0.0f;
             }
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// Rows by adapter. One work-group counts, scans and places; the rows of one
+// adapter come in no particular order (a row's result does not depend on its
+// place). Where at least 16 lanes of a wave share an adapter, as in runs of
+// rows, one of them counts for all: an LDS atomic takes one address at a time.
+constexpr int ST = 1024;
+
+template <bool PLACE>
+__device__ __forceinline__ int count_id(int* bins, int bin, bool on) {
+    const uint64_t act = __builtin_amdgcn_ballot_w64(on);
+    if (!act) return 0;
+    const int lane = threadIdx.x & 63;
+    const int lead = __builtin_ctzll(act);
+    const int b0 = __builtin_amdgcn_readlane(bin, lead);
+    const uint64_t same = __builtin_amdgcn_ballot_w64(on && bin == b0);
+    const int n = __builtin_popcountll(same);
+    int pos = 0;
+    if (n >= 16) {
+        int base = 0;
+        if (lane == lead) base = atomicAdd(&bins[b0], n);
+        base = __builtin_amdgcn_readlane(base, lead);
+        if (bin == b0) pos = base + __builtin_popcountll(same & ((1ull << lane) - 1));
+        else if (on) pos = atomicAdd(&bins[bin], 1);
+    } else if (on) {
+        pos = atomicAdd(&bins[bin], 1);
+    }
+    return pos;
+}
+
+__global__ __launch_bounds__(ST) void lora_sort_kernel(const int32_t* __restrict__ ids, int M, int L,
+                                                       int32_t* __restrict__ perm, int32_t* __restrict__ sid,
+                                                       const uint8_t* __restrict__ aq,
+                                                       const uint8_t* __restrict__ asf, int64_t K,
+                                                       uint8_t* __restrict__ ah) {
+    const int tid = threadIdx.x;
+    if (blockIdx.x > 0) {                  // the launch's other work-groups: A's exact f16 values
+        const uint32_t groups = (uint32_t)(K / 16), ldh = (uint32_t)pitch_h(K), total = (uint32_t)M * groups;
+        for (uint32_t b = (blockIdx.x - 1) * ST + tid; b < total; b += (gridDim.x - 1) * ST) {
+            const uint32_t r = b / groups, g = b - r * groups;
+            const u32x2 w = *reinterpret_cast<const u32x2*>(aq + (int64_t)b * 8);
+            store_block_f16(ah + r * ldh + g * 32, w[0], w[1], asf[b]);
+            if (g == groups - 1)
+                for (uint32_t j = groups * 32; j < ldh; j += 16)
+                    *reinterpret_cast<u32x4*>(ah + r * ldh + j) = (u32x4){0u, 0u, 0u, 0u};
+        }
+        return;
+    }
+    __shared__ int bins[kLoraMaxAdapters + 1];       // the last used one: rows without an adapter
+    __shared__ int wave_sum[ST / 64];
+    for (int i = tid; i <= L; i += ST) bins[i] = 0;
+    __syncthreads();
+    auto bin_of = [&](int i) {
+        const int id = ids[i];
+        return id >= 0 && id < L ? id : L;
+    };
+    const int rounds = (M + ST - 1) / ST;
+    for (int k = 0; k < rounds; ++k) {
+        const int i = k * ST + tid;
+        count_id<false>(bins, i < M ? bin_of(i) : -1, i < M);
+    }
+    __syncthreads();
+    // exclusive scan: each thread its share of consecutive bins
+    const int share = (L + 1 + ST - 1) / ST, lo = min(tid * share, L + 1), hi = min(lo + share, L + 1);
+    int sum = 0;
+    for (int i = lo; i < hi; ++i) sum += bins[i];
+    int incl = sum;
+    for (int off = 1; off < 64; off <<= 1) {
+        const int up = __shfl_up(incl, off, 64);
+        if ((tid & 63) >= off) incl += up;
+    }
+    if ((tid & 63) == 63) wave_sum[tid >> 6] = incl;
+    __syncthreads();
+    int base = incl - sum;
+    for (int w = 0; w < (tid >> 6); ++w) base += wave_sum[w];
+    for (int i = lo; i < hi; ++i) {
+        const int n = bins[i];
+        bins[i] = base;
+        base += n;
+    }
+    __syncthreads();
+    for (int k = 0; k < rounds; ++k) {
+        const int i = k * ST + tid;
+        const int bin = i < M ? bin_of(i) : -1;
+        const int pos = count_id<true>(bins, bin, i < M);
+        if (i < M) {
+            perm[pos] = i;
+            sid[pos] = bin < L ? bin : -1;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Expand into LDS: delta[r][n] = (v B_a^T) of row r of a tile of up to 64
+// rows and 16 CB columns from n0. The tile's adapters are dealt to the nw
+// waves; each gathers its adapter's rows (a row has one adapter, so one wave
+// writes it; the caller has zeroed delta). `lane`'s row of the tile has adapter
+// id (-1: none) and is row row_of of v.
+template <int CB, int LD>
+__device__ __forceinline__ void expand_tile(const LoraParams& p, int id, int row_of, int64_t n0, int wave, int nw,
+                                            float (*delta)[LD]) {
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+    uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
+    for (int d = 0; todo; ++d) {
+        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        const uint64_t rows = __builtin_amdgcn_ballot_w64(id == a);
+        todo &= ~rows;
+        if (d % nw != wave) continue;
+        const int rank = p.rank ? min(max(p.rank[a], 0), p.R) : p.R;
+        const int n = __builtin_popcountll(rows);
+        // lane i receives the tile row of the adapter's i-th row: the lanes
+        // that have the adapter push theirs (the others to lane 63 upwards
+        // never read: i < n below)
+        const int to = id == a ? __builtin_popcountll(rows & ((1ull << lane) - 1)) : n + __builtin_popcountll(~rows & ((1ull << lane) - 1));
+        const int tile_row = __builtin_amdgcn_ds_permute(4 * to, lane);
+        const int v_row = __builtin_amdgcn_ds_permute(4 * to, row_of);
+        for (int g = 0; g < n; g += 16) {
+            const int64_t row = __shfl(v_row, g + c, 64);
+            float4_t acc[CB];
+#pragma unroll
+            for (int f = 0; f < CB; ++f) acc[f] = (float4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+            for (int k0 = 0; k0 < rank; k0 += 32) {
+                const int k = k0 + 8 * q;
+                u32x4 hi, low;
+                lora_v_operand(p, g + c < n && k < rank, row, k, hi, low);
+#pragma unroll
+                for (int f = 0; f < CB; ++f) {
+                    const int64_t col = n0 + 16 * f + c;
+                    const bf16x8_t b = __builtin_bit_cast(bf16x8_t, lora_b_operand(p, col < p.N, a, col, k, rank));
+                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi), b, acc[f], 0, 0, 0);
+                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low), b, acc[f], 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = __shfl(tile_row, g + 4 * q + i, 64);
+                if (g + 4 * q + i < n)
+#pragma unroll
+                    for (int f = 0; f < CB; ++f) delta[r][16 * f + c] = acc[f][i];
+            }
+        }
+    }
+}
+
+// K chunks: out = bf16(alpha * (their sum, in order) + adapters), for one tile
+// of 64 listed rows and 32 columns.
+constexpr int RT = 256;
+__global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles, const float* __restrict__ partial,
+                                                         int ksplit, const float* __restrict__ a_gs,
+                                                         const float* __restrict__ b_alpha,
+                                                         uint16_t* __restrict__ out) {
+    constexpr int LD = 36;
+    __shared__ __attribute__((aligned(16))) float delta[kLoraRows][LD];
+    __shared__ int rows[kLoraRows];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t m0 = (int64_t)(blockIdx.x % tiles) * kLoraRows, n0 = (int64_t)(blockIdx.x / tiles) * 32;
+    for (int i = tid; i < kLoraRows * LD; i += RT) (&delta[0][0])[i] = 0.0f;
+    const bool in = m0 + lane < p.M;
+    const int id = in ? p.ids[m0 + lane] : -1;
+    const int row_of = in ? p.perm[m0 + lane] : -1;
+    if (wave == 0) rows[lane] = row_of;
+    // each thread: four columns of rows tid / 8 and tid / 8 + 32
+    __syncthreads();
+    const int col = 4 * (tid & 7);
+    float4_t sum[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int row = rows[(tid >> 3) + 32 * t];
+        sum[t] = (float4_t){0.f, 0.f, 0.f, 0.f};
+        if (row < 0 || n0 + col >= p.N) continue;
+        const float* src = partial + (int64_t)row * p.N + n0 + col;
+        sum[t] = *reinterpret_cast<const float4_t*>(src);
+#pragma unroll 8
+        for (int k = 1; k < ksplit; ++k) sum[t] += *reinterpret_cast<const float4_t*>(src + (int64_t)k * p.M * p.N);
+    }
+    expand_tile<2, LD>(p, id, row_of, n0, wave, RT / 64, delta);
+    __syncthreads();
+    const float alpha = a_gs[0] * b_alpha[0];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int r = (tid >> 3) + 32 * t, row = rows[r];
+        if (row < 0 || n0 + col >= p.N) continue;
+        float o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = alpha * sum[t][e] + delta[r][col + e];
+        *reinterpret_cast<u32x2*>(out + (int64_t)row * p.N + n0 + col) =
+            (u32x2){pack_bf16x2_rne(o[0], o[1]), pack_bf16x2_rne(o[2], o[3])};
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Up to 32 rows: the projection as a weight stream. A work-group owns 16 CB
+// columns and all rows; its waves share K in whole groups of four 128-element
+// steps, so every wave has a kilobyte per step and column block in flight, and
+// nothing of the projection goes through memory again: the waves' sums meet
+// in LDS (added in wave order), where the expand's are too.
+template <int MT, int CB>
+__global__ __launch_bounds__(NT) void lora_stream_kernel(LoraParams p, int per, const uint8_t* __restrict__ aqp,
+                                                         const uint8_t* __restrict__ asfp,
+                                                         const uint8_t* __restrict__ bq,
+                                                         const uint8_t* __restrict__ bsf,
+                                                         const float* __restrict__ a_gs,
+                                                         const float* __restrict__ b_alpha,
+                                                         uint16_t* __restrict__ out) {
+    constexpr int LD = 16 * CB + 4;
+    __shared__ __attribute__((aligned(16))) float delta[16 * MT][LD];
+    __shared__ __attribute__((aligned(16))) float red[NW][16 * MT][LD];
+    const int tid = threadIdx.x, lane = tid & 63, nthreads = blockDim.x, nw = nthreads / 64;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int64_t ldq = pitch_q(p.K), ldwsf = pitch_wsf(p.K);
+    const int steps = (int)(ldq / 64), quads = (int)(ldwsf / 32);
+    const int64_t blk0 = (int64_t)blockIdx.x * CB;              // 16-column blocks
+    const int64_t blocks = p.N / 16;
+
+    struct Group {
+        u32x4 w[CB][4], a[MT][4];
+        u32x2 ws[CB], as[MT];
+    };
+    auto load = [&](int g, Group& r) {
+#pragma unroll
+        for (int f = 0; f < CB; ++f) {
+            const int64_t blk = blk0 + f < blocks ? blk0 + f : blocks - 1;
+            r.ws[f] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(bsf + blk * 16 * ldwsf + (int64_t)g * kWsfQuad + c * 32 + q * 8));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int st = min(4 * g + u, steps - 1);       // beyond the last step the scales are zero
+                r.w[f][u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
+                    bq + blk * 16 * ldq + (int64_t)st * kWqStep + (q >> 1) * kWqHalf + c * 32 + (q & 1) * 16));
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            r.as[m] = *reinterpret_cast<const u32x2*>(asfp + (int64_t)m * 16 * ldwsf + (int64_t)g * 512 + c * 32 + q * 8);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int st = min(4 * g + u, steps - 1);
+                r.a[m][u] = *reinterpret_cast<const u32x4*>(aqp + ((int64_t)m * steps + st) * 1024 + lane * 16);
+            }
+        }
+    };
+    float4_t acc[MT][CB];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int f = 0; f < CB; ++f) acc[m][f] = (float4_t){0.f, 0.f, 0.f, 0.f};
+    // dword s of a step's 16 bytes: K values 32 q + 8 s .. + 7 in both operands,
+    // in scale group 2 q + s / 2
+    auto compute = [&](const Group& r) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int sh = 16 * (u & 1) + 8 * (s >> 1);
+                half8_t ha[MT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) ha[m] = dequant8(r.a[m][u][s], scale_pair((r.as[m][u >> 1] >> sh) & 0xFFu));
+#pragma unroll
+                for (int f = 0; f < CB; ++f) {
+                    const half8_t hb = dequant8(r.w[f][u][s], scale_pair((r.ws[f][u >> 1] >> sh) & 0xFFu));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ha[m], hb, acc[m][f], 0, 0, 0);
+                }
+            }
+    };
+    const int g0 = wave * per, g1 = min(quads, g0 + per);
+    Group cur;
+    if (g0 < g1) load(g0, cur);
+    __builtin_amdgcn_sched_barrier(0);
+
+    // the adapters while the first weights are on their way
+    for (int i = tid; i < 16 * MT * LD; i += nthreads) (&delta[0][0])[i] = 0.0f;
+    int id = lane < p.M ? p.ids[lane] : -1;
+    if (id >= p.L) id = -1;
+    __syncthreads();
+    expand_tile<CB, LD>(p, id, lane, blk0 * 16, wave, nw, delta);
+
+    for (int g = g0; g < g1; ++g) {
+        Group next;
+        if (g + 1 < g1) load(g + 1, next);
+        compute(cur);
+        cur = next;
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int f = 0; f < CB; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) red[wave][16 * m + 4 * q + i][16 * f + c] = acc[m][f][i];
+    __syncthreads();
+    const float alpha = a_gs[0] * b_alpha[0];
+    for (int e = tid; e < 16 * MT * 8 * CB; e += nthreads) {
+        const int r = e / (8 * CB), n = 2 * (e % (8 * CB));
+        const int64_t col = blk0 * 16 + n;
+        if (r >= p.M || col >= p.N) continue;
+        float s0 = red[0][r][n], s1 = red[0][r][n + 1];
+        for (int w = 1; w < nw; ++w) {
+            s0 += red[w][r][n];
+            s1 += red[w][r][n + 1];
+        }
+        *reinterpret_cast<uint32_t*>(out + (int64_t)r * p.N + col) =
+            pack_bf16x2_rne(alpha * s0 + delta[r][n], alpha * s1 + delta[r][n + 1]);
+    }
+}
+
+template <int MT, int CB>
+hipError_t launch_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t* asfp, const uint8_t* bq,
+                         const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out, hipStream_t s) {
+    const int quads = (int)(pitch_wsf(p.K) / 32), per = (quads + NW - 1) / NW, nw = (quads + per - 1) / per;
+    const int64_t grid = (p.N / 16 + CB - 1) / CB;
+    lora_stream_kernel<MT, CB><<<(unsigned)grid, 64 * nw, 0, s>>>(p, per, aqp, asfp, bq, bsf, a_gs, b_alpha, out);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -157,15 +527,40 @@ int lora_planes(int64_t M, int64_t K, int64_t L, int64_t R) {
     return (int)((nb + per - 1) / per);
 }
 
-hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const float* scale, const int32_t* ids,
-                              const int32_t* rank, int64_t M, int64_t K, int64_t L, int64_t R, int planes, float* v,
-                              hipStream_t s) {
-    const int64_t tiles = (M + kLoraRows - 1) / kLoraRows, rbs = (R + kRankBlock - 1) / kRankBlock;
-    int64_t slots = M < L ? M : L;
-    if (slots > kSlots) slots = kSlots;
-    const dim3 grid((unsigned)tiles, (unsigned)slots, (unsigned)(planes * rbs));
-    lora_shrink_kernel<<<grid, NT, 0, s>>>(x, a, scale, ids, rank, M, K, (int)L, (int)R, planes, v);
+hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int64_t L, int32_t* perm, int32_t* sid, const uint8_t* aq,
+                            const uint8_t* asf, int64_t K, uint16_t* ah, hipStream_t s) {
+    int64_t g = (M * (K / 16) + ST - 1) / ST;
+    if (g > 2048) g = 2048;
+    lora_sort_kernel<<<(unsigned)(1 + g), ST, 0, s>>>(ids, (int)M, (int)L, perm, sid, aq, asf, K,
+                                                      reinterpret_cast<uint8_t*>(ah));
     return hipGetLastError();
+}
+
+hipError_t launch_lora_shrink(const LoraParams& p, const uint8_t* aq, const uint8_t* asf, uint8_t* aqp, uint8_t* asfp,
+                              hipStream_t s) {
+    const int64_t tiles = (p.M + kLoraRows - 1) / kLoraRows, rbs = (p.R + kRankBlock - 1) / kRankBlock;
+    int64_t slots = p.M < p.L ? p.M : p.L;
+    if (slots > kSlots) slots = kSlots;
+    const int64_t blocks = tiles * slots * p.planes * rbs;
+    const int64_t more = aqp ? (lora_stream_aq_bytes(p.M, p.K) / 16 + lora_stream_asf_bytes(p.M, p.K) / 8 + NT - 1) / NT : 0;
+    lora_shrink_kernel<<<(unsigned)(blocks + more), NT, 0, s>>>(p, (int)tiles, (int)slots, (int)blocks, aq, asf, aqp,
+                                                               asfp);
+    return hipGetLastError();
+}
+
+hipError_t launch_lora_reduce(const LoraParams& p, const float* partial, int ksplit, const float* a_gs,
+                              const float* b_alpha, uint16_t* out, hipStream_t s) {
+    const int64_t tiles = (p.M + kLoraRows - 1) / kLoraRows;
+    lora_reduce_kernel<<<(unsigned)(tiles * ((p.N + 31) / 32)), RT, 0, s>>>(p, (int)tiles, partial, ksplit, a_gs, b_alpha,
+                                                                            out);
+    return hipGetLastError();
+}
+
+hipError_t launch_lora_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t* asfp, const uint8_t* bq,
+                              const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out,
+                              hipStream_t s) {
+    if (p.M <= 16) return launch_stream<1, 1>(p, aqp, asfp, bq, bsf, a_gs, b_alpha, out, s);
+    return launch_stream<2, 2>(p, aqp, asfp, bq, bsf, a_gs, b_alpha, out, s);
 }
 
 }  // namespace nvfp4

@@ -84,7 +84,8 @@ def check(s, out):
     (16, 512, 1040, 4, 16), (17, 256, 512, 17, 32), (33, 784, 272, 5, 72), (61, 1536, 1024, 32, 32),
     (64, 512, 4096, 64, 128), (65, 528, 512, 65, 16), (128, 512, 256, 3, 256), (129, 1040, 528, 9, 40),
     (256, 768, 640, 6, 16), (300, 512, 256, 20, 64), (513, 6144, 512, 2, 16), (1300, 6144, 144, 7, 136),
-    (4093, 4096, 128, 300, 8)])
+    (4093, 4096, 128, 300, 8), (31, 1040, 2064, 9, 24), (32, 16, 7168, 2, 256), (8, 528, 144, 8, 64),
+    (16, 1296, 12304, 3, 8), (700, 1024, 2048, 48, 32), (5000, 256, 128, 8192, 8)])
 def test_random_ids(nv, M, N, K, L, R):
     import torch
     s = make(nv, M, N, K, L, R, M + N + K + L + R)

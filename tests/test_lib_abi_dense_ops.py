@@ -27,7 +27,7 @@ def test_gemm_lora_argument_errors(lib):
 
     assert call(M=0) == 0
     assert call(M=-1) == 1 and call(N=0) == 1 and call(L=0) == 1 and call(R=0) == 1 and call(K=-16) == 1
-    assert call(N=24) == 2 and call(K=24) == 2 and call(R=12) == 2 and call(R=264) == 2 and call(L=65536) == 2
+    assert call(N=24) == 2 and call(K=24) == 2 and call(R=12) == 2 and call(R=264) == 2 and call(L=8193) == 2
     assert call(M=1 << 23, K=16) == 2 and call(M=1 << 20, K=1 << 13) == 2
     for name in ("aq", "asf", "a_gs", "bq", "bsf", "b_alpha", "x", "lora_a", "lora_b", "scale", "ids"):
         assert call(**{name: 0}) == 1, name
@@ -36,10 +36,10 @@ def test_gemm_lora_argument_errors(lib):
         assert call(**{name: A16 + off}) == 1, name
     assert call(out=A16 + 4) == 1 and call(out=0) == 1
     need = ws(4, 32, 64, 2, 8)
-    assert need > lib.nvfp4_gemm_workspace(4, 32, 64) and call(nbytes=need - 1) == 3
+    assert need > 0 and call(nbytes=need - 1) == 3
     assert call(wsp=0) == 3 and call(wsp=A16 + 64) == 3
     assert ws(4, 24, 64, 2, 8) == 0 and ws(4, 32, 64, 2, 4) == 0 and ws(-1, 32, 64, 2, 8) == 0
-    # the shrunk rows come on top of nvfp4_gemm's workspace
+    # a tiled batch: the shrunk rows come on top of nvfp4_gemm's workspace
     assert ws(4096, 6144, 7168, 8, 64) >= lib.nvfp4_gemm_workspace(4096, 6144, 7168) + 4096 * 64 * 4
 
 
