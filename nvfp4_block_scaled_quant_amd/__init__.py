@@ -408,12 +408,6 @@ def moe_forward_noalloc(x, topk_ids, topk_weights, w13, w13_sf, w13_alpha, w2, w
     return y
 
 
-def _on(device):
-    """Makes the operands' device the current one for a call (the library
-    launches on the current device) and names its current stream."""
-    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else _NO_GUARD
-
-
 class _NoGuard:
     def __enter__(self):
         pass
@@ -423,6 +417,22 @@ class _NoGuard:
 
 
 _NO_GUARD = _NoGuard()
+
+
+def _on(index):
+    """Makes the operands' device the current one for a call (the library
+    launches on the current device)."""
+    return _NO_GUARD if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+
+
+def _operand(t, dtype, shape, name, dev):
+    """Address of an operand of exactly this dtype, shape and device (the
+    messages are _need's)."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev
+            or not t.is_contiguous()):
+        _need(t, dtype, name, len(shape), dev)
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, adapter_ids,
@@ -436,48 +446,49 @@ def gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, ad
     lora_rank[a] ranks."""
     _need(x, torch.bfloat16, "x", 2)
     dev = x.device
-    for t, n, d, nd in ((aq, "aq", torch.uint8, 2), (asf, "asf", torch.uint8, 2),
-                        (bq, "bq", torch.uint8, 4), (bsf, "bsf", torch.uint8, 4),
-                        (a_gs, "a_gs", torch.float32, None), (b_alpha, "b_alpha", torch.float32, None),
-                        (lora_a, "lora_a", torch.bfloat16, 3), (lora_b, "lora_b", torch.bfloat16, 3),
-                        (lora_scale, "lora_scale", torch.float32, 1),
-                        (adapter_ids, "adapter_ids", torch.int32, 1)):
-        _need(t, d, n, nd, dev)
+    _need(bq, torch.uint8, "bq", 4, dev)
+    _need(lora_a, torch.bfloat16, "lora_a", 3, dev)
+    _need(a_gs, torch.float32, "a_gs", None, dev)
+    _need(b_alpha, torch.float32, "b_alpha", None, dev)
     if a_gs.numel() < 1 or b_alpha.numel() < 1:
         raise ValueError("gemm_lora: a_gs and b_alpha must hold one float32 each")
     M, K = x.shape
-    N = bq.shape[0] * 16
-    L, R = lora_a.shape[0], lora_a.shape[1]
+    blocks = bq.shape[0]
+    N = blocks * 16
+    L, R, _ = lora_a.shape
     if K % 16 or K == 0 or N == 0:
         raise ValueError("gemm_lora: K must be a positive multiple of 16 and N positive")
     if R % 8 or not 8 <= R <= 256 or not 1 <= L <= 8192:
         raise ValueError("gemm_lora: R must be a multiple of 8 from 8 to 256, and L from 1 to 8192")
-    shq, shs = packed_shapes(1, K, N)
-    if (aq.shape != (M, K // 2) or asf.shape != (M, K // 16) or tuple(bq.shape) != shq[1:]
-            or tuple(bsf.shape) != shs[1:] or lora_a.shape != (L, R, K) or lora_b.shape != (L, N, R)
-            or lora_scale.shape != (L,) or adapter_ids.shape != (M,)):
-        raise ValueError("gemm_lora: operand shapes do not match")
-    if lora_rank is not None:
-        _need(lora_rank, torch.int32, "lora_rank", 1, dev)
-        if lora_rank.shape != (L,):
-            raise ValueError("gemm_lora: lora_rank must have shape (L,)")
-    with _on(dev):
-        out = _out(out, (M, N), torch.bfloat16, dev, "out")
+    steps = (K + 127) // 128                                # packed_shapes
+    u8, bf16 = torch.uint8, torch.bfloat16
+    ptrs = (_operand(aq, u8, (M, K // 2), "aq", dev), _operand(asf, u8, (M, K // 16), "asf", dev),
+            a_gs.data_ptr(), _operand(bq, u8, (blocks, 2 * steps, 16, 32), "bq", dev),
+            _operand(bsf, u8, (blocks, (steps + 3) // 4, 16, 32), "bsf", dev), b_alpha.data_ptr(),
+            x.data_ptr(), _operand(lora_a, bf16, (L, R, K), "lora_a", dev),
+            _operand(lora_b, bf16, (L, N, R), "lora_b", dev),
+            _operand(lora_scale, torch.float32, (L,), "lora_scale", dev),
+            None if lora_rank is None else _operand(lora_rank, torch.int32, (L,), "lora_rank", dev),
+            _operand(adapter_ids, torch.int32, (M,), "adapter_ids", dev))
+    with _on(dev.index):
+        out = _out(out, (M, N), bf16, dev, "out")
         ws = _workspace(workspace, _lib.nvfp4_gemm_lora_workspace(M, N, K, L, R), dev)
-        _check(_lib.nvfp4_gemm_lora(
-            _ptr(aq), _ptr(asf), _ptr(a_gs), _ptr(bq), _ptr(bsf), _ptr(b_alpha), _ptr(x), _ptr(lora_a),
-            _ptr(lora_b), _ptr(lora_scale), _ptr(lora_rank), _ptr(adapter_ids), M, N, K, L, R, _ptr(out),
-            _ptr(ws), _nbytes(ws), _stream()), "nvfp4_gemm_lora")
+        _check(_lib.nvfp4_gemm_lora(*ptrs, M, N, K, L, R, out.data_ptr(), ws.data_ptr(), _nbytes(ws),
+                                    torch._C._cuda_getCurrentRawStream(dev.index)), "nvfp4_gemm_lora")
     return out
 
 
-def _gated_sizes(x, w13, dev):
-    if w13.shape[0] != x.shape[1] or w13.shape[1] % 2:
-        raise ValueError(f"w13 must be (H, 2I) with H = {x.shape[1]}, got {tuple(w13.shape)}")
-    H, I = x.shape[1], w13.shape[1] // 2
+def _gated_sizes(x, w13):
+    """T, H, I of a gated block's x (T, H) and w13 (H, 2I)."""
+    _need(x, torch.bfloat16, "x", 2)
+    _need(w13, torch.bfloat16, "w13", 2, x.device)
+    T, H = x.shape
+    if w13.shape[0] != H or w13.shape[1] % 2:
+        raise ValueError(f"w13 must be (H, 2I) with H = {H}, got {tuple(w13.shape)}")
+    I = w13.shape[1] // 2
     if H % 16 or I % 16 or H == 0 or I == 0:
         raise ValueError("gated: H and I must be positive multiples of 16")
-    return x.shape[0], H, I
+    return T, H, I
 
 
 def gated_forward(x, w13, act=None, gate_up=None, workspace=None):
@@ -485,17 +496,15 @@ def gated_forward(x, w13, act=None, gate_up=None, workspace=None):
     (T, H), w13 bf16 (H, 2I) = [gate | up] -> act bf16 (T, I). gate_up: None,
     or a bf16 (T, 2I) tensor that receives the rounded gate | up values that
     gated_backward takes."""
-    _need(x, torch.bfloat16, "x", 2)
+    T, H, I = _gated_sizes(x, w13)
     dev = x.device
-    _need(w13, torch.bfloat16, "w13", 2, dev)
-    T, H, I = _gated_sizes(x, w13, dev)
-    with _on(dev):
+    gu = None if gate_up is None else _operand(gate_up, torch.bfloat16, (T, 2 * I), "gate_up", dev)
+    with _on(dev.index):
         act = _out(act, (T, I), torch.bfloat16, dev, "act")
-        if gate_up is not None:
-            _out(gate_up, (T, 2 * I), torch.bfloat16, dev, "gate_up")
         ws = _workspace(workspace, _lib.nvfp4_gated_workspace(T, H, I), dev)
-        _check(_lib.nvfp4_gated_forward(_ptr(x), _ptr(w13), T, H, I, _ptr(act), _ptr(gate_up),
-                                        _ptr(ws), _nbytes(ws), _stream()), "nvfp4_gated_forward")
+        _check(_lib.nvfp4_gated_forward(x.data_ptr(), w13.data_ptr(), T, H, I, act.data_ptr(), gu, ws.data_ptr(),
+                                        _nbytes(ws), torch._C._cuda_getCurrentRawStream(dev.index)),
+               "nvfp4_gated_forward")
     return act
 
 
@@ -504,26 +513,23 @@ def gated_backward(d_act, x, w13, gate_up, dx=None, dw13=None, need_dx=True, nee
     """Gradients of gated_forward: d_act bf16 (T, I), the forward's x, w13 and
     gate_up -> (dx bf16 (T, H), dw13 bf16 (H, 2I)). need_dx / need_dw13 =
     False skips that product and returns None in its place."""
-    _need(x, torch.bfloat16, "x", 2)
-    dev = x.device
-    _need(w13, torch.bfloat16, "w13", 2, dev)
-    T, H, I = _gated_sizes(x, w13, dev)
-    _need(d_act, torch.bfloat16, "d_act", 2, dev)
-    _need(gate_up, torch.bfloat16, "gate_up", 2, dev)
-    if d_act.shape != (T, I) or gate_up.shape != (T, 2 * I):
-        raise ValueError("gated_backward: inconsistent shapes")
+    T, H, I = _gated_sizes(x, w13)
+    dev, bf16 = x.device, torch.bfloat16
+    d_ptr = _operand(d_act, bf16, (T, I), "d_act", dev)
+    gu_ptr = _operand(gate_up, bf16, (T, 2 * I), "gate_up", dev)
     if not (need_dx or need_dw13):
         raise ValueError("gated_backward: nothing to compute")
     if (dx is not None and not need_dx) or (dw13 is not None and not need_dw13):
         raise ValueError("gated_backward: an output is given for a gradient that is not computed")
-    with _on(dev):
+    with _on(dev.index):
         if need_dx:
-            dx = _out(dx, (T, H), torch.bfloat16, dev, "dx")
+            dx = _out(dx, (T, H), bf16, dev, "dx")
         if need_dw13:
-            dw13 = _out(dw13, (H, 2 * I), torch.bfloat16, dev, "dw13")
+            dw13 = _out(dw13, (H, 2 * I), bf16, dev, "dw13")
         ws = _workspace(workspace, _lib.nvfp4_gated_backward_workspace(T, H, I), dev)
-        _check(_lib.nvfp4_gated_backward(_ptr(d_act), _ptr(x), _ptr(w13), _ptr(gate_up), T, H, I,
-                                         _ptr(dx), _ptr(dw13), _ptr(ws), _nbytes(ws), _stream()),
+        _check(_lib.nvfp4_gated_backward(d_ptr, x.data_ptr(), w13.data_ptr(), gu_ptr, T, H, I,
+                                         dx.data_ptr() if need_dx else None, dw13.data_ptr() if need_dw13 else None,
+                                         ws.data_ptr(), _nbytes(ws), torch._C._cuda_getCurrentRawStream(dev.index)),
                "nvfp4_gated_backward")
     return dx, dw13
 

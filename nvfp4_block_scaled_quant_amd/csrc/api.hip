@@ -607,19 +607,23 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
     lo.L = (int)L;
     lo.R = (int)R;
     if (lora_streams(M)) {
-        NVFP4_TRY(launch_lora_shrink(lo, aq, asf, ws + w.aqp, ws + w.asfp, stream));
+        NVFP4_TRY(launch_lora_shrink(lo, aq, asf, ws + w.aqp, ws + w.asfp, nullptr, stream));
         NVFP4_TRY(launch_lora_stream(lo, ws + w.aqp, ws + w.asfp, bq, bsf, a_gs, b_alpha, out, stream));
         return NVFP4_OK;
     }
     uint16_t* ah = reinterpret_cast<uint16_t*>(ws + w.gemm);
     int32_t* perm = reinterpret_cast<int32_t*>(ws + w.perm);
     int32_t* sid = reinterpret_cast<int32_t*>(ws + w.sid);
-    NVFP4_TRY(launch_lora_sort(adapter_ids, M, L, perm, sid, aq, asf, K, ah, stream));
-    lo.perm = perm;
-    lo.ids = sid;
-    NVFP4_TRY(launch_lora_shrink(lo, nullptr, nullptr, nullptr, nullptr, stream));
     GemmParams p = {};
     p.ksplit = dense_ksplit(M, N, K);
+    if (lora_sorts(M) || p.ksplit == 1) {
+        NVFP4_TRY(launch_lora_sort(adapter_ids, M, L, perm, sid, aq, asf, K, ah, stream));
+        lo.perm = perm;
+        lo.ids = sid;
+        NVFP4_TRY(launch_lora_shrink(lo, nullptr, nullptr, nullptr, nullptr, nullptr, stream));
+    } else {
+        NVFP4_TRY(launch_lora_shrink(lo, aq, asf, nullptr, nullptr, ah, stream));
+    }
     p.mode = p.ksplit > 1 ? kGemmDense : kGemmLora;
     p.ah = ah;
     p.M = M;
@@ -633,6 +637,7 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
     p.out_bf16 = out;
     p.partial = reinterpret_cast<float*>(ws + w.gemm + gemm_ws_partial_offset(M, K));
     p.lora = lo;
+    p.full_tiles = gemm_full_tiles(M, (N + kGemmBN - 1) / kGemmBN, 256, 0.58);
     NVFP4_TRY(launch_gemm(p, stream));
     if (p.ksplit > 1) NVFP4_TRY(launch_lora_reduce(lo, p.partial, p.ksplit, a_gs, b_alpha, out, stream));
     return NVFP4_OK;

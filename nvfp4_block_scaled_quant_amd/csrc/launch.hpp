@@ -200,6 +200,9 @@ constexpr int64_t kLoraMaxRank = 256;
 constexpr int64_t kLoraMaxAdapters = 8192;
 constexpr int kLoraRows = 64;     // rows of a tile of the adapters' kernels
 constexpr int kLoraStreamRows = 32;
+// Whether the rows are listed by adapter first: a batch of one tile of the
+// adapters' kernels gathers them as it finds them.
+inline bool lora_sorts(int64_t M) { return M > kLoraRows; }
 // Whether M rows take the weight-streaming kernel (then A is laid out by
 // launch_lora_shrink) or the tiled GEMM.
 inline bool lora_streams(int64_t M) { return M <= kLoraStreamRows; }
@@ -213,9 +216,10 @@ int lora_planes(int64_t M, int64_t K, int64_t L, int64_t R);
 // A's exact f16 form (launch_dequant_rows_f16).
 hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int64_t L, int32_t* perm, int32_t* sid, const uint8_t* aq,
                             const uint8_t* asf, int64_t K, uint16_t* ah, hipStream_t s);
-// p.v; with aqp not null also A in the streaming kernel's layout.
+// p.v; beside it, with aqp not null, A in the streaming kernel's layout, or with
+// ah not null A's exact f16 form.
 hipError_t launch_lora_shrink(const LoraParams& p, const uint8_t* aq, const uint8_t* asf, uint8_t* aqp, uint8_t* asfp,
-                              hipStream_t s);
+                              uint16_t* ah, hipStream_t s);
 // out = bf16(alpha * sum over chunks of partial[c] (M, N) + adapters)
 hipError_t launch_lora_reduce(const LoraParams& p, const float* partial, int ksplit, const float* a_gs,
                               const float* b_alpha, uint16_t* out, hipStream_t s);
@@ -263,6 +267,7 @@ struct GemmParams {
     // kGemmLora: the dense GEMM over the rows grouped by adapter, whose
     // epilogue adds the adapters (one K chunk)
     LoraParams lora;
+    int64_t full_tiles;        // kGemmLora: row tiles of 256 rows (the rest: 128)
 };
 
 hipError_t launch_gemm(const GemmParams& p, hipStream_t s);
@@ -279,6 +284,11 @@ __host__ __device__ inline int64_t dense_tile_rows(int64_t M, int64_t N) {
     const int64_t t256 = (M + kGemmBM - 1) / kGemmBM * ((N + kGemmBN - 1) / kGemmBN);
     return t256 < 128 ? kGemmBM / 2 : kGemmBM;
 }
+
+// Number of 256-row tiles of a GEMM of M rows and ntn column tiles, the rest
+// of the rows in 128-row tiles at `half` of a full tile's time, that ends
+// first when `cus` CUs take the full tiles and then the half ones.
+int64_t gemm_full_tiles(int64_t M, int64_t ntn, int64_t cus, double half);
 
 // out[m][n] = bf16((a_gs[0] * b_alpha[0]) * sum over chunks c, in order, of
 // partial[c][m][n]) for (M, N), N % 4 == 0.

@@ -33,8 +33,29 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int NT = 512;
 constexpr int NW = NT / 64;
+constexpr uint32_t kRsrcWord3 = 0x00020000u;
+constexpr int kStreamNT = 2;        // buffer-load cache policy: non-temporal (read once)
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, kRsrcWord3);
+}
+
 constexpr int kRankBlock = 64;      // ranks of a work-group (4 column blocks of 16)
-constexpr int kSlots = 16;          // work-groups that share a tile's adapters
+
+// A's exact f16 values, rows padded with zeros to whole steps (32-bit indices:
+// M * pitch_h(K) is below 2^31).
+__device__ void dequant_a(const uint8_t* __restrict__ aq, const uint8_t* __restrict__ asf, int64_t M, int64_t K,
+                          uint8_t* __restrict__ ah, uint32_t first, uint32_t stride) {
+    const uint32_t groups = (uint32_t)(K / 16), ldh = (uint32_t)pitch_h(K), total = (uint32_t)M * groups;
+    for (uint32_t b = first; b < total; b += stride) {
+        const uint32_t r = b / groups, g = b - r * groups;
+        const u32x2 w = *reinterpret_cast<const u32x2*>(aq + (int64_t)b * 8);
+        store_block_f16(ah + r * ldh + g * 32, w[0], w[1], asf[b]);
+        if (g == groups - 1)
+            for (uint32_t j = groups * 32; j < ldh; j += 16)
+                *reinterpret_cast<u32x4*>(ah + r * ldh + j) = (u32x4){0u, 0u, 0u, 0u};
+    }
+}
 
 // A in the streaming kernel's layout, zero beyond M and K: data per 16-row
 // block and 128-element step as one kilobyte (lane l = 16 q + c holds bytes
@@ -74,10 +95,11 @@ __device__ void lay_out_a(const LoraParams& p, const uint8_t* __restrict__ aq, c
 __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles, int slots, int shrink_blocks,
                                                          const uint8_t* __restrict__ aq,
                                                          const uint8_t* __restrict__ asf, uint8_t* __restrict__ aqp,
-                                                         uint8_t* __restrict__ asfp) {
+                                                         uint8_t* __restrict__ asfp, uint8_t* __restrict__ ah) {
     if ((int)blockIdx.x >= shrink_blocks) {          // the launch's further work-groups: A's layout
-        lay_out_a(p, aq, asf, aqp, asfp, (int64_t)(blockIdx.x - shrink_blocks) * NT + threadIdx.x,
-                  (int64_t)(gridDim.x - shrink_blocks) * NT);
+        const uint32_t first = (blockIdx.x - shrink_blocks) * NT + threadIdx.x, stride = (gridDim.x - shrink_blocks) * NT;
+        if (ah) dequant_a(aq, asf, p.M, p.K, ah, first, stride);
+        else lay_out_a(p, aq, asf, aqp, asfp, first, stride);
         return;
     }
     __shared__ int list[kLoraRows];
@@ -199,7 +221,6 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
 // rows, one of them counts for all: an LDS atomic takes one address at a time.
 constexpr int ST = 1024;
 
-template <bool PLACE>
 __device__ __forceinline__ int count_id(int* bins, int bin, bool on) {
     const uint64_t act = __builtin_amdgcn_ballot_w64(on);
     if (!act) return 0;
@@ -228,15 +249,7 @@ __global__ __launch_bounds__(ST) void lora_sort_kernel(const int32_t* __restrict
                                                        uint8_t* __restrict__ ah) {
     const int tid = threadIdx.x;
     if (blockIdx.x > 0) {                  // the launch's other work-groups: A's exact f16 values
-        const uint32_t groups = (uint32_t)(K / 16), ldh = (uint32_t)pitch_h(K), total = (uint32_t)M * groups;
-        for (uint32_t b = (blockIdx.x - 1) * ST + tid; b < total; b += (gridDim.x - 1) * ST) {
-            const uint32_t r = b / groups, g = b - r * groups;
-            const u32x2 w = *reinterpret_cast<const u32x2*>(aq + (int64_t)b * 8);
-            store_block_f16(ah + r * ldh + g * 32, w[0], w[1], asf[b]);
-            if (g == groups - 1)
-                for (uint32_t j = groups * 32; j < ldh; j += 16)
-                    *reinterpret_cast<u32x4*>(ah + r * ldh + j) = (u32x4){0u, 0u, 0u, 0u};
-        }
+        dequant_a(aq, asf, M, K, ah, (blockIdx.x - 1) * ST + tid, (gridDim.x - 1) * ST);
         return;
     }
     __shared__ int bins[kLoraMaxAdapters + 1];       // the last used one: rows without an adapter
@@ -250,7 +263,7 @@ __global__ __launch_bounds__(ST) void lora_sort_kernel(const int32_t* __restrict
     const int rounds = (M + ST - 1) / ST;
     for (int k = 0; k < rounds; ++k) {
         const int i = k * ST + tid;
-        count_id<false>(bins, i < M ? bin_of(i) : -1, i < M);
+        count_id(bins, i < M ? bin_of(i) : -1, i < M);
     }
     __syncthreads();
     // exclusive scan: each thread its share of consecutive bins
@@ -275,7 +288,7 @@ __global__ __launch_bounds__(ST) void lora_sort_kernel(const int32_t* __restrict
     for (int k = 0; k < rounds; ++k) {
         const int i = k * ST + tid;
         const int bin = i < M ? bin_of(i) : -1;
-        const int pos = count_id<true>(bins, bin, i < M);
+        const int pos = count_id(bins, bin, i < M);
         if (i < M) {
             perm[pos] = i;
             sid[pos] = bin < L ? bin : -1;
@@ -285,44 +298,54 @@ __global__ __launch_bounds__(ST) void lora_sort_kernel(const int32_t* __restrict
 
 // ---------------------------------------------------------------------------
 // Expand into LDS: delta[r][n] = (v B_a^T) of row r of a tile of up to 64
-// rows and 16 CB columns from n0. The tile's adapters are dealt to the nw
-// waves; each gathers its adapter's rows (a row has one adapter, so one wave
-// writes it; the caller has zeroed delta). `lane`'s row of the tile has adapter
-// id (-1: none) and is row row_of of v.
+// rows and 16 CB columns from n0. The tile's (adapter, 16 of its rows) pairs
+// are dealt to the nw waves (a row has one adapter, so one wave writes it; the
+// caller has zeroed delta). `lane`'s row of the tile has adapter id (-1: none)
+// and is row row_of of v.
 template <int CB, int LD>
 __device__ __forceinline__ void expand_tile(const LoraParams& p, int id, int row_of, int64_t n0, int wave, int nw,
                                             float (*delta)[LD]) {
     const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
     uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
-    for (int d = 0; todo; ++d) {
+    int turn = 0;                       // number of the adapter's first pair
+    while (todo) {
         const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
         const uint64_t rows = __builtin_amdgcn_ballot_w64(id == a);
         todo &= ~rows;
-        if (d % nw != wave) continue;
-        const int rank = p.rank ? min(max(p.rank[a], 0), p.R) : p.R;
         const int n = __builtin_popcountll(rows);
-        // lane i receives the tile row of the adapter's i-th row: the lanes
-        // that have the adapter push theirs (the others to lane 63 upwards
-        // never read: i < n below)
-        const int to = id == a ? __builtin_popcountll(rows & ((1ull << lane) - 1)) : n + __builtin_popcountll(~rows & ((1ull << lane) - 1));
+        const int first = turn;
+        turn += (n + 15) / 16;
+        // this wave's pairs among first .. turn - 1
+        int pair = first + (wave - first % nw + nw) % nw;
+        if (pair >= turn) continue;
+        const int rank = p.rank ? min(max(p.rank[a], 0), p.R) : p.R;
+        // lane i receives the adapter's i-th row: the lanes that have it push
+        // theirs to 0 .. n - 1, the others to the rest
+        const uint64_t below = (1ull << lane) - 1;
+        const int to = id == a ? __builtin_popcountll(rows & below) : n + __builtin_popcountll(~rows & below);
         const int tile_row = __builtin_amdgcn_ds_permute(4 * to, lane);
         const int v_row = __builtin_amdgcn_ds_permute(4 * to, row_of);
-        for (int g = 0; g < n; g += 16) {
+        for (; pair < turn; pair += nw) {
+            const int g = 16 * (pair - first);
             const int64_t row = __shfl(v_row, g + c, 64);
             float4_t acc[CB];
 #pragma unroll
             for (int f = 0; f < CB; ++f) acc[f] = (float4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
+#pragma unroll 1
             for (int k0 = 0; k0 < rank; k0 += 32) {
                 const int k = k0 + 8 * q;
-                u32x4 hi, low;
-                lora_v_operand(p, g + c < n && k < rank, row, k, hi, low);
+                u32x4 b[CB], hi, low;
 #pragma unroll
                 for (int f = 0; f < CB; ++f) {
                     const int64_t col = n0 + 16 * f + c;
-                    const bf16x8_t b = __builtin_bit_cast(bf16x8_t, lora_b_operand(p, col < p.N, a, col, k, rank));
-                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi), b, acc[f], 0, 0, 0);
-                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low), b, acc[f], 0, 0, 0);
+                    b[f] = lora_b_operand(p, col < p.N, a, col, k, rank);
+                }
+                lora_v_operand(p, g + c < n && k < rank, row, k, hi, low);
+#pragma unroll
+                for (int f = 0; f < CB; ++f) {
+                    const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, b[f]);
+                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi), bf, acc[f], 0, 0, 0);
+                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low), bf, acc[f], 0, 0, 0);
                 }
             }
 #pragma unroll
@@ -338,48 +361,44 @@ __device__ __forceinline__ void expand_tile(const LoraParams& p, int id, int row
 
 // K chunks: out = bf16(alpha * (their sum, in order) + adapters), for one tile
 // of 64 listed rows and 32 columns.
-constexpr int RT = 256;
+constexpr int RT = 1024;
 __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles, const float* __restrict__ partial,
                                                          int ksplit, const float* __restrict__ a_gs,
                                                          const float* __restrict__ b_alpha,
                                                          uint16_t* __restrict__ out) {
     constexpr int LD = 36;
     __shared__ __attribute__((aligned(16))) float delta[kLoraRows][LD];
-    __shared__ int rows[kLoraRows];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t m0 = (int64_t)(blockIdx.x % tiles) * kLoraRows, n0 = (int64_t)(blockIdx.x / tiles) * 32;
     for (int i = tid; i < kLoraRows * LD; i += RT) (&delta[0][0])[i] = 0.0f;
     const bool in = m0 + lane < p.M;
-    const int id = in ? p.ids[m0 + lane] : -1;
-    const int row_of = in ? p.perm[m0 + lane] : -1;
-    if (wave == 0) rows[lane] = row_of;
-    // each thread: four columns of rows tid / 8 and tid / 8 + 32
-    __syncthreads();
-    const int col = 4 * (tid & 7);
-    float4_t sum[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int row = rows[(tid >> 3) + 32 * t];
-        sum[t] = (float4_t){0.f, 0.f, 0.f, 0.f};
-        if (row < 0 || n0 + col >= p.N) continue;
+    int id = in ? p.ids[m0 + lane] : -1;
+    if (id >= p.L) id = -1;
+    const int row_of = in ? (p.perm ? p.perm[m0 + lane] : (int)(m0 + lane)) : -1;
+    // each thread: two columns of tile row tid / 16
+    const int col = 2 * (tid & 15), r = tid >> 4;
+    const int row = __shfl(row_of, r, 64);
+    const bool mine = row >= 0 && n0 + col < p.N;
+    float s0 = 0.0f, s1 = 0.0f;
+    if (mine) {
+        typedef float float2_t __attribute__((ext_vector_type(2)));
         const float* src = partial + (int64_t)row * p.N + n0 + col;
-        sum[t] = *reinterpret_cast<const float4_t*>(src);
+        const int64_t plane = p.M * p.N;
 #pragma unroll 8
-        for (int k = 1; k < ksplit; ++k) sum[t] += *reinterpret_cast<const float4_t*>(src + (int64_t)k * p.M * p.N);
+        for (int k = 0; k < ksplit; ++k) {
+            const float2_t v = *reinterpret_cast<const float2_t*>(src + k * plane);
+            s0 += v[0];
+            s1 += v[1];
+        }
     }
+    __syncthreads();
     expand_tile<2, LD>(p, id, row_of, n0, wave, RT / 64, delta);
     __syncthreads();
-    const float alpha = a_gs[0] * b_alpha[0];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int r = (tid >> 3) + 32 * t, row = rows[r];
-        if (row < 0 || n0 + col >= p.N) continue;
-        float o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = alpha * sum[t][e] + delta[r][col + e];
-        *reinterpret_cast<u32x2*>(out + (int64_t)row * p.N + n0 + col) =
-            (u32x2){pack_bf16x2_rne(o[0], o[1]), pack_bf16x2_rne(o[2], o[3])};
+    if (mine) {
+        const float alpha = a_gs[0] * b_alpha[0];
+        *reinterpret_cast<uint32_t*>(out + (int64_t)row * p.N + n0 + col) =
+            pack_bf16x2_rne(alpha * s0 + delta[r][col], alpha * s1 + delta[r][col + 1]);
     }
 }
 
@@ -390,7 +409,8 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
 // nothing of the projection goes through memory again: the waves' sums meet
 // in LDS (added in wave order), where the expand's are too.
 template <int MT, int CB>
-__global__ __launch_bounds__(NT) void lora_stream_kernel(LoraParams p, int per, const uint8_t* __restrict__ aqp,
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : 2)))
+void lora_stream_kernel(LoraParams p, int per, const uint8_t* __restrict__ aqp,
                                                          const uint8_t* __restrict__ asfp,
                                                          const uint8_t* __restrict__ bq,
                                                          const uint8_t* __restrict__ bsf,
@@ -412,25 +432,30 @@ __global__ __launch_bounds__(NT) void lora_stream_kernel(LoraParams p, int per, 
         u32x4 w[CB][4], a[MT][4];
         u32x2 ws[CB], as[MT];
     };
-    auto load = [&](int g, Group& r) {
+    // buffer loads: one lane offset per operand, the rest in scalar offsets
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(bq, p.N * ldq), rws = make_rsrc(bsf, p.N * ldwsf);
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(aqp, (int64_t)16 * MT * ldq), ras = make_rsrc(asfp, (int64_t)16 * MT * ldwsf);
+    const uint32_t w_off = (q >> 1) * kWqHalf + c * 32 + (q & 1) * 16, sf_off = c * 32 + q * 8, a_off = lane * 16;
+    auto load_w = [&](int g, Group& r) {
 #pragma unroll
         for (int f = 0; f < CB; ++f) {
-            const int64_t blk = blk0 + f < blocks ? blk0 + f : blocks - 1;
-            r.ws[f] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(bsf + blk * 16 * ldwsf + (int64_t)g * kWsfQuad + c * 32 + q * 8));
+            const uint32_t blk = (uint32_t)(blk0 + f < blocks ? blk0 + f : blocks - 1);
+            r.ws[f] = __builtin_amdgcn_raw_buffer_load_b64(rws, sf_off, blk * 16 * (uint32_t)ldwsf + (uint32_t)g * kWsfQuad, kStreamNT);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int st = min(4 * g + u, steps - 1);       // beyond the last step the scales are zero
-                r.w[f][u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
-                    bq + blk * 16 * ldq + (int64_t)st * kWqStep + (q >> 1) * kWqHalf + c * 32 + (q & 1) * 16));
+                r.w[f][u] = __builtin_amdgcn_raw_buffer_load_b128(rw, w_off, blk * 16 * (uint32_t)ldq + (uint32_t)st * kWqStep, kStreamNT);
             }
         }
+    };
+    auto load_a = [&](int g, Group& r) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            r.as[m] = *reinterpret_cast<const u32x2*>(asfp + (int64_t)m * 16 * ldwsf + (int64_t)g * 512 + c * 32 + q * 8);
+            r.as[m] = __builtin_amdgcn_raw_buffer_load_b64(ras, sf_off, (uint32_t)(m * quads + g) * 512, 0);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int st = min(4 * g + u, steps - 1);
-                r.a[m][u] = *reinterpret_cast<const u32x4*>(aqp + ((int64_t)m * steps + st) * 1024 + lane * 16);
+                r.a[m][u] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_off, (uint32_t)(m * steps + st) * 1024, 0);
             }
         }
     };
@@ -459,9 +484,12 @@ __global__ __launch_bounds__(NT) void lora_stream_kernel(LoraParams p, int per, 
                 }
             }
     };
+    // two groups in flight (an index past the wave's last group loads it
+    // again); A, which every work-group reads, follows from the L2
     const int g0 = wave * per, g1 = min(quads, g0 + per);
-    Group cur;
-    if (g0 < g1) load(g0, cur);
+    Group r0, r1;
+    load_w(g0, r0);
+    load_w(min(g0 + 1, g1 - 1), r1);
     __builtin_amdgcn_sched_barrier(0);
 
     // the adapters while the first weights are on their way
@@ -471,12 +499,19 @@ __global__ __launch_bounds__(NT) void lora_stream_kernel(LoraParams p, int per, 
     __syncthreads();
     expand_tile<CB, LD>(p, id, lane, blk0 * 16, wave, nw, delta);
 
-    for (int g = g0; g < g1; ++g) {
-        Group next;
-        if (g + 1 < g1) load(g + 1, next);
-        compute(cur);
-        cur = next;
+    int g = g0;
+    load_a(g0, r0);
+    load_a(min(g0 + 1, g1 - 1), r1);
+    for (; g + 2 < g1; g += 2) {
+        compute(r0);
+        load_w(g + 2, r0);
+        load_a(g + 2, r0);
+        compute(r1);
+        load_w(min(g + 3, g1 - 1), r1);
+        load_a(min(g + 3, g1 - 1), r1);
     }
+    compute(r0);
+    if (g + 1 < g1) compute(r1);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -537,14 +572,18 @@ hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int64_t L, int32_t* p
 }
 
 hipError_t launch_lora_shrink(const LoraParams& p, const uint8_t* aq, const uint8_t* asf, uint8_t* aqp, uint8_t* asfp,
-                              hipStream_t s) {
+                              uint16_t* ah, hipStream_t s) {
     const int64_t tiles = (p.M + kLoraRows - 1) / kLoraRows, rbs = (p.R + kRankBlock - 1) / kRankBlock;
+    // work-groups that share a tile's adapters: as many as it can hold when it
+    // is the only tile; listed rows put few adapters into a tile
     int64_t slots = p.M < p.L ? p.M : p.L;
-    if (slots > kSlots) slots = kSlots;
+    if (slots > (tiles > 1 ? 8 : kLoraRows)) slots = tiles > 1 ? 8 : kLoraRows;
     const int64_t blocks = tiles * slots * p.planes * rbs;
-    const int64_t more = aqp ? (lora_stream_aq_bytes(p.M, p.K) / 16 + lora_stream_asf_bytes(p.M, p.K) / 8 + NT - 1) / NT : 0;
+    const int64_t more = aqp  ? (lora_stream_aq_bytes(p.M, p.K) / 16 + lora_stream_asf_bytes(p.M, p.K) / 8 + NT - 1) / NT
+                         : ah ? (p.M * (p.K / 16) + NT - 1) / NT
+                              : 0;
     lora_shrink_kernel<<<(unsigned)(blocks + more), NT, 0, s>>>(p, (int)tiles, (int)slots, (int)blocks, aq, asf, aqp,
-                                                               asfp);
+                                                               asfp, reinterpret_cast<uint8_t*>(ah));
     return hipGetLastError();
 }
 
