@@ -546,21 +546,26 @@ namespace {
 // the shrunk rows, then A for streaming, or the tiled GEMM's workspace
 // and the rows' order
 struct LoraLayout {
-    size_t v, aqp, asfp, gemm, perm, sid, total;
+    size_t v, aqp, asfp, gemm, perm, sid, vs, total;
+    int ksplit, planes;        // ksplit 1: the expand is in the GEMM's epilogue, from vs
 };
 
 LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     LoraLayout w = {};
     const int64_t m = M > 0 ? M : 1;
-    w.aqp = align_up((size_t)lora_planes(m, K, L, R) * (size_t)m * (size_t)R * 4);
-    if (lora_streams(m)) {
+    const bool stream = lora_streams(m);
+    w.ksplit = dense_ksplit(m, N, K);
+    w.planes = lora_planes(m, K, L, R);
+    w.aqp = align_up((size_t)w.planes * (size_t)m * (size_t)R * 4);
+    if (stream) {
         w.asfp = w.aqp + align_up((size_t)lora_stream_aq_bytes(m, K));
         w.total = w.asfp + align_up((size_t)lora_stream_asf_bytes(m, K));
     } else {
         w.gemm = w.aqp;
         w.perm = w.gemm + align_up(nvfp4_gemm_workspace(m, N, K));
         w.sid = w.perm + align_up((size_t)m * 4);
-        w.total = w.sid + align_up((size_t)m * 4);
+        w.vs = w.sid + align_up((size_t)m * 4);
+        w.total = w.vs + (w.ksplit == 1 ? align_up((size_t)m * (size_t)R * 4) : 0);
     }
     return w;
 }
@@ -597,7 +602,7 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
     lo.a = lora_a;
     lo.scale = lora_scale;
     lo.v = reinterpret_cast<float*>(ws + w.v);
-    lo.planes = lora_planes(M, K, L, R);
+    lo.planes = w.planes;
     lo.b = lora_b;
     lo.ids = adapter_ids;
     lo.rank = lora_rank;
@@ -607,23 +612,34 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
     lo.L = (int)L;
     lo.R = (int)R;
     if (lora_streams(M)) {
-        NVFP4_TRY(launch_lora_shrink(lo, aq, asf, ws + w.aqp, ws + w.asfp, nullptr, stream));
+        NVFP4_TRY(launch_lora_shrink(lo, kLoraAsIs, nullptr, nullptr, aq, asf, ws + w.aqp, ws + w.asfp, nullptr, stream));
         NVFP4_TRY(launch_lora_stream(lo, ws + w.aqp, ws + w.asfp, bq, bsf, a_gs, b_alpha, out, stream));
         return NVFP4_OK;
     }
     uint16_t* ah = reinterpret_cast<uint16_t*>(ws + w.gemm);
     int32_t* perm = reinterpret_cast<int32_t*>(ws + w.perm);
     int32_t* sid = reinterpret_cast<int32_t*>(ws + w.sid);
-    GemmParams p = {};
-    p.ksplit = dense_ksplit(M, N, K);
-    if (lora_sorts(M) || p.ksplit == 1) {
-        NVFP4_TRY(launch_lora_sort(adapter_ids, M, L, perm, sid, aq, asf, K, ah, stream));
+    LoraOrder order = lora_order(M);
+    const bool fused = w.ksplit == 1;
+    if (fused) {
+        lo.vs = reinterpret_cast<uint16_t*>(ws + w.vs);
+        if (order == kLoraAsIs) order = kLoraRank;      // the fused epilogue takes listed rows
+    }
+    if (order == kLoraSort) {
+        NVFP4_TRY(launch_lora_sort(adapter_ids, M, L, perm, sid, stream));
         lo.perm = perm;
         lo.ids = sid;
-        NVFP4_TRY(launch_lora_shrink(lo, nullptr, nullptr, nullptr, nullptr, nullptr, stream));
-    } else {
-        NVFP4_TRY(launch_lora_shrink(lo, aq, asf, nullptr, nullptr, ah, stream));
     }
+    // A's f16 form beside the shrink; a fused expand has the joining launch for
+    // it, whose many small work-groups suit it better
+    NVFP4_TRY(launch_lora_shrink(lo, order, perm, sid, aq, asf, nullptr, nullptr, fused ? nullptr : ah, stream));
+    if (order == kLoraRank) {
+        lo.perm = perm;
+        lo.ids = sid;
+    }
+    if (fused) NVFP4_TRY(launch_lora_join(lo, aq, asf, ah, stream));
+    GemmParams p = {};
+    p.ksplit = w.ksplit;
     p.mode = p.ksplit > 1 ? kGemmDense : kGemmLora;
     p.ah = ah;
     p.M = M;

@@ -299,6 +299,24 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
     return v;
 }
 
+// Sum of n values of type V, `stride` V apart, in order. Up to B loads are in
+// flight before the first is added (a plain loop over few values would wait
+// for each).
+template <int B, typename V>
+__device__ __forceinline__ V sum_planes(const V* __restrict__ src, int n, int64_t stride) {
+    V sum = src[0];
+    for (int c0 = 1; c0 < n; c0 += B) {
+        V v[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (c0 + j < n) v[j] = src[(c0 + j) * stride];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if (c0 + j < n) sum += v[j];
+    }
+    return sum;
+}
+
 // Byte transpose of a 4x4 block held in 4 words: in r[i] byte j = M[i][j];
 // out c[j] byte i = M[i][j].
 __device__ __forceinline__ void transpose4x4(const uint32_t (&r)[4], uint32_t (&c)[4]) {

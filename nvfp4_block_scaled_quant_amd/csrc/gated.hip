@@ -405,13 +405,8 @@ __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedGemm p) {
     const int64_t I4 = p.I / 4, n = p.M * I4, plane = p.M * 2 * p.I;
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
         const int64_t row = t / I4, col = 4 * (t - row * I4);
-        const float* src = p.partial + row * 2 * p.I + col;
-        float4_t g = *reinterpret_cast<const float4_t*>(src), u = *reinterpret_cast<const float4_t*>(src + p.I);
-#pragma unroll 8
-        for (int c = 1; c < p.ksplit; ++c) {
-            g += *reinterpret_cast<const float4_t*>(src + c * plane);
-            u += *reinterpret_cast<const float4_t*>(src + c * plane + p.I);
-        }
+        const float4_t* src = reinterpret_cast<const float4_t*>(p.partial + row * 2 * p.I + col);
+        const float4_t g = sum_planes<8>(src, p.ksplit, plane / 4), u = sum_planes<8>(src + I4, p.ksplit, plane / 4);
         float a[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) a[k] = silu_mul(g[k], u[k]);
@@ -429,10 +424,7 @@ __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedGemm p) {
 __global__ __launch_bounds__(256) void gated_sum_kernel(const float* __restrict__ partial, int ksplit, int64_t n4,
                                                         uint16_t* __restrict__ out) {
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n4; t += (int64_t)gridDim.x * 256) {
-        const float4_t* src = reinterpret_cast<const float4_t*>(partial) + t;
-        float4_t v = src[0];
-#pragma unroll 8
-        for (int c = 1; c < ksplit; ++c) v += src[c * n4];
+        const float4_t v = sum_planes<8>(reinterpret_cast<const float4_t*>(partial) + t, ksplit, n4);
         *reinterpret_cast<u32x2*>(out + 4 * t) = (u32x2){pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
     }
 }

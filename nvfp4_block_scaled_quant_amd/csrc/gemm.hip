@@ -605,42 +605,72 @@ void gemm_kernel(GemmParams p) {
             // (the rows are grouped by adapter: one or two), added to the rows
             // that have the adapter (the others' results are dropped by a
             // select, not multiplied by zero: a NaN of one adapter reaches no
-            // other row). v is float32 and enters as the sum of two bf16
-            // values (2^-17 relative), B_a is bf16.
+            // other row). v enters as the sum of two bf16 values, B_a is bf16.
+            // The operands come straight from memory (L2), 32 ranks at a time
+            // in flight: with one work-group per CU nothing else hides their
+            // latency.
             typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
             const LoraParams& lo = p.lora;
+            const int m4 = l32 & 3;
+            const bool odd = (m4 & 1) != 0, upper = (m4 & 2) != 0;
+            auto swap1 = [](float x) {      // quad_perm(1,0,3,2)
+                return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0xB1, 0xF, 0xF, false));
+            };
+            auto swap2 = [](float x) {      // quad_perm(2,3,0,1)
+                return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x4E, 0xF, 0xF, false));
+            };
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
+                const int local = wm * (32 * MI) + 32 * i + l32;
+                const bool in = local < row_count;
+                const int64_t pos = (int64_t)row_start + (in ? local : 0);
+                const int id = in ? lo.ids[pos] : -1;
+                int dst_row[4];                 // rows this lane stores, after the quad transposes below
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int lr = wm * (32 * MI) + 32 * i + 8 * g + 4 * h + m4;
+                    dst_row[g] = lr < row_count ? lo.perm[(int64_t)row_start + lr] : -1;
+                }
+                uint32_t todo = (uint32_t)__builtin_amdgcn_ballot_w64(id >= 0);   // lanes l, l + 32 hold one row
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[i][j][r] *= alpha;
-                const int local = wm * (32 * MI) + 32 * i + l32;
-                const bool in = local < row_count;
-                const int id = in ? lo.ids[(int64_t)row_start + local] : -1;
-                const int64_t row = in ? lo.perm[(int64_t)row_start + local] : 0;
-                uint32_t todo = (uint32_t)__builtin_amdgcn_ballot_w64(id >= 0);   // lanes l, l + 32 hold one row
                 while (todo) {
                     const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
                     const uint32_t rows = (uint32_t)__builtin_amdgcn_ballot_w64(id == a);
                     todo &= ~rows;
                     const int rank = lo.rank ? min(max(lo.rank[a], 0), lo.R) : lo.R;
+                    const uint16_t* vrow = lo.vs + pos * 2 * lo.R;
                     float16_t d[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int r = 0; r < 16; ++r) d[j][r] = 0.0f;
-                    for (int r0 = 0; r0 < rank; r0 += 16) {
-                        const int k = r0 + 8 * h;              // this lane's 8 ranks (R % 8 == 0: k + 8 <= R)
-                        u32x4 hi, lw;
-                        lora_v_operand(lo, id == a && k < rank, row, k, hi, lw);
+                    for (int r0 = 0; r0 < rank; r0 += 32) {
+                        u32x4 hi[2], lw[2], b[2][2];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + l32;
-                            const bf16x8_t fbv = __builtin_bit_cast(bf16x8_t, lora_b_operand(lo, col < N, a, col, k, rank));
-                            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, hi), fbv, d[j], 0, 0, 0);
-                            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, lw), fbv, d[j], 0, 0, 0);
+                        for (int t = 0; t < 2; ++t) {
+                            const int k = r0 + 16 * t + 8 * h;     // this lane's 8 ranks (R % 8 == 0: k + 8 <= R)
+                            hi[t] = lw[t] = (u32x4){0u, 0u, 0u, 0u};
+                            if (id == a && k < rank) {
+                                hi[t] = *reinterpret_cast<const u32x4*>(vrow + k);
+                                lw[t] = *reinterpret_cast<const u32x4*>(vrow + lo.R + k);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + l32;
+                                b[t][j] = lora_b_operand(lo, col < N, a, col, k, rank);
+                            }
                         }
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const bf16x8_t fbv = __builtin_bit_cast(bf16x8_t, b[t][j]);
+                                d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, hi[t]), fbv, d[j], 0, 0, 0);
+                                d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, lw[t]), fbv, d[j], 0, 0, 0);
+                            }
                     }
                     const uint32_t mine = rows >> (4 * h);     // bit 8 (r / 4) + r % 4: this lane's row r
 #pragma unroll
@@ -650,17 +680,23 @@ void gemm_kernel(GemmParams p) {
                         for (int j = 0; j < 2; ++j) acc[i][j][r] += take ? d[j][r] : 0.0f;
                     }
                 }
+                // 4 x 4 transposes inside each quad of lanes, as in store_f32:
+                // lane 4 c + m then has columns 4 c .. 4 c + 3 of row m of each
+                // group of four, one 8-byte store
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int lr = wm * (32 * MI) + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-                    if (lr >= row_count) continue;
-                    uint16_t* dst = p.out_bf16 + (int64_t)lo.perm[(int64_t)row_start + lr] * N;
+                for (int g = 0; g < 4; ++g)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + l32;
-                        if (col < N) dst[col] = (uint16_t)f32_to_bf16_rne(acc[i][j][r]);
+                        float v0 = acc[i][j][4 * g], v1 = acc[i][j][4 * g + 1], v2 = acc[i][j][4 * g + 2], v3 = acc[i][j][4 * g + 3];
+                        const float a0 = swap1(odd ? v0 : v1), a1 = swap1(odd ? v2 : v3);
+                        if (odd) { v0 = a0; v2 = a1; } else { v1 = a0; v3 = a1; }
+                        const float b0 = swap2(upper ? v0 : v2), b1 = swap2(upper ? v1 : v3);
+                        if (upper) { v0 = b0; v1 = b1; } else { v2 = b0; v3 = b1; }
+                        const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + 4 * (l32 >> 2);
+                        if (dst_row[g] >= 0 && col < N)
+                            *reinterpret_cast<u32x2*>(p.out_bf16 + (int64_t)dst_row[g] * N + col) =
+                                (u32x2){pack_bf16x2_rne(v0, v1), pack_bf16x2_rne(v2, v3)};
                     }
-                }
             }
         } else if (p.ksplit > 1) {
             store_f32(p.partial + (int64_t)chunk * p.M * N, 1.0f);

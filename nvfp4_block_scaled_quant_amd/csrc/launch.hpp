@@ -177,10 +177,11 @@ hipError_t launch_combine(const float* o2, const int32_t* slot_row, const float*
 
 enum GemmMode { kGemmDense = 0, kGemmL1 = 1, kGemmL2 = 2, kGemmLora = 3 };
 
-// Low-rank adapters of the rows of a dense GEMM (lora.hip). v holds the
-// shrunk rows scale[a] * x A_a^T as `planes` partial sums (planes, M, R)
-// float32, written only for rows that have an adapter and zero from the
-// adapter's rank on; b (L, N, R) bf16. perm / ids list the rows grouped by
+// Low-rank adapters of the rows of a dense GEMM (lora.hip). The shrunk rows
+// scale[a] * x A_a^T are written only for rows that have an adapter and are
+// zero from the adapter's rank on: v, `planes` partial sums (planes, M, R) in
+// float32, and for the fused epilogue vs (M, 2R) bf16 in the listed order: the
+// rounding of each sum, then the rounding of what is left (2^-17 together). b is (L, N, R) bf16. perm / ids list the rows grouped by
 // adapter: row perm[i] has adapter ids[i] (-1: none); perm null: the rows in
 // order, and ids (M) the caller's (outside [0, L): none).
 struct LoraParams {
@@ -188,6 +189,7 @@ struct LoraParams {
     const uint16_t* a;         // (L, R, K)
     const float* scale;        // (L)
     float* v;
+    uint16_t* vs;
     int planes;
     const uint16_t* b;
     const int32_t* perm;
@@ -200,9 +202,12 @@ constexpr int64_t kLoraMaxRank = 256;
 constexpr int64_t kLoraMaxAdapters = 8192;
 constexpr int kLoraRows = 64;     // rows of a tile of the adapters' kernels
 constexpr int kLoraStreamRows = 32;
-// Whether the rows are listed by adapter first: a batch of one tile of the
-// adapters' kernels gathers them as it finds them.
-inline bool lora_sorts(int64_t M) { return M > kLoraRows; }
+// How the rows are listed by adapter: a batch of one tile of the adapters'
+// kernels not at all (a tile gathers its rows), a small one by the shrink's own
+// work-groups, larger ones by a launch of its own.
+enum LoraOrder { kLoraAsIs = 0, kLoraRank = 1, kLoraSort = 2 };
+constexpr int kLoraRankRows = 256;
+inline LoraOrder lora_order(int64_t M) { return M <= kLoraRows ? kLoraAsIs : M <= kLoraRankRows ? kLoraRank : kLoraSort; }
 // Whether M rows take the weight-streaming kernel (then A is laid out by
 // launch_lora_shrink) or the tiled GEMM.
 inline bool lora_streams(int64_t M) { return M <= kLoraStreamRows; }
@@ -210,16 +215,17 @@ inline bool lora_streams(int64_t M) { return M <= kLoraStreamRows; }
 // groups of four steps for the scales
 inline int64_t lora_stream_aq_bytes(int64_t M, int64_t K) { return (M + 15) / 16 * 16 * pitch_q(K); }
 inline int64_t lora_stream_asf_bytes(int64_t M, int64_t K) { return (M + 15) / 16 * 16 * pitch_wsf(K); }
-// number of partial sums (K ranges) of the shrink
+// number of partial sums (K ranges) of the shrink into v
 int lora_planes(int64_t M, int64_t K, int64_t L, int64_t R);
-// Rows by adapter: perm (M), sid (M) from the caller's ids; and, beside it,
-// A's exact f16 form (launch_dequant_rows_f16).
-hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int64_t L, int32_t* perm, int32_t* sid, const uint8_t* aq,
-                            const uint8_t* asf, int64_t K, uint16_t* ah, hipStream_t s);
-// p.v; beside it, with aqp not null, A in the streaming kernel's layout, or with
-// ah not null A's exact f16 form.
-hipError_t launch_lora_shrink(const LoraParams& p, const uint8_t* aq, const uint8_t* asf, uint8_t* aqp, uint8_t* asfp,
-                              uint16_t* ah, hipStream_t s);
+// perm (M), sid (M) from the caller's ids (kLoraSort)
+hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int64_t L, int32_t* perm, int32_t* sid, hipStream_t s);
+// p.v. order kLoraRank: also perm and sid (p.ids are the caller's, and
+// p.perm is not read). Beside it, with aqp not null, A in the streaming
+// kernel's layout, or with ah not null A's exact f16 form.
+hipError_t launch_lora_shrink(const LoraParams& p, LoraOrder order, int32_t* perm, int32_t* sid, const uint8_t* aq,
+                              const uint8_t* asf, uint8_t* aqp, uint8_t* asfp, uint16_t* ah, hipStream_t s);
+// For the fused epilogue: p.vs from p.v, and A's exact f16 form.
+hipError_t launch_lora_join(const LoraParams& p, const uint8_t* aq, const uint8_t* asf, uint16_t* ah, hipStream_t s);
 // out = bf16(alpha * sum over chunks of partial[c] (M, N) + adapters)
 hipError_t launch_lora_reduce(const LoraParams& p, const float* partial, int ksplit, const float* a_gs,
                               const float* b_alpha, uint16_t* out, hipStream_t s);

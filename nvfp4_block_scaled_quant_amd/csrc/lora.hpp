@@ -10,29 +10,22 @@ namespace nvfp4 {
 // Eight ranks k .. k + 7 of row `row` of v as hi + lo in bf16 (zeros when not
 // `on`): v is the sum of its partial sums in order, hi its rounding and lo the
 // rounding of what is left, so hi + lo is within 2^-17 of v.
+// UNROLL partial sums are loaded at a time.
+template <int UNROLL>
 __device__ __forceinline__ void lora_v_operand(const LoraParams& lo, bool on, int64_t row, int k, u32x4& hi,
                                                u32x4& low) {
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    float4_t v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     if (on) {
-        const float* src = lo.v + row * lo.R + k;
-        const int64_t plane = lo.M * lo.R;
-#pragma unroll 4
-        for (int c = 0; c < lo.planes; ++c) {
-            const float4_t v0 = *reinterpret_cast<const float4_t*>(src + c * plane);
-            const float4_t v1 = *reinterpret_cast<const float4_t*>(src + c * plane + 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] += v0[e];
-                v[4 + e] += v1[e];
-            }
-        }
+        const float4_t* src = reinterpret_cast<const float4_t*>(lo.v + row * lo.R + k);
+        const int64_t plane = lo.M * lo.R / 4;
+        v[0] = sum_planes<UNROLL>(src, lo.planes, plane);
+        v[1] = sum_planes<UNROLL>(src + 1, lo.planes, plane);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        hi[e] = pack_bf16x2_rne(v[2 * e], v[2 * e + 1]);
-        low[e] = pack_bf16x2_rne(v[2 * e] - bf16_to_f32(hi[e] & 0xFFFFu), v[2 * e + 1] - bf16_to_f32(hi[e] >> 16));
+        const float v0 = v[e >> 1][2 * (e & 1)], v1 = v[e >> 1][2 * (e & 1) + 1];
+        hi[e] = pack_bf16x2_rne(v0, v1);
+        low[e] = pack_bf16x2_rne(v0 - bf16_to_f32(hi[e] & 0xFFFFu), v1 - bf16_to_f32(hi[e] >> 16));
     }
 }
 
