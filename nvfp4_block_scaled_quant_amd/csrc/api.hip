@@ -536,6 +536,7 @@ namespace {
 bool lora_shape_ok(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     if (M < 0 || N <= 0 || K <= 0 || L <= 0 || R <= 0 || K % 16 || N % 16 || R % 8) return false;
     if (R > kLoraMaxRank || L > kLoraMaxAdapters || M > (int64_t)1 << 22) return false;
+    if (K > (int64_t)1 << 24 || 2 * R * K >= 0x7FFFFFFF) return false;      // 32-bit offsets inside an adapter
     return M * pitch_h(K) < 0x7FFFFFFF && N * pitch_q(K) < 0x7FFFFFFF;
 }
 
@@ -619,25 +620,20 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
     uint16_t* ah = reinterpret_cast<uint16_t*>(ws + w.gemm);
     int32_t* perm = reinterpret_cast<int32_t*>(ws + w.perm);
     int32_t* sid = reinterpret_cast<int32_t*>(ws + w.sid);
-    LoraOrder order = lora_order(M);
+    const LoraOrder order = M <= kLoraRankRows ? kLoraRank : kLoraSort;
     const bool fused = w.ksplit == 1;
-    if (fused) {
-        lo.vs = reinterpret_cast<uint16_t*>(ws + w.vs);
-        if (order == kLoraAsIs) order = kLoraRank;      // the fused epilogue takes listed rows
-    }
+    if (fused) lo.vs = reinterpret_cast<uint16_t*>(ws + w.vs);
     if (order == kLoraSort) {
         NVFP4_TRY(launch_lora_sort(adapter_ids, M, L, perm, sid, stream));
         lo.perm = perm;
         lo.ids = sid;
     }
-    // A's f16 form beside the shrink; a fused expand has the joining launch for
-    // it, whose many small work-groups suit it better
-    NVFP4_TRY(launch_lora_shrink(lo, order, perm, sid, aq, asf, nullptr, nullptr, fused ? nullptr : ah, stream));
+    NVFP4_TRY(launch_lora_shrink(lo, order, perm, sid, aq, asf, nullptr, nullptr, ah, stream));
     if (order == kLoraRank) {
         lo.perm = perm;
         lo.ids = sid;
     }
-    if (fused) NVFP4_TRY(launch_lora_join(lo, aq, asf, ah, stream));
+    if (fused) NVFP4_TRY(launch_lora_join(lo, stream));
     GemmParams p = {};
     p.ksplit = w.ksplit;
     p.mode = p.ksplit > 1 ? kGemmDense : kGemmLora;

@@ -601,15 +601,19 @@ void gemm_kernel(GemmParams p) {
             store_f32(p.out_f32, alpha);
         } else if (MODE == kGemmLora) {
             // The adapters, on the matrix cores, into the same accumulators:
-            // delta = v B_a^T per 32-row block and adapter that occurs in it
-            // (the rows are grouped by adapter: one or two), added to the rows
-            // that have the adapter (the others' results are dropped by a
-            // select, not multiplied by zero: a NaN of one adapter reaches no
+            // delta = v B_a^T per adapter that occurs in the tile (the rows are
+            // grouped by adapter: one or two) and 32-row block that has it, added
+            // to the rows that have the adapter (the others' results are dropped
+            // by a select, not multiplied by zero: a NaN of one adapter reaches no
             // other row). v enters as the sum of two bf16 values, B_a is bf16.
-            // The operands come straight from memory (L2), 32 ranks at a time
-            // in flight: with one work-group per CU nothing else hides their
-            // latency.
+            // 64 ranks at a time, both go to the now idle LDS by loads that write
+            // it directly: rows of 128 bytes in the layout of the main loop's A.
+            // (Fragments straight from memory, each lane in another row than its
+            // neighbours, took about 25 us of a tile's 200.)
             typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+            constexpr uint32_t kBeyond = 0x80000000u;       // an offset that reads zeros
+            constexpr int V_LOW = BM * 128, V_B = 2 * BM * 128;   // LDS: v hi, v low, B_a
+            static_assert(V_B + BN * 128 <= LDS_BYTES, "the adapters' operands fit in LDS");
             const LoraParams& lo = p.lora;
             const int m4 = l32 & 3;
             const bool odd = (m4 & 1) != 0, upper = (m4 & 2) != 0;
@@ -619,72 +623,112 @@ void gemm_kernel(GemmParams p) {
             auto swap2 = [](float x) {      // quad_perm(2,3,0,1)
                 return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0x4E, 0xF, 0xF, false));
             };
+            // adapters of the tile's 64 MI rows, the same masks in every wave
+            int id[4];                      // (fixed sizes: see a_off)
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                const int local = wm * (32 * MI) + 32 * i + l32;
-                const bool in = local < row_count;
-                const int64_t pos = (int64_t)row_start + (in ? local : 0);
-                const int id = in ? lo.ids[pos] : -1;
-                int dst_row[4];                 // rows this lane stores, after the quad transposes below
+                const int local = 64 * i + lane;
+                id[i] = local < row_count ? lo.ids[(int64_t)row_start + local] : -1;
+            }
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int lr = wm * (32 * MI) + 32 * i + 8 * g + 4 * h + m4;
-                    dst_row[g] = lr < row_count ? lo.perm[(int64_t)row_start + lr] : -1;
-                }
-                uint32_t todo = (uint32_t)__builtin_amdgcn_ballot_w64(id >= 0);   // lanes l, l + 32 hold one row
+            for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[i][j][r] *= alpha;
-                while (todo) {
-                    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-                    const uint32_t rows = (uint32_t)__builtin_amdgcn_ballot_w64(id == a);
-                    todo &= ~rows;
-                    const int rank = lo.rank ? min(max(lo.rank[a], 0), lo.R) : lo.R;
-                    const uint16_t* vrow = lo.vs + pos * 2 * lo.R;
-                    float16_t d[2];
+            const int64_t n0 = (int64_t)nt * BN;
+            const __amdgpu_buffer_rsrc_t rv = make_rsrc(lo.vs + (int64_t)row_start * 2 * lo.R, (int64_t)row_count * 4 * lo.R);
+            const int lr = lane >> 3;       // a load covers 8 rows
+            const uint32_t frag = 16 * (h ^ ((l32 >> 1) & 7));    // chunk of rank step 0; step t: ^ 32 t
+            for (int r0 = 0; r0 < lo.R; r0 += 64) {
+                auto chunk_of = [&](int row) { return 8 * ((lane & 7) ^ ((row >> 1) & 7)); };
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) d[j][r] = 0.0f;
-                    for (int r0 = 0; r0 < rank; r0 += 32) {
-                        u32x4 hi[2], lw[2], b[2][2];
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const int k = r0 + 16 * t + 8 * h;     // this lane's 8 ranks (R % 8 == 0: k + 8 <= R)
-                            hi[t] = lw[t] = (u32x4){0u, 0u, 0u, 0u};
-                            if (id == a && k < rank) {
-                                hi[t] = *reinterpret_cast<const u32x4*>(vrow + k);
-                                lw[t] = *reinterpret_cast<const u32x4*>(vrow + lo.R + k);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + l32;
-                                b[t][j] = lora_b_operand(lo, col < N, a, col, k, rank);
-                            }
-                        }
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const bf16x8_t fbv = __builtin_bit_cast(bf16x8_t, b[t][j]);
-                                d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, hi[t]), fbv, d[j], 0, 0, 0);
-                                d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, lw[t]), fbv, d[j], 0, 0, 0);
-                            }
-                    }
-                    const uint32_t mine = rows >> (4 * h);     // bit 8 (r / 4) + r % 4: this lane's row r
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const bool take = (mine >> (8 * (r >> 2) + (r & 3))) & 1u;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) acc[i][j][r] += take ? d[j][r] : 0.0f;
-                    }
+                for (int t = 0; t < MI; ++t) {
+                    const int row = 8 * (MI * wave + t) + lr, k = r0 + chunk_of(row);
+                    const uint32_t off = row < row_count && k < lo.R ? (uint32_t)(row * 2 * lo.R + k) * 2 : kBeyond;
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void*)(smem_raw + (MI * wave + t) * 1024), 16, off, 0, 0, 0);
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void*)(smem_raw + V_LOW + (MI * wave + t) * 1024), 16, off,
+                                                             2 * lo.R, 0, 0);
                 }
-                // 4 x 4 transposes inside each quad of lanes, as in store_f32:
-                // lane 4 c + m then has columns 4 c .. 4 c + 3 of row m of each
-                // group of four, one 8-byte store
+                uint64_t todo[4];
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
+                for (int i = 0; i < MI; ++i) todo[i] = __builtin_amdgcn_ballot_w64(id[i] >= 0);
+                while (true) {
+                    int a = -1;
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+                        if (a < 0 && todo[i]) a = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo[i]));
+                    if (a < 0) break;
+                    const int rank = lo.rank ? min(max(lo.rank[a], 0), lo.R) : lo.R;
+                    const __amdgpu_buffer_rsrc_t rB = make_rsrc(lo.b + ((int64_t)a * N + n0) * lo.R,
+                                                                min((int64_t)BN, N - n0) * lo.R * 2);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int row = 8 * (4 * wave + t) + lr, k = r0 + chunk_of(row);
+                        const uint32_t off = n0 + row < N && k < rank ? (uint32_t)(row * lo.R + k) * 2 : kBeyond;
+                        __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void*)(smem_raw + V_B + (4 * wave + t) * 1024), 16, off, 0, 0, 0);
+                    }
+                    __syncthreads();
+                    // matching rows of this wave's 32-row blocks: rows wm * 32 MI + 32 i
+                    uint64_t match[4];
+#pragma unroll
+                    for (int i = 0; i < MI; ++i) {
+                        match[i] = __builtin_amdgcn_ballot_w64(id[i] == a);
+                        todo[i] &= ~match[i];
+                    }
+                    const int steps = min(4, (rank - r0 + 15) / 16);
+#pragma unroll
+                    for (int i = 0; i < MI; ++i) {
+                        const int blk = wm * MI + i;               // 32-row block of the tile
+                        uint64_t m64 = match[0];
+#pragma unroll
+                        for (int e = 1; e < MI; ++e)
+                            if (blk / 2 == e) m64 = match[e];
+                        const uint32_t rows = (uint32_t)(m64 >> (32 * (blk & 1)));
+                        if (!rows) continue;
+                        const uint8_t* vr = smem_raw + (32 * blk + l32) * 128;
+                        const uint8_t* br = smem_raw + V_B + (wn * 64 + l32) * 128;
+                        const uint32_t mine = rows >> (4 * h);     // bit 8 (r / 4) + r % 4: this lane's row r
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float16_t d;
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) d[r] = 0.0f;
+#pragma unroll 1
+                            for (int t = 0; t < steps; ++t) {
+                                const uint32_t at = frag ^ (32u * t);
+                                u32x4 b = *reinterpret_cast<const u32x4*>(br + j * 32 * 128 + at);
+                                const bf16x8_t hi = *reinterpret_cast<const bf16x8_t*>(vr + at);
+                                const bf16x8_t lw = *reinterpret_cast<const bf16x8_t*>(vr + V_LOW + at);
+                                if (rank & 7) b = lora_mask_rank(b, r0 + 16 * t + 8 * h, rank);
+                                d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, __builtin_bit_cast(bf16x8_t, b), d, 0, 0, 0);
+                                d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lw, __builtin_bit_cast(bf16x8_t, b), d, 0, 0, 0);
+                            }
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                acc[i][j][r] += (mine >> (8 * (r >> 2) + (r & 3))) & 1u ? d[r] : 0.0f;
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                    __syncthreads();            // before the next adapter's B_a or ranks
+                }
+            }
+            int dst[4][4];
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int local = wm * (32 * MI) + 32 * i + 8 * g + 4 * h + m4;
+                    dst[i][g] = local < row_count ? lo.perm[(int64_t)row_start + local] : -1;
+                }
+            // 4 x 4 transposes inside each quad of lanes, as in store_f32: lane
+            // 4 c + m then has columns 4 c .. 4 c + 3 of row m of each group of
+            // four, one 8-byte store
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int row = dst[i][g];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         float v0 = acc[i][j][4 * g], v1 = acc[i][j][4 * g + 1], v2 = acc[i][j][4 * g + 2], v3 = acc[i][j][4 * g + 3];
@@ -693,11 +737,11 @@ void gemm_kernel(GemmParams p) {
                         const float b0 = swap2(upper ? v0 : v2), b1 = swap2(upper ? v1 : v3);
                         if (upper) { v0 = b0; v1 = b1; } else { v2 = b0; v3 = b1; }
                         const int64_t col = (int64_t)nt * BN + wn * 64 + 32 * j + 4 * (l32 >> 2);
-                        if (dst_row[g] >= 0 && col < N)
-                            *reinterpret_cast<u32x2*>(p.out_bf16 + (int64_t)dst_row[g] * N + col) =
+                        if (row >= 0 && col < N)
+                            *reinterpret_cast<u32x2*>(p.out_bf16 + (int64_t)row * N + col) =
                                 (u32x2){pack_bf16x2_rne(v0, v1), pack_bf16x2_rne(v2, v3)};
                     }
-            }
+                }
         } else if (p.ksplit > 1) {
             store_f32(p.partial + (int64_t)chunk * p.M * N, 1.0f);
         } else {

@@ -201,13 +201,13 @@ struct LoraParams {
 constexpr int64_t kLoraMaxRank = 256;
 constexpr int64_t kLoraMaxAdapters = 8192;
 constexpr int kLoraRows = 64;     // rows of a tile of the adapters' kernels
-constexpr int kLoraStreamRows = 32;
-// How the rows are listed by adapter: a batch of one tile of the adapters'
-// kernels not at all (a tile gathers its rows), a small one by the shrink's own
-// work-groups, larger ones by a launch of its own.
+constexpr int kLoraStreamRows = 64;
+constexpr int kLoraMaxPlanes = 4;
+// How the rows are listed by adapter: streamed batches not at all (their one
+// tile gathers its rows), small ones by the shrink's own work-groups, larger
+// ones by a launch of its own.
 enum LoraOrder { kLoraAsIs = 0, kLoraRank = 1, kLoraSort = 2 };
 constexpr int kLoraRankRows = 256;
-inline LoraOrder lora_order(int64_t M) { return M <= kLoraRows ? kLoraAsIs : M <= kLoraRankRows ? kLoraRank : kLoraSort; }
 // Whether M rows take the weight-streaming kernel (then A is laid out by
 // launch_lora_shrink) or the tiled GEMM.
 inline bool lora_streams(int64_t M) { return M <= kLoraStreamRows; }
@@ -220,12 +220,12 @@ int lora_planes(int64_t M, int64_t K, int64_t L, int64_t R);
 // perm (M), sid (M) from the caller's ids (kLoraSort)
 hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int64_t L, int32_t* perm, int32_t* sid, hipStream_t s);
 // p.v. order kLoraRank: also perm and sid (p.ids are the caller's, and
-// p.perm is not read). Beside it, with aqp not null, A in the streaming
-// kernel's layout, or with ah not null A's exact f16 form.
+// p.perm is not read). Beside it A, in the streaming kernel's layout (aqp, asfp)
+// or in its exact f16 form (ah); the others null.
 hipError_t launch_lora_shrink(const LoraParams& p, LoraOrder order, int32_t* perm, int32_t* sid, const uint8_t* aq,
                               const uint8_t* asf, uint8_t* aqp, uint8_t* asfp, uint16_t* ah, hipStream_t s);
-// For the fused epilogue: p.vs from p.v, and A's exact f16 form.
-hipError_t launch_lora_join(const LoraParams& p, const uint8_t* aq, const uint8_t* asf, uint16_t* ah, hipStream_t s);
+// For the fused epilogue: p.vs from p.v.
+hipError_t launch_lora_join(const LoraParams& p, hipStream_t s);
 // out = bf16(alpha * sum over chunks of partial[c] (M, N) + adapters)
 hipError_t launch_lora_reduce(const LoraParams& p, const float* partial, int ksplit, const float* a_gs,
                               const float* b_alpha, uint16_t* out, hipStream_t s);

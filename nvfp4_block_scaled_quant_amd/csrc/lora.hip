@@ -3,7 +3,7 @@
 // with A_a (R, K) and B_a (N, R) in bf16. The product with A_a ("shrink") gives
 // v[m] = scale[a] x[m] A_a^T in float32; the product with B_a ("expand") is added
 // to the projection before its one rounding. Per batch size:
-//   up to 32 rows   shrink (beside it A laid out for streaming), then one kernel
+//   up to 64 rows   shrink (beside it A laid out for streaming), then one kernel
 //                   that streams the weights and adds the adapters
 //   more rows       the rows are listed by adapter, shrink (beside it A's f16
 //                   form), the tiled GEMM; the expand is in its epilogue, or,
@@ -15,12 +15,14 @@
 // arithmetic is small, so the split is made for bytes in flight. A work-group
 // takes one tile of 64 (listed) rows, one adapter that occurs in it and one
 // range of K, and gathers the rows that have the adapter, so an adapter is read
-// once per tile however its rows are scattered. Its 8 waves interleave over the
-// range in blocks of 64 K values, read straight from memory into
-// v_mfma_f32_16x16x32_bf16 operands (one load covers 64 contiguous bytes of 16
-// rows; the next block's loads are issued before a block's products), and join
-// their sums in wave order through LDS. Ranges of K are separate partial sums,
-// added in order by the reader.
+// once per tile however its rows are scattered. x and A_a go to LDS by loads
+// that write it directly, in a ring of stages of 64 K values (128 bytes of 64
+// rows each), and from there to v_mfma_f32_16x16x32_bf16: reading the operands'
+// fragments straight from memory has every lane in another row than its
+// neighbours, 16 bytes an address, and ran at a quarter of the rate. Ranges of
+// K are separate partial sums, added in order by the reader.
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "lora.hpp"
@@ -34,12 +36,26 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 constexpr int NT = 512;
 constexpr int NW = NT / 64;
 constexpr uint32_t kRsrcWord3 = 0x00020000u;
+constexpr uint32_t kBeyond = 0x80000000u;      // an offset outside every buffer: reads zeros
 constexpr int kStreamNT = 2;        // buffer-load cache policy: non-temporal (read once)
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, kRsrcWord3);
 }
 
+constexpr int waitcnt_imm(int vm, int lgkm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4) | (lgkm << 8); }
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Work-group barrier for data in LDS: unlike __syncthreads() it does not wait
+// for global loads and stores in flight.
+__device__ __forceinline__ void lds_sync() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+constexpr int kShrinkStage = 2 * 64 * 128;      // 64 rows of x and of A_a, 64 K values
 constexpr int kRankBlock = 64;      // ranks of a work-group (4 column blocks of 16)
 
 // A's exact f16 values, rows padded with zeros to whole steps (32-bit indices:
@@ -72,20 +88,14 @@ __device__ void dequant_a(const uint8_t* __restrict__ aq, const uint8_t* __restr
     }
 }
 
-// For the fused epilogue: A's exact f16 values, and the shrunk rows' partial
-// sums joined into vs (the kernel's first work-groups).
-__global__ __launch_bounds__(256) void lora_join_kernel(LoraParams p, int join_blocks, const uint8_t* __restrict__ aq,
-                                                        const uint8_t* __restrict__ asf, uint8_t* __restrict__ ah) {
-    if ((int)blockIdx.x >= join_blocks) {
-        dequant_a(aq, asf, p.M, p.K, ah, (blockIdx.x - join_blocks) * 256 + threadIdx.x, (gridDim.x - join_blocks) * 256);
-        return;
-    }
+// For the fused epilogue: the shrunk rows' partial sums joined into vs.
+__global__ __launch_bounds__(256) void lora_join_kernel(LoraParams p) {
     const int R8 = p.R / 8;
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, pos = t / R8;
     const int k = 8 * (int)(t - pos * R8);
     if (pos >= p.M || p.ids[pos] < 0) return;
     u32x4 hi, low;
-    lora_v_operand<8>(p, true, p.perm[pos], k, hi, low);
+    lora_v_operand(p, p.perm[pos], k, hi, low);
     uint16_t* dst = p.vs + pos * 2 * p.R + k;
     *reinterpret_cast<u32x4*>(dst) = hi;
     *reinterpret_cast<u32x4*>(dst + p.R) = low;
@@ -126,7 +136,10 @@ __device__ void lay_out_a(const LoraParams& p, const uint8_t* __restrict__ aq, c
     }
 }
 
-__global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles, int slots, int shrink_blocks,
+// NS stages, STEP of them between two barriers: 4 and 1 where two work-groups
+// share a CU, 8 and 2 for small batches, which are bound by the time of a step
+template <int NS, int STEP>
+__global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles, int rbs, int slots, int shrink_blocks,
                                                          bool rank_rows, int32_t* __restrict__ perm_out,
                                                          int32_t* __restrict__ sid_out,
                                                          const uint8_t* __restrict__ aq,
@@ -138,15 +151,19 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
         else lay_out_a(p, aq, asf, aqp, asfp, first, stride);
         return;
     }
-    constexpr int G = kLoraRows / 16, TR = kLoraRows;
+    constexpr int TR = kLoraRows;
+    extern __shared__ __attribute__((aligned(16))) uint8_t ring[];
     __shared__ int list[TR];
-    __shared__ __attribute__((aligned(16))) float red[NW][16][kRankBlock + 4];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, q = lane >> 4;
-    const int tile = blockIdx.x % tiles, rest = blockIdx.x / tiles;
-    const int slot = rest % slots, z = rest / slots;
-    const int plane = z % p.planes, rb = z / p.planes;
+    // (the slots, which may have nothing to do, are the last work-groups)
+    // Work-groups go to the eight XCDs in turn: each gets neighbouring tiles,
+    // which mostly have the same adapter, so that its L2 serves it to them.
+    const int rest = blockIdx.x / tiles, turn = blockIdx.x % tiles;
+    const int per_xcd = tiles / 8, full = per_xcd * 8;
+    const int tile = turn < full ? turn % 8 * per_xcd + turn / 8 : turn;
+    const int plane = rest % p.planes, rb = rest / p.planes % rbs, slot = rest / (p.planes * rbs);
     const int64_t m0 = (int64_t)tile * TR;
     const int rbase = rb * kRankBlock;
     const int64_t M = p.M, K = p.K;
@@ -168,9 +185,10 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
             }
             key[tid] = mine;
         }
-        __syncthreads();
+        lds_sync();
         if (tid < M) {
             int pos = 0;
+#pragma unroll 4
             for (int j = 0; j < (int)M; j += 4) {
                 const u32x4 k = *reinterpret_cast<const u32x4*>(key + j);
 #pragma unroll
@@ -178,7 +196,7 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
             }
             order[pos] = mine;
         }
-        __syncthreads();
+        lds_sync();
         if (in) {
             row_of = order[m0 + lane] % kLoraRankRows;
             id = order[m0 + lane] / kLoraRankRows;
@@ -194,7 +212,7 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
         row_of = p.perm ? p.perm[m0 + lane] : (int)(m0 + lane);
     }
     uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
-    // blocks of 64 K values of this plane, dealt to the waves in turn
+    // blocks of 64 K values of this plane
     const int nb = (int)((K + 63) / 64), per = (nb + planes - 1) / planes;
     const int b0 = plane * per, b1 = min(nb, b0 + per);
 
@@ -208,103 +226,74 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
         const int rk = p.rank ? min(max(p.rank[a], 0), R) : R;
         const int n = __builtin_popcountll(rows);
         const float sc = p.scale[a];
-        __syncthreads();                             // the previous adapter's readers are done
+        lds_sync();                             // the previous adapter's readers are done
         if (wave == 0 && id == a) {
             const int at = __builtin_popcountll(rows & ((1ull << lane) - 1));
             list[at] = row_of;
         }
-        __syncthreads();
+        lds_sync();
 
-        const int groups = (n + 15) / 16;            // 16-row groups of the gathered rows
+        // loads into LDS: wave w brings rows 8 w .. + 7 of x and of A_a of each
+        // stage; lane l's 16 bytes are chunk l % 8 of row l / 8, stored swizzled
+        // (chunk c of row r at c ^ ((r >> 1) & 7), so that the 16 rows of a
+        // fragment read cover all banks). Rows, ranks and K values that are not
+        // there have offsets beyond the buffers and read zeros (x is below 2 GiB,
+        // as M * pitch_h(K) is).
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x, M * K * 2), ra = make_rsrc(p.a + (int64_t)a * R * K, (int64_t)R * K * 2);
         const int cols = min(max(rk - rbase, 0), kRankBlock);
-        const uint16_t* xr[G];
-        const uint16_t* ar[4];
-        bool xok[G], aok[4];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            xok[g] = 16 * g + c < n;
-            xr[g] = p.x + (int64_t)(xok[g] ? list[16 * g + c] : 0) * K + 8 * q;
-        }
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            aok[f] = 16 * f + c < cols;
-            ar[f] = p.a + ((int64_t)a * R + rbase + (aok[f] ? 16 * f + c : 0)) * K + 8 * q;
-        }
-        float4_t acc[G][4];
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int f = 0; f < 4; ++f) acc[g][f] = (float4_t){0.f, 0.f, 0.f, 0.f};
-        struct Block {
-            u32x4 x[G][2], a[4][2];
+        const int lr = 8 * wave + (lane >> 3), ch = (lane & 7) ^ ((lr >> 1) & 7);
+        const uint32_t x_off = lr < n ? (uint32_t)(((int64_t)list[lr] * K + 8 * ch) * 2) : kBeyond;
+        const uint32_t a_off = lr < cols ? (uint32_t)(((int64_t)(rbase + lr) * K + 8 * ch) * 2) : kBeyond;
+        auto issue = [&](int b) {                    // b past the range: zeros
+            const uint32_t k = (uint32_t)b * 64;
+            const uint32_t out = b < b1 && k + 8 * ch < (uint32_t)K ? 0u : kBeyond;
+            uint8_t* at = ring + (b - b0) % NS * kShrinkStage + wave * 1024;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)at, 16, x_off | out, 2 * k, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(at + kShrinkStage / 2), 16, a_off | out, 2 * k, 0, 0);
         };
-        auto load = [&](int b, Block& r) {
-            const int64_t k = (int64_t)b * 64;
-            const u32x4 zero = {0u, 0u, 0u, 0u};
+        // wave w: rows 16 (w % 4) .. + 15, ranks 32 (w / 4) .. + 31
+        const int g = wave & 3, rh = wave >> 2;
+        const bool busy = 16 * g < n && 32 * rh < cols;
+        float4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const uint32_t sw = 16 * ((c >> 1) & 7);
+        const uint32_t fx = (16 * g + c) * 128, fa = kShrinkStage / 2 + (32 * rh + c) * 128;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const bool kin = k + 32 * t + 8 * q < K;     // K % 8 == 0: a lane's 8 values are in or out together
+        for (int t = 0; t < NS - STEP; ++t) issue(b0 + t);
+        for (int b = b0; b < b1; b += STEP) {
+            // this wave's loads of the step's blocks are done when only later
+            // ones are outstanding; after the barrier everyone's are, and the
+            // blocks of the step before have been read by everyone: their stages
+            // are refilled
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * (NS - 2 * STEP), 0));
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    r.x[g][t] = zero;
-                    if (kin && xok[g]) r.x[g][t] = *reinterpret_cast<const u32x4*>(xr[g] + k + 32 * t);
-                }
+            for (int t = 0; t < STEP; ++t) issue(b + NS - STEP + t);
+            if (busy) {
 #pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    r.a[f][t] = zero;
-                    if (kin && aok[f]) r.a[f][t] = *reinterpret_cast<const u32x4*>(ar[f] + k + 32 * t);
-                }
-            }
-        };
-        auto compute = [&](const Block& r) {
+                for (int t = 0; t < 2 * STEP; ++t) {
+                    const uint8_t* st = ring + (b + t / 2 - b0) % NS * kShrinkStage;
+                    const uint32_t at = (64 * (t & 1) + 16 * q) ^ sw;
+                    const bf16x8_t vx = *reinterpret_cast<const bf16x8_t*>(st + fx + at);
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                if (g >= groups) continue;
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    if (16 * f >= cols) continue;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        acc[g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8_t, r.x[g][t]), __builtin_bit_cast(bf16x8_t, r.a[f][t]),
-                            acc[g][f], 0, 0, 0);
+                    for (int f = 0; f < 2; ++f)
+                        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            vx, *reinterpret_cast<const bf16x8_t*>(st + fa + f * 2048 + at), acc[f], 0, 0, 0);
                 }
             }
-        };
-        if (cols > 0 && b0 + wave < b1) {
-            // (past the end a block that is there is loaded again and not used)
-            Block even, odd;
-            int b = b0 + wave;
-            load(b, even);
-            while (true) {
-                load(min(b + NW, b1 - 1), odd);
-                __builtin_amdgcn_sched_barrier(0);
-                compute(even);
-                if ((b += NW) >= b1) break;
-                load(min(b + NW, b1 - 1), even);
-                __builtin_amdgcn_sched_barrier(0);
-                compute(odd);
-                if ((b += NW) >= b1) break;
-            }
         }
-        // acc[g][f][i] = D[gathered row 16 g + 4 q + i][rank 16 f + c]
-        const int store = min(R - rbase, kRankBlock);
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));      // no load into LDS outlives its adapter
+        // acc[f][i] = D[gathered row 16 g + 4 q + i][rank 32 rh + 16 f + c]
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            if (g >= groups) continue;
-            if (g > 0) __syncthreads();
+        for (int i = 0; i < 4; ++i) {
+            const int r = 16 * g + 4 * q + i;
+            if (r >= n) continue;
+            float* dst = p.v + ((int64_t)plane * M + list[r]) * R + rbase;
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) red[wave][4 * q + i][16 * f + c] = acc[g][f][i];
-            __syncthreads();
-            for (int e = tid; e < 16 * kRankBlock; e += NT) {
-                const int r = e / kRankBlock, col = e % kRankBlock;
-                if (16 * g + r >= n || col >= store) continue;
-                float sum = red[0][r][col];
-#pragma unroll
-                for (int w = 1; w < NW; ++w) sum += red[w][r][col];
-                p.v[((int64_t)plane * M + list[16 * g + r]) * R + rbase + col] = col < cols ? sc * sum : 0.0f;
+            for (int f = 0; f < 2; ++f) {
+                const int col = 32 * rh + 16 * f + c;
+                if (rbase + col < R) dst[col] = col < cols ? sc * acc[f][i] : 0.0f;
             }
         }
     }
@@ -397,72 +386,113 @@ __global__ __launch_bounds__(ST) void lora_sort_kernel(const int32_t* __restrict
 // ---------------------------------------------------------------------------
 // Expand into LDS: delta[r][n] = (v B_a^T) of row r of a tile of up to 64
 // rows and 16 CB columns from n0. The tile's (adapter, 16 of its rows) pairs
-// are dealt to the nw waves (a row has one adapter, so one wave writes it; the
-// caller has zeroed delta). `lane`'s row of the tile has adapter id (-1: none)
-// and is row row_of of v.
-template <int CB, int LD, int UNROLL>
+// are dealt to nw waves (a row has one adapter, so one wave writes it; the
+// caller has zeroed delta); a wave goes through its pairs 32 ranks at a time and
+// asks for the next 32 before it multiplies. `lane`'s row of the tile has
+// adapter id (-1: none) and is row row_of of v.
+template <int CB, int LD>
 __device__ __forceinline__ void expand_tile(const LoraParams& p, int id, int row_of, int64_t n0, int wave, int nw,
                                             float (*delta)[LD]) {
     const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
     uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
-    int turn = 0;                       // number of the adapter's first pair
-    while (todo) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-        const uint64_t rows = __builtin_amdgcn_ballot_w64(id == a);
-        todo &= ~rows;
-        const int n = __builtin_popcountll(rows);
-        const int first = turn;
-        turn += (n + 15) / 16;
-        // this wave's pairs among first .. turn - 1
-        int pair = first + (wave - first % nw + nw) % nw;
-        if (pair >= turn) continue;
-        const int rank = p.rank ? min(max(p.rank[a], 0), p.R) : p.R;
-        // lane i receives the adapter's i-th row: the lanes that have it push
-        // theirs to 0 .. n - 1, the others to the rest
-        const uint64_t below = (1ull << lane) - 1;
-        const int to = id == a ? __builtin_popcountll(rows & below) : n + __builtin_popcountll(~rows & below);
-        const int tile_row = __builtin_amdgcn_ds_permute(4 * to, lane);
-        const int v_row = __builtin_amdgcn_ds_permute(4 * to, row_of);
-        for (; pair < turn; pair += nw) {
-            const int g = 16 * (pair - first);
-            const int64_t row = __shfl(v_row, g + c, 64);
-            float4_t acc[CB];
-#pragma unroll
-            for (int f = 0; f < CB; ++f) acc[f] = (float4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-            for (int k0 = 0; k0 < rank; k0 += 32) {
-                const int k = k0 + 8 * q;
-                u32x4 b[CB], hi, low;
-#pragma unroll
-                for (int f = 0; f < CB; ++f) {
-                    const int64_t col = n0 + 16 * f + c;
-                    b[f] = lora_b_operand(p, col < p.N, a, col, k, rank);
-                }
-                lora_v_operand<UNROLL>(p, g + c < n && k < rank, row, k, hi, low);
-#pragma unroll
-                for (int f = 0; f < CB; ++f) {
-                    const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, b[f]);
-                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi), bf, acc[f], 0, 0, 0);
-                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low), bf, acc[f], 0, 0, 0);
+    uint64_t rows = 0;                  // of the adapter at hand
+    int a = 0, rank = 0, n = 0;
+    int turn = 0, first = 0, pair = -nw;   // pairs seen, the adapter's first one, this wave's
+    int tile_row = 0, v_row = 0, k0 = 0;
+    bool fresh = true;                  // the next step starts a pair
+    struct Step {
+        bool on, first, last;           // a step; of its pair the first, the last
+        int n, g, tile_row;
+        u32x4 b[CB];
+        float4_t v[kLoraMaxPlanes][2];
+    };
+    auto next = [&](Step& t) {
+        t.first = fresh;
+        if (fresh) {
+            k0 = 0;
+            pair += nw;
+            while (pair >= turn && todo) {
+                a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+                rows = __builtin_amdgcn_ballot_w64(id == a);
+                todo &= ~rows;
+                n = __builtin_popcountll(rows);
+                first = turn;
+                turn += (n + 15) / 16;
+                pair = first + (wave - first % nw + nw) % nw;     // may lie beyond turn
+                if (pair < turn) {
+                    rank = p.rank ? min(max(p.rank[a], 0), p.R) : p.R;
+                    // lane i receives the adapter's i-th row: the lanes that
+                    // have it push theirs to 0 .. n - 1, the others to the rest
+                    const uint64_t below = (1ull << lane) - 1;
+                    const int to = id == a ? __builtin_popcountll(rows & below) : n + __builtin_popcountll(~rows & below);
+                    tile_row = __builtin_amdgcn_ds_permute(4 * to, lane);
+                    v_row = __builtin_amdgcn_ds_permute(4 * to, row_of);
                 }
             }
+        } else {
+            k0 += 32;
+        }
+        t.on = pair < turn;
+        if (!t.on) return;
+        t.last = fresh = k0 + 32 >= rank;
+        t.n = n;
+        t.g = 16 * (pair - first);
+        t.tile_row = tile_row;
+        const int k = k0 + 8 * q;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = __shfl(tile_row, g + 4 * q + i, 64);
-                if (g + 4 * q + i < n)
+        for (int f = 0; f < CB; ++f) {
+            const int64_t col = n0 + 16 * f + c;
+            t.b[f] = lora_b_operand(p, col < p.N, a, col, k, rank);
+        }
+        const int64_t row = __shfl(v_row, t.g + c, 64);
+        const bool in = t.g + c < n && k < rank;
+        const float4_t* src = reinterpret_cast<const float4_t*>(p.v + row * p.R + k);
+        const int64_t plane = p.M * p.R / 4;
 #pragma unroll
-                    for (int f = 0; f < CB; ++f) delta[r][16 * f + c] = acc[f][i];
+        for (int j = 0; j < kLoraMaxPlanes; ++j) {
+            t.v[j][0] = t.v[j][1] = (float4_t){0.f, 0.f, 0.f, 0.f};
+            if (in && j < p.planes) {
+                t.v[j][0] = src[j * plane];
+                t.v[j][1] = src[j * plane + 1];
             }
         }
+    };
+    float4_t acc[CB];
+    auto work = [&](const Step& t) {
+        if (t.first)
+#pragma unroll
+            for (int f = 0; f < CB; ++f) acc[f] = (float4_t){0.f, 0.f, 0.f, 0.f};
+        u32x4 hi, low;
+        lora_split(t.v, hi, low);
+#pragma unroll
+        for (int f = 0; f < CB; ++f) {
+            const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, t.b[f]);
+            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi), bf, acc[f], 0, 0, 0);
+            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low), bf, acc[f], 0, 0, 0);
+        }
+        if (!t.last) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = __shfl(t.tile_row, (t.g + 4 * q + i) & 63, 64);
+            if (t.g + 4 * q + i < t.n)
+#pragma unroll
+                for (int f = 0; f < CB; ++f) delta[r][16 * f + c] = acc[f][i];
+        }
+    };
+    Step even, odd;
+    next(even);
+    while (even.on) {
+        next(odd);
+        work(even);
+        if (!odd.on) break;
+        next(even);
+        work(odd);
     }
 }
 
 // K chunks: out = bf16(alpha * (their sum, in order) + adapters), for one tile
 // of 64 listed rows and 32 columns.
-// (RT threads: 1024 for a batch that is one tile, which can hold up to 64
-// adapters; else 256, as listed rows put few adapters into a tile and several
-// work-groups share a CU)
-template <int RT>
+constexpr int RT = 256;
 __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles, const float* __restrict__ partial,
                                                          int ksplit, const float* __restrict__ a_gs,
                                                          const float* __restrict__ b_alpha,
@@ -472,52 +502,45 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t m0 = (int64_t)(blockIdx.x % tiles) * kLoraRows, n0 = (int64_t)(blockIdx.x / tiles) * 32;
-    for (int i = tid; i < kLoraRows * LD; i += RT) (&delta[0][0])[i] = 0.0f;
     const bool in = m0 + lane < p.M;
-    int id = in ? p.ids[m0 + lane] : -1;
-    if (id >= p.L) id = -1;
-    const int row_of = in ? (p.perm ? p.perm[m0 + lane] : (int)(m0 + lane)) : -1;
-    // each thread: C columns of tile rows tid / (32 / C), + RT C / 32
-    constexpr int C = RT == 1024 ? 2 : 4, TPR = 32 / C, NR = kLoraRows * TPR / RT;
-    typedef float vec_t __attribute__((ext_vector_type(C)));
-    const int col = C * (tid % TPR), r0 = tid / TPR;
-    vec_t sum[NR];
-    int row[NR];
+    const int id = in ? p.ids[m0 + lane] : -1;
+    const int row_of = in ? p.perm[m0 + lane] : -1;
+    for (int i = tid; i < kLoraRows * LD; i += RT) (&delta[0][0])[i] = 0.0f;
+    // each thread: four columns of tile rows tid / 8 and tid / 8 + 32
+    const int col = 4 * (tid & 7);
+    float4_t sum[2];
+    int row[2];
 #pragma unroll
-    for (int t = 0; t < NR; ++t) {
-        row[t] = __shfl(row_of, r0 + t * (RT / TPR), 64);
+    for (int t = 0; t < 2; ++t) {
+        row[t] = __shfl(row_of, (tid >> 3) + 32 * t, 64);
         if (n0 + col >= p.N) row[t] = -1;
         if (row[t] >= 0)
-            sum[t] = sum_planes<8>(reinterpret_cast<const vec_t*>(partial + (int64_t)row[t] * p.N + n0 + col), ksplit, p.M * p.N / C);
+            sum[t] = sum_planes<8>(reinterpret_cast<const float4_t*>(partial + (int64_t)row[t] * p.N + n0 + col), ksplit, p.M * p.N / 4);
     }
     __syncthreads();
-    expand_tile<2, LD, 8>(p, id, row_of, n0, wave, RT / 64, delta);
+    expand_tile<2, LD>(p, id, row_of, n0, wave, RT / 64, delta);
     __syncthreads();
     const float alpha = a_gs[0] * b_alpha[0];
 #pragma unroll
-    for (int t = 0; t < NR; ++t) {
-        const int r = r0 + t * (RT / TPR);
+    for (int t = 0; t < 2; ++t) {
         if (row[t] < 0) continue;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(out + (int64_t)row[t] * p.N + n0 + col);
-#pragma unroll
-        for (int e = 0; e < C; e += 2)
-            dst[e / 2] = pack_bf16x2_rne(alpha * sum[t][e] + delta[r][col + e], alpha * sum[t][e + 1] + delta[r][col + e + 1]);
+        const float* d = &delta[(tid >> 3) + 32 * t][col];
+        *reinterpret_cast<u32x2*>(out + (int64_t)row[t] * p.N + n0 + col) =
+            (u32x2){pack_bf16x2_rne(alpha * sum[t][0] + d[0], alpha * sum[t][1] + d[1]),
+                    pack_bf16x2_rne(alpha * sum[t][2] + d[2], alpha * sum[t][3] + d[3])};
     }
 }
 
 // ---------------------------------------------------------------------------
-// Up to 32 rows: the projection as a weight stream. A work-group owns 16 CB
-// columns and all rows; its first nk waves (up to 8) share K in whole groups
-// of four 128-element steps, so every wave has a kilobyte per step and column
-// block in flight, and nothing of the projection goes through memory again: the
-// waves' sums meet in LDS (added in wave order), where the expand's are too.
-// The adapters' pairs are dealt from the last wave on: it has no share of K
-// (loads return in order: in a wave that streams, the adapters' operands
-// arrive after its weights). With two row blocks and all eight waves streaming
-// there is none: a ninth would leave them too few registers.
-template <int MT> constexpr int kStreamWaves = MT == 1 ? NW + 1 : NW;
+// Up to 64 rows: the projection as a weight stream. A work-group owns 16 CB
+// columns and all rows; its first nk waves share K in whole groups of four
+// 128-element steps, so every wave has a kilobyte per step and column block in
+// flight, and nothing of the projection goes through memory again: the waves'
+// sums meet in LDS (added in wave order), where the expand's are too. The other
+// waves do the expand meanwhile (loads return in order: in a wave that streams,
+// the adapters' operands would arrive after its weights).
 template <int MT, int CB>
-__global__ __launch_bounds__(64 * kStreamWaves<MT>) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : 2)))
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : 2)))
 void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict__ aqp,
                                                          const uint8_t* __restrict__ asfp,
                                                          const uint8_t* __restrict__ bq,
@@ -526,8 +549,9 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
                                                          const float* __restrict__ b_alpha,
                                                          uint16_t* __restrict__ out) {
     constexpr int LD = 16 * CB + 4;
-    __shared__ __attribute__((aligned(16))) float delta[16 * MT][LD];
-    __shared__ __attribute__((aligned(16))) float red[NW][16 * MT][LD];
+    extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+    float (*delta)[LD] = reinterpret_cast<float (*)[LD]>(dyn);                       // [16 MT]
+    float (*red)[16 * MT][LD] = reinterpret_cast<float (*)[16 * MT][LD]>(dyn + 16 * MT * LD * 4);   // [nk]
     const int tid = threadIdx.x, lane = tid & 63, nthreads = blockDim.x, nw = nthreads / 64;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, q = lane >> 4;
@@ -537,8 +561,12 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
     const int64_t blocks = p.N / 16;
 
     struct Group {
-        u32x4 w[CB][4], a[MT][4];
-        u32x2 ws[CB], as[MT];
+        u32x4 w[CB][4];
+        u32x2 ws[CB];
+    };
+    struct Half {                       // A of two of the group's steps
+        u32x4 a[MT][2];
+        uint32_t as[MT];
     };
     // buffer loads: one lane offset per operand, the rest in scalar offsets
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(bq, p.N * ldq), rws = make_rsrc(bsf, p.N * ldwsf);
@@ -556,13 +584,13 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
             }
         }
     };
-    auto load_a = [&](int g, Group& r) {
+    auto load_a = [&](int g, int half, Half& r) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            r.as[m] = __builtin_amdgcn_raw_buffer_load_b64(ras, sf_off, (uint32_t)(m * quads + g) * 512, 0);
+            r.as[m] = __builtin_amdgcn_raw_buffer_load_b32(ras, sf_off, (uint32_t)(m * quads + g) * 512 + 4 * half, 0);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int st = min(4 * g + u, steps - 1);
+            for (int u = 0; u < 2; ++u) {
+                const int st = min(4 * g + 2 * half + u, steps - 1);
                 r.a[m][u] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_off, (uint32_t)(m * steps + st) * 1024, 0);
             }
         }
@@ -574,62 +602,63 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
         for (int f = 0; f < CB; ++f) acc[m][f] = (float4_t){0.f, 0.f, 0.f, 0.f};
     // dword s of a step's 16 bytes: K values 32 q + 8 s .. + 7 in both operands,
     // in scale group 2 q + s / 2
-    auto compute = [&](const Group& r) {
+    auto compute = [&](const Group& r, int half, const Half& x) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int sh = 16 * (u & 1) + 8 * (s >> 1);
+                const int sh = 16 * u + 8 * (s >> 1);
                 half8_t ha[MT];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) ha[m] = dequant8(r.a[m][u][s], scale_pair((r.as[m][u >> 1] >> sh) & 0xFFu));
+                for (int m = 0; m < MT; ++m) ha[m] = dequant8(x.a[m][u][s], scale_pair((x.as[m] >> sh) & 0xFFu));
 #pragma unroll
                 for (int f = 0; f < CB; ++f) {
-                    const half8_t hb = dequant8(r.w[f][u][s], scale_pair((r.ws[f][u >> 1] >> sh) & 0xFFu));
+                    const half8_t hb = dequant8(r.w[f][2 * half + u][s], scale_pair((r.ws[f][half] >> sh) & 0xFFu));
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
                         acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ha[m], hb, acc[m][f], 0, 0, 0);
                 }
             }
     };
-    // two groups in flight (an index past the wave's last group loads it
-    // again); A, which every work-group reads, follows from the L2
+    // two groups of weights in flight; A, which every work-group reads, comes
+    // from the L2
     const int g0 = wave * per, g1 = min(quads, g0 + per);
-    const bool streams = wave < nk;
-    int id = lane < p.M ? p.ids[lane] : -1;
-    if (id >= p.L) id = -1;
-    Group r0, r1;
-    if (streams) {
-        load_w(g0, r0);
-        load_w(min(g0 + 1, g1 - 1), r1);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-
-    // the adapters while the first weights are on their way
     for (int i = tid; i < 16 * MT * LD; i += nthreads) (&delta[0][0])[i] = 0.0f;
     __syncthreads();
-    expand_tile<CB, LD, 4>(p, id, lane, blk0 * 16, nw - 1 - wave, nw, delta);
-
-    if (streams) {
-    int g = g0;
-    load_a(g0, r0);
-    load_a(min(g0 + 1, g1 - 1), r1);
-    for (; g + 2 < g1; g += 2) {
-        compute(r0);
-        load_w(g + 2, r0);
-        load_a(g + 2, r0);
-        compute(r1);
-        load_w(min(g + 3, g1 - 1), r1);
-        load_a(min(g + 3, g1 - 1), r1);
-    }
-    compute(r0);
-    if (g + 1 < g1) compute(r1);
+    if (wave < nk) {
+        // (an index past the wave's last group loads it again)
+        Group r0, r1;
+        load_w(g0, r0);
+        load_w(min(g0 + 1, g1 - 1), r1);
+        Half x0, x1;
+        load_a(g0, 0, x0);
+        load_a(g0, 1, x1);
+        int g = g0;
+        auto group = [&](const Group& r) {
+            compute(r, 0, x0);
+            load_a(min(g + 1, g1 - 1), 0, x0);
+            compute(r, 1, x1);
+            load_a(min(g + 1, g1 - 1), 1, x1);
+            ++g;
+        };
+        while (true) {
+            group(r0);
+            if (g >= g1) break;
+            load_w(min(g + 1, g1 - 1), r0);
+            group(r1);
+            if (g >= g1) break;
+            load_w(min(g + 1, g1 - 1), r1);
+        }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int f = 0; f < CB; ++f)
+            for (int f = 0; f < CB; ++f)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) red[wave][16 * m + 4 * q + i][16 * f + c] = acc[m][f][i];
+                for (int i = 0; i < 4; ++i) red[wave][16 * m + 4 * q + i][16 * f + c] = acc[m][f][i];
+    } else {
+        int id = lane < p.M ? p.ids[lane] : -1;
+        if (id >= p.L) id = -1;
+        expand_tile<CB, LD>(p, id, lane, blk0 * 16, wave - nk, nw - nk, delta);
     }
     __syncthreads();
     const float alpha = a_gs[0] * b_alpha[0];
@@ -650,28 +679,33 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
 template <int MT, int CB>
 hipError_t launch_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t* asfp, const uint8_t* bq,
                          const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out, hipStream_t s) {
-    const int quads = (int)(pitch_wsf(p.K) / 32), per = (quads + NW - 1) / NW, nk = (quads + per - 1) / per;
+    // one wave of eight expands for a row or two, four for more
+    const int expand = p.M <= 2 ? 1 : 4, most = NW - expand;
+    const int quads = (int)(pitch_wsf(p.K) / 32), per = (quads + most - 1) / most, nk = (quads + per - 1) / per;
     const int64_t grid = (p.N / 16 + CB - 1) / CB;
-    // waves beside the streaming ones: one, or what is left of eight
-    const int nw = nk < NW ? NW : kStreamWaves<MT>;
-    lora_stream_kernel<MT, CB><<<(unsigned)grid, 64 * nw, 0, s>>>(p, nk, per, aqp, asfp, bq, bsf, a_gs, b_alpha, out);
+    const int lds = (1 + nk) * 16 * MT * (16 * CB + 4) * 4;
+    static std::atomic<int> lds_set[kMaxDevices];
+    hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&lora_stream_kernel<MT, CB>), lds, lds_set);
+    if (e != hipSuccess) return e;
+    lora_stream_kernel<MT, CB><<<(unsigned)grid, 64 * (nk + expand), lds, s>>>(p, nk, per, aqp, asfp, bq, bsf, a_gs,
+                                                                              b_alpha, out);
     return hipGetLastError();
 }
 
 }  // namespace
 
 // Work-groups of the shrink before K is split: tiles x the adapters a tile can
-// hold x rank blocks; K ranges (at most 8, each at least 8 blocks of 64, one
-// per wave) bring the launch to about one work-group per CU. Listed tiles hold
-// few adapters, which the host cannot know; counting one per tile is right for
-// runs of rows and only costs partial sums where there are more.
+// hold x rank blocks; K ranges (at most 4, each at least 4 blocks of 64) bring
+// the launch to about two work-groups per CU. Listed tiles hold few adapters,
+// which the host cannot know; counting one per tile, with room for the tiles
+// where two meet, is right for runs of rows.
 int lora_planes(int64_t M, int64_t K, int64_t L, int64_t R) {
     const int64_t tiles = (M + kLoraRows - 1) / kLoraRows, rbs = (R + kRankBlock - 1) / kRankBlock;
     const int64_t here = tiles > 1 ? 1 : (M < L ? M : L);
     const int64_t nb = (K + 63) / 64;
-    int64_t n = 256 / (tiles * rbs * here);
-    if (n > nb / 8) n = nb / 8;
-    if (n > 8) n = 8;
+    int64_t n = (tiles > 1 ? 416 : 512) / (tiles * rbs * here);
+    if (n > nb / 4) n = nb / 4;
+    if (n > kLoraMaxPlanes) n = kLoraMaxPlanes;
     if (n < 1) n = 1;
     const int64_t per = (nb + n - 1) / n;
     return (int)((nb + per - 1) / per);
@@ -688,33 +722,35 @@ hipError_t launch_lora_shrink(const LoraParams& p, LoraOrder order, int32_t* per
     // work-groups that share a tile's adapters: as many as it can hold when it
     // is the only tile; listed rows put few adapters into a tile
     int64_t slots = p.M < p.L ? p.M : p.L;
-    if (order != kLoraAsIs && slots > 4) slots = 4;
+    const int64_t most = tiles <= 4 ? 8 : tiles <= 16 ? 4 : tiles <= 64 ? 2 : 1;
+    if (order != kLoraAsIs && slots > most) slots = most;
     const int64_t blocks = tiles * slots * p.planes * rbs;
     const int64_t more = aqp  ? (lora_stream_aq_bytes(p.M, p.K) / 16 + lora_stream_asf_bytes(p.M, p.K) / 8 + NT - 1) / NT
-                         : ah ? (p.M * (p.K / 16) + 4 * NT - 1) / (4 * NT)
-                              : 0;
-    lora_shrink_kernel<<<(unsigned)(blocks + more), NT, 0, s>>>(p, (int)tiles, (int)slots, (int)blocks,
-                                                               order == kLoraRank, perm, sid, aq, asf, aqp, asfp,
-                                                               reinterpret_cast<uint8_t*>(ah));
-    return hipGetLastError();
+                              : (p.M * (p.K / 16) + 4 * NT - 1) / (4 * NT);
+    auto launch = [&](auto ns, auto step) {
+        constexpr int NS = decltype(ns)::value, STEP = decltype(step)::value, lds = NS * kShrinkStage;
+        static std::atomic<int> lds_set[kMaxDevices];
+        hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&lora_shrink_kernel<NS, STEP>), lds, lds_set);
+        if (e != hipSuccess) return e;
+        lora_shrink_kernel<NS, STEP><<<(unsigned)(blocks + more), NT, lds, s>>>(
+            p, (int)tiles, (int)rbs, (int)slots, (int)blocks, order == kLoraRank, perm, sid, aq, asf, aqp, asfp,
+            reinterpret_cast<uint8_t*>(ah));
+        return hipGetLastError();
+    };
+    return tiles <= 4 ? launch(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{})
+                      : launch(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
 }
 
-hipError_t launch_lora_join(const LoraParams& p, const uint8_t* aq, const uint8_t* asf, uint16_t* ah, hipStream_t s) {
-    const int64_t join = (p.M * (p.R / 8) + 255) / 256;
-    int64_t more = (p.M * (p.K / 16) + 1023) / 1024;
-    if (more > 4096) more = 4096;
-    lora_join_kernel<<<(unsigned)(join + more), 256, 0, s>>>(p, (int)join, aq, asf, reinterpret_cast<uint8_t*>(ah));
+hipError_t launch_lora_join(const LoraParams& p, hipStream_t s) {
+    lora_join_kernel<<<(unsigned)((p.M * (p.R / 8) + 255) / 256), 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
 hipError_t launch_lora_reduce(const LoraParams& p, const float* partial, int ksplit, const float* a_gs,
                               const float* b_alpha, uint16_t* out, hipStream_t s) {
     const int64_t tiles = (p.M + kLoraRows - 1) / kLoraRows;
-    const unsigned grid = (unsigned)(tiles * ((p.N + 31) / 32));
-    if (tiles == 1)
-        lora_reduce_kernel<1024><<<grid, 1024, 0, s>>>(p, 1, partial, ksplit, a_gs, b_alpha, out);
-    else
-        lora_reduce_kernel<256><<<grid, 256, 0, s>>>(p, (int)tiles, partial, ksplit, a_gs, b_alpha, out);
+    lora_reduce_kernel<<<(unsigned)(tiles * ((p.N + 31) / 32)), RT, 0, s>>>(p, (int)tiles, partial, ksplit, a_gs, b_alpha,
+                                                                            out);
     return hipGetLastError();
 }
 
@@ -722,7 +758,8 @@ hipError_t launch_lora_stream(const LoraParams& p, const uint8_t* aqp, const uin
                               const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out,
                               hipStream_t s) {
     if (p.M <= 16) return launch_stream<1, 1>(p, aqp, asfp, bq, bsf, a_gs, b_alpha, out, s);
-    return launch_stream<2, 2>(p, aqp, asfp, bq, bsf, a_gs, b_alpha, out, s);
+    if (p.M <= 32) return launch_stream<2, 2>(p, aqp, asfp, bq, bsf, a_gs, b_alpha, out, s);
+    return launch_stream<4, 2>(p, aqp, asfp, bq, bsf, a_gs, b_alpha, out, s);
 }
 
 }  // namespace nvfp4
