@@ -202,7 +202,7 @@ constexpr int64_t kLoraMaxRank = 256;
 constexpr int64_t kLoraMaxAdapters = 8192;
 constexpr int kLoraRows = 64;     // rows of a tile of the adapters' kernels
 constexpr int kLoraStreamRows = 64;
-constexpr int kLoraMaxPlanes = 4;
+constexpr int kLoraMaxPlanes = 8;
 // How the rows are listed by adapter: streamed batches not at all (their one
 // tile gathers its rows), small ones by the shrink's own work-groups, larger
 // ones by a launch of its own.

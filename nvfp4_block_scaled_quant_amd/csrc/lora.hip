@@ -385,88 +385,118 @@ __global__ __launch_bounds__(ST) void lora_sort_kernel(const int32_t* __restrict
 
 // ---------------------------------------------------------------------------
 // Expand into LDS: delta[r][n] = (v B_a^T) of row r of a tile of up to 64
-// rows and 16 CB columns from n0. The tile's (adapter, 16 of its rows) pairs
-// are dealt to nw waves (a row has one adapter, so one wave writes it; the
-// caller has zeroed delta); a wave goes through its pairs 32 ranks at a time and
-// asks for the next 32 before it multiplies. `lane`'s row of the tile has
-// adapter id (-1: none) and is row row_of of v.
+// rows and 16 CB columns from n0, in two parts.
+//
+// join_v: nthreads threads join the rows' partial sums of v into LDS as bf16
+// hi + low (rows of 2 R values, lds_v_pitch(R) apart; row(r) < 0: none). v is
+// read in order; a fragment of v straight from memory has every lane in
+// another row than its neighbours, one address each.
+__host__ __device__ inline int lds_v_pitch(int R) { return 2 * R + 8; }      // 16 bytes of skew between rows
+
+template <typename F>
+__device__ __forceinline__ void join_v(const LoraParams& p, int nrows, F row_of, int thread, int nthreads,
+                                       uint16_t* __restrict__ lv) {
+    const int R8 = p.R / 8, pitch = lds_v_pitch(p.R);
+    for (int e = thread; e < nrows * R8; e += nthreads) {
+        const int r = e / R8, k = 8 * (e - r * R8), row = row_of(r);
+        if (row < 0) continue;
+        u32x4 hi, low;
+        lora_v_operand(p, row, k, hi, low);
+        *reinterpret_cast<u32x4*>(lv + r * pitch + k) = hi;
+        *reinterpret_cast<u32x4*>(lv + r * pitch + p.R + k) = low;
+    }
+}
+
+// Expand: the tile's (adapter, 16 of its rows) pairs are dealt to nw waves (a
+// row has one adapter, so one wave writes it; the caller has zeroed delta); a
+// wave goes through its pairs 32 ranks at a time, with B_a of the next AHEAD
+// steps on its way. The constructor asks for the first ones, run() (when lv is
+// complete) does the work. `lane`'s row of the tile has adapter id (-1: none).
 template <int CB, int LD>
-__device__ __forceinline__ void expand_tile(const LoraParams& p, int id, int row_of, int64_t n0, int wave, int nw,
-                                            float (*delta)[LD]) {
-    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-    uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
-    uint64_t rows = 0;                  // of the adapter at hand
-    int a = 0, rank = 0, n = 0;
-    int turn = 0, first = 0, pair = -nw;   // pairs seen, the adapter's first one, this wave's
-    int tile_row = 0, v_row = 0, k0 = 0;
-    bool fresh = true;                  // the next step starts a pair
+struct Expand {
+    static constexpr int AHEAD = 3;
     struct Step {
         bool on, first, last;           // a step; of its pair the first, the last
-        int n, g, tile_row;
+        int n, g, k0, rank, tile_row;
         u32x4 b[CB];
-        float4_t v[kLoraMaxPlanes][2];
     };
-    auto next = [&](Step& t) {
+    const LoraParams& p;
+    const int64_t n0;
+    const int id, wave, nw, lane, c, q;
+    const int my_rank;                  // of the lane's row's adapter
+    uint64_t todo, rows = 0;            // rows not looked at, rows of the adapter at hand
+    int a = 0, rank = 0, n = 0;
+    int turn = 0, first = 0, pair;      // pairs seen, the adapter's first one, this wave's
+    int tile_row = 0, k0 = 0;
+    bool fresh = true;                  // the next step starts a pair
+    Step st[AHEAD + 1];
+
+    __device__ __forceinline__ Expand(const LoraParams& p_, int id_, int64_t n0_, int wave_, int nw_)
+        : p(p_), n0(n0_), id(id_), wave(wave_), nw(nw_), lane(threadIdx.x & 63), c(lane & 15), q(lane >> 4),
+          my_rank(p_.rank && id_ >= 0 ? min(max(p_.rank[id_], 0), p_.R) : p_.R),
+          todo(__builtin_amdgcn_ballot_w64(id_ >= 0)), pair(wave_ - nw_) {
+#pragma unroll
+        for (int t = 0; t < AHEAD; ++t) next(st[t]);
+    }
+    __device__ __forceinline__ void next(Step& t) {
         t.first = fresh;
         if (fresh) {
             k0 = 0;
             pair += nw;
             while (pair >= turn && todo) {
-                a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+                const int lead = __builtin_ctzll(todo);
+                a = __builtin_amdgcn_readlane(id, lead);
+                rank = __builtin_amdgcn_readlane(my_rank, lead);
                 rows = __builtin_amdgcn_ballot_w64(id == a);
                 todo &= ~rows;
                 n = __builtin_popcountll(rows);
                 first = turn;
                 turn += (n + 15) / 16;
-                pair = first + (wave - first % nw + nw) % nw;     // may lie beyond turn
                 if (pair < turn) {
-                    rank = p.rank ? min(max(p.rank[a], 0), p.R) : p.R;
                     // lane i receives the adapter's i-th row: the lanes that
                     // have it push theirs to 0 .. n - 1, the others to the rest
                     const uint64_t below = (1ull << lane) - 1;
                     const int to = id == a ? __builtin_popcountll(rows & below) : n + __builtin_popcountll(~rows & below);
                     tile_row = __builtin_amdgcn_ds_permute(4 * to, lane);
-                    v_row = __builtin_amdgcn_ds_permute(4 * to, row_of);
                 }
             }
         } else {
             k0 += 32;
         }
         t.on = pair < turn;
-        if (!t.on) return;
-        t.last = fresh = k0 + 32 >= rank;
-        t.n = n;
-        t.g = 16 * (pair - first);
-        t.tile_row = tile_row;
+        if (t.on) {
+            t.last = fresh = k0 + 32 >= rank;
+            t.n = n;
+            t.g = 16 * (pair - first);
+            t.k0 = k0;
+            t.rank = rank;
+            t.tile_row = tile_row;
+        }
+        // (buffer loads without a branch, so that the compiler's waits leave the
+        // later steps' in flight: what is not there lies beyond the buffer)
+        const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + ((int64_t)a * p.N + n0) * p.R, min((int64_t)16 * CB, p.N - n0) * p.R * 2);
         const int k = k0 + 8 * q;
 #pragma unroll
-        for (int f = 0; f < CB; ++f) {
-            const int64_t col = n0 + 16 * f + c;
-            t.b[f] = lora_b_operand(p, col < p.N, a, col, k, rank);
-        }
-        const int64_t row = __shfl(v_row, t.g + c, 64);
-        const bool in = t.g + c < n && k < rank;
-        const float4_t* src = reinterpret_cast<const float4_t*>(p.v + row * p.R + k);
-        const int64_t plane = p.M * p.R / 4;
-#pragma unroll
-        for (int j = 0; j < kLoraMaxPlanes; ++j) {
-            t.v[j][0] = t.v[j][1] = (float4_t){0.f, 0.f, 0.f, 0.f};
-            if (in && j < p.planes) {
-                t.v[j][0] = src[j * plane];
-                t.v[j][1] = src[j * plane + 1];
-            }
-        }
-    };
-    float4_t acc[CB];
-    auto work = [&](const Step& t) {
+        for (int f = 0; f < CB; ++f)
+            t.b[f] = __builtin_amdgcn_raw_buffer_load_b128(
+                rb, t.on && k < rank ? (uint32_t)((16 * f + c) * p.R + k) * 2 : kBeyond, 0, 0);
+    }
+    __device__ __forceinline__ void work(const Step& t, float4_t (&acc)[CB], const uint16_t* __restrict__ lv,
+                                         float (*delta)[LD]) {
         if (t.first)
 #pragma unroll
             for (int f = 0; f < CB; ++f) acc[f] = (float4_t){0.f, 0.f, 0.f, 0.f};
-        u32x4 hi, low;
-        lora_split(t.v, hi, low);
+        const uint16_t* vr = lv + __shfl(t.tile_row, t.g + c, 64) * lds_v_pitch(p.R) + t.k0 + 8 * q;
+        u32x4 hi = {0u, 0u, 0u, 0u}, low = {0u, 0u, 0u, 0u};
+        if (t.g + c < t.n && t.k0 + 8 * q < t.rank) {
+            hi = *reinterpret_cast<const u32x4*>(vr);
+            low = *reinterpret_cast<const u32x4*>(vr + p.R);
+        }
 #pragma unroll
         for (int f = 0; f < CB; ++f) {
-            const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, t.b[f]);
+            u32x4 b = t.b[f];
+            if (t.rank & 7) b = lora_mask_rank(b, t.k0 + 8 * q, t.rank);
+            const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, b);
             acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi), bf, acc[f], 0, 0, 0);
             acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low), bf, acc[f], 0, 0, 0);
         }
@@ -478,17 +508,19 @@ __device__ __forceinline__ void expand_tile(const LoraParams& p, int id, int row
 #pragma unroll
                 for (int f = 0; f < CB; ++f) delta[r][16 * f + c] = acc[f][i];
         }
-    };
-    Step even, odd;
-    next(even);
-    while (even.on) {
-        next(odd);
-        work(even);
-        if (!odd.on) break;
-        next(even);
-        work(odd);
     }
-}
+    __device__ __forceinline__ void run(const uint16_t* __restrict__ lv, float (*delta)[LD]) {
+        float4_t acc[CB];
+        while (true) {
+#pragma unroll
+            for (int t = 0; t <= AHEAD; ++t) {
+                if (!st[t].on) return;
+                next(st[(t + AHEAD) % (AHEAD + 1)]);
+                work(st[t], acc, lv, delta);
+            }
+        }
+    }
+};
 
 // K chunks: out = bf16(alpha * (their sum, in order) + adapters), for one tile
 // of 64 listed rows and 32 columns.
@@ -498,14 +530,19 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
                                                          const float* __restrict__ b_alpha,
                                                          uint16_t* __restrict__ out) {
     constexpr int LD = 36;
+    extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+    uint16_t* lv = reinterpret_cast<uint16_t*>(dyn);
     __shared__ __attribute__((aligned(16))) float delta[kLoraRows][LD];
+    __shared__ int rows[kLoraRows];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t m0 = (int64_t)(blockIdx.x % tiles) * kLoraRows, n0 = (int64_t)(blockIdx.x / tiles) * 32;
     const bool in = m0 + lane < p.M;
     const int id = in ? p.ids[m0 + lane] : -1;
     const int row_of = in ? p.perm[m0 + lane] : -1;
+    if (wave == 0) rows[lane] = id >= 0 ? row_of : -1;
     for (int i = tid; i < kLoraRows * LD; i += RT) (&delta[0][0])[i] = 0.0f;
+    lds_sync();
     // each thread: four columns of tile rows tid / 8 and tid / 8 + 32
     const int col = 4 * (tid & 7);
     float4_t sum[2];
@@ -517,9 +554,11 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
         if (row[t] >= 0)
             sum[t] = sum_planes<8>(reinterpret_cast<const float4_t*>(partial + (int64_t)row[t] * p.N + n0 + col), ksplit, p.M * p.N / 4);
     }
-    __syncthreads();
-    expand_tile<2, LD>(p, id, row_of, n0, wave, RT / 64, delta);
-    __syncthreads();
+    Expand<2, LD> expand(p, id, n0, wave, RT / 64);
+    join_v(p, kLoraRows, [&](int r) { return rows[r]; }, tid, RT, lv);
+    lds_sync();
+    expand.run(lv, delta);
+    lds_sync();
     const float alpha = a_gs[0] * b_alpha[0];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -540,7 +579,7 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
 // waves do the expand meanwhile (loads return in order: in a wave that streams,
 // the adapters' operands would arrive after its weights).
 template <int MT, int CB>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : 2)))
+__global__ __launch_bounds__(MT == 4 ? NT + 256 : NT) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : MT == 4 ? 3 : 2)))
 void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict__ aqp,
                                                          const uint8_t* __restrict__ asfp,
                                                          const uint8_t* __restrict__ bq,
@@ -552,6 +591,7 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
     extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
     float (*delta)[LD] = reinterpret_cast<float (*)[LD]>(dyn);                       // [16 MT]
     float (*red)[16 * MT][LD] = reinterpret_cast<float (*)[16 * MT][LD]>(dyn + 16 * MT * LD * 4);   // [nk]
+    uint16_t* lv = reinterpret_cast<uint16_t*>(dyn + (1 + nk) * 16 * MT * LD * 4);
     const int tid = threadIdx.x, lane = tid & 63, nthreads = blockDim.x, nw = nthreads / 64;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, q = lane >> 4;
@@ -623,22 +663,29 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
     // two groups of weights in flight; A, which every work-group reads, comes
     // from the L2
     const int g0 = wave * per, g1 = min(quads, g0 + per);
-    for (int i = tid; i < 16 * MT * LD; i += nthreads) (&delta[0][0])[i] = 0.0f;
-    __syncthreads();
+    // the expanding waves wait for each other on a counter in LDS (all waves of
+    // a work-group run at the same time): a barrier would hold up the streams
+    __shared__ int joined;
+    if (tid == 0) joined = 0;
+    lds_sync();
     if (wave < nk) {
         // (an index past the wave's last group loads it again)
         Group r0, r1;
         load_w(g0, r0);
         load_w(min(g0 + 1, g1 - 1), r1);
-        Half x0, x1;
-        load_a(g0, 0, x0);
-        load_a(g0, 1, x1);
+        // A of half a group at a time; with four row blocks three waves on a SIMD
+        // hide its latency, and there are registers for one of them only
+        constexpr int AB = MT == 4 ? 1 : 2;
+        Half x[AB];
+#pragma unroll
+        for (int t = 0; t < AB; ++t) load_a(g0, t, x[t]);
         int g = g0;
         auto group = [&](const Group& r) {
-            compute(r, 0, x0);
-            load_a(min(g + 1, g1 - 1), 0, x0);
-            compute(r, 1, x1);
-            load_a(min(g + 1, g1 - 1), 1, x1);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                compute(r, t, x[t % AB]);
+                load_a(t + AB >= 2 ? min(g + 1, g1 - 1) : g, (t + AB) % 2, x[t % AB]);
+            }
             ++g;
         };
         while (true) {
@@ -656,11 +703,23 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
 #pragma unroll
                 for (int i = 0; i < 4; ++i) red[wave][16 * m + 4 * q + i][16 * f + c] = acc[m][f][i];
     } else {
+        // the few instructions of the expand go ahead of the streams' many
+        __builtin_amdgcn_s_setprio(3);
+        const int t = tid - 64 * nk, nt = 64 * (nw - nk);
         int id = lane < p.M ? p.ids[lane] : -1;
         if (id >= p.L) id = -1;
-        expand_tile<CB, LD>(p, id, lane, blk0 * 16, wave - nk, nw - nk, delta);
+        Expand<CB, LD> expand(p, id, blk0 * 16, wave - nk, nw - nk);
+        // (rows without an adapter have no v: what is joined for them is not used)
+        join_v(p, (int)p.M, [](int r) { return r; }, t, nt, lv);
+        for (int i = t; i < 16 * MT * LD; i += nt) (&delta[0][0])[i] = 0.0f;
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+        if (lane == 0) __hip_atomic_fetch_add(&joined, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        while (__hip_atomic_load(&joined, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) < nw - nk) __builtin_amdgcn_s_sleep(1);
+        asm volatile("" ::: "memory");
+        expand.run(lv, delta);
     }
-    __syncthreads();
+    lds_sync();
     const float alpha = a_gs[0] * b_alpha[0];
     for (int e = tid; e < 16 * MT * 8 * CB; e += nthreads) {
         const int r = e / (8 * CB), n = 2 * (e % (8 * CB));
@@ -679,11 +738,12 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
 template <int MT, int CB>
 hipError_t launch_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t* asfp, const uint8_t* bq,
                          const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out, hipStream_t s) {
-    // one wave of eight expands for a row or two, four for more
-    const int expand = p.M <= 2 ? 1 : 4, most = NW - expand;
+    // waves that stream and waves that expand: eight in all where two
+    // work-groups share a CU, else four and up to eight
+    const int expand = p.M <= 2 ? 1 : 4, most = MT == 4 ? NW : NW - expand;
     const int quads = (int)(pitch_wsf(p.K) / 32), per = (quads + most - 1) / most, nk = (quads + per - 1) / per;
     const int64_t grid = (p.N / 16 + CB - 1) / CB;
-    const int lds = (1 + nk) * 16 * MT * (16 * CB + 4) * 4;
+    const int lds = (1 + nk) * 16 * MT * (16 * CB + 4) * 4 + (int)p.M * lds_v_pitch(p.R) * 2;
     static std::atomic<int> lds_set[kMaxDevices];
     hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&lora_stream_kernel<MT, CB>), lds, lds_set);
     if (e != hipSuccess) return e;
@@ -695,7 +755,7 @@ hipError_t launch_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t*
 }  // namespace
 
 // Work-groups of the shrink before K is split: tiles x the adapters a tile can
-// hold x rank blocks; K ranges (at most 4, each at least 4 blocks of 64) bring
+// hold x rank blocks; K ranges (at most 8, each at least 4 blocks of 64) bring
 // the launch to about two work-groups per CU. Listed tiles hold few adapters,
 // which the host cannot know; counting one per tile, with room for the tiles
 // where two meet, is right for runs of rows.
@@ -749,8 +809,12 @@ hipError_t launch_lora_join(const LoraParams& p, hipStream_t s) {
 hipError_t launch_lora_reduce(const LoraParams& p, const float* partial, int ksplit, const float* a_gs,
                               const float* b_alpha, uint16_t* out, hipStream_t s) {
     const int64_t tiles = (p.M + kLoraRows - 1) / kLoraRows;
-    lora_reduce_kernel<<<(unsigned)(tiles * ((p.N + 31) / 32)), RT, 0, s>>>(p, (int)tiles, partial, ksplit, a_gs, b_alpha,
-                                                                            out);
+    const int lds = kLoraRows * lds_v_pitch(p.R) * 2;
+    static std::atomic<int> lds_set[kMaxDevices];
+    hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&lora_reduce_kernel), lds, lds_set);
+    if (e != hipSuccess) return e;
+    lora_reduce_kernel<<<(unsigned)(tiles * ((p.N + 31) / 32)), RT, lds, s>>>(p, (int)tiles, partial, ksplit, a_gs,
+                                                                              b_alpha, out);
     return hipGetLastError();
 }
 
