@@ -664,9 +664,9 @@ bool gated_shape_ok(int64_t T, int64_t H, int64_t I) {
 }
 
 // the three products' plans; workspace: dgu, then the backward's partial sums
-GatedPlan gated_fwd_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(T, I, kGatedBN / 2, 2 * I, H); }
-GatedPlan gated_dx_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(T, H, kGatedBN, H, 2 * I); }
-GatedPlan gated_dw_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(H, 2 * I, kGatedBN, 2 * I, T); }
+GatedPlan gated_fwd_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(kGatedFwd, T, I, kGatedBN / 2, 2 * I, H); }
+GatedPlan gated_dx_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(kGatedDx, T, H, kGatedBN, H, 2 * I); }
+GatedPlan gated_dw_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(kGatedDw, H, 2 * I, kGatedBN, 2 * I, T); }
 
 size_t gated_partial_bytes(const GatedPlan& g, int64_t rows, int64_t cols) {
     return g.ksplit > 1 ? align_up((size_t)g.ksplit * (size_t)rows * (size_t)cols * 4) : 0;

@@ -10,7 +10,7 @@
 // All three products run through one tile routine (below) on
 // v_mfma_f32_32x32x16_bf16. The two directions a reduction can lie in are
 // handled at the LDS read: an operand whose rows are contiguous along K
-// (x in the forward; [dg | du] and w13 in dx) is staged as rows of 64 bytes and
+// (x in the forward; [dg | du] and w13 in dx) is staged as its rows and
 // read with 16-byte loads; one whose rows are contiguous along M or N (w13 in
 // the forward; both operands of dw13) is staged as K rows and read with the
 // transposing LDS load (ds_read_b64_tr_b16: 16 lanes read 4 K rows of 16
@@ -22,9 +22,9 @@
 // wave w owns rows 32 MI (w / 4) .. and columns 64 (w % 4) .. +64. In the
 // forward a wave's 64 columns are 32 gate columns and the matching 32 up
 // columns, so both projections of an output meet in one lane and the
-// activation and the product are its epilogue. Stages of 32 K elements move
-// from memory to LDS by buffer loads that write LDS directly; a ring of
-// stages keeps several in flight. Every load is issued with either an offset
+// activation and the product are its epilogue. Stages of 32 or 64 K
+// elements move from memory to LDS by buffer loads that write LDS directly, into
+// a ring of stages. Every load is issued with either an offset
 // inside the operand or one beyond the buffer (which reads zeros): K tails,
 // rows beyond M and columns beyond N are zeros in both operands, so nothing
 // else (a NaN beside the tile) enters a sum.
@@ -48,18 +48,21 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) short4_t lds_short4;
 
 constexpr int NT = 512;                     // 8 waves
-constexpr int KS = 32;                      // K elements per stage
 constexpr int BN = kGatedBN;                // tile columns
-constexpr int B_BYTES = BN * KS * 2;        // 16 KB
 constexpr uint32_t kRsrcWord3 = 0x00020000u;
 constexpr uint32_t kBeyond = 0x80000000u;   // an offset outside every buffer: reads zeros
 constexpr int kWaves = NT / 64;
 
-template <int MI> constexpr int kABytes = 64 * MI * KS * 2;
-template <int MI> constexpr int kStage = kABytes<MI> + B_BYTES;
-// ring depth: what 128 KB hold, in powers of two
-template <int MI> constexpr int kStages = 4;
-template <int MI> constexpr int kLds = kStages<MI> * kStage<MI>;
+// K elements per stage: 64 where both operands are contiguous along K, whose
+// rows are then read 128 bytes at a time (64 bytes a row and stage cost dx 5 to
+// 20 %); else 32, which leaves room for more stages in flight (4 % of the forward
+// at 4096 rows)
+template <int MODE> constexpr int kKS = MODE == kGatedDx ? 64 : 32;
+template <int MODE, int MI> constexpr int kABytes = 64 * MI * kKS<MODE> * 2;
+template <int MODE, int MI> constexpr int kStage = kABytes<MODE, MI> + BN * kKS<MODE> * 2;
+// ring depth: 120 to 144 KB
+template <int MODE, int MI> constexpr int kStages = MODE == kGatedDx ? (MI == 4 ? 2 : 3) : (MI == 4 ? 4 : MI == 2 ? 5 : 6);
+template <int MODE, int MI> constexpr int kLds = kStages<MODE, MI> * kStage<MODE, MI>;
 
 constexpr int waitcnt_imm(int vm, int lgkm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4) | (lgkm << 8); }
 
@@ -125,9 +128,10 @@ __device__ __forceinline__ TileId map_tile(int b, int total, int mt, int ntn) {
 // contiguous along K, ld elements apart; true: K rows, contiguous along the
 // tile's W columns (column ranges given per 8-column chunk by `off`).
 //
-// LDS layout of a stage. K-contiguous: rows of 64 bytes, 16-byte chunk c of
-// row r stored at c ^ ((r >> 2) & 3), so the 16 rows a 16-lane group reads
-// cover all 64 banks. K-strided: 32 K rows of 2 W bytes; 16-byte chunk c of
+// LDS layout of a stage of KS K elements. K-contiguous: rows of 2 KS bytes,
+// 16-byte chunk c of row r stored at c ^ ((r >> 1) & 7) (KS = 64; c ^ ((r >> 2) &
+// 3) for 32), so the 16 rows a 16-lane group reads cover all 64 banks. K-strided:
+// KS K rows of 2 W bytes; 16-byte chunk c of
 // row k at c ^ swz(k), so the 4 K rows x 64 bytes that 32 lanes of a
 // transposing load read cover all banks.
 template <int W> __device__ __forceinline__ int kstrided_swz(int k) {
@@ -139,9 +143,12 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
     constexpr bool A_KS = MODE == kGatedDw;              // A contiguous along M
     constexpr bool B_KS = MODE != kGatedDx;              // B contiguous along N
     constexpr int AW = 64 * MI;                          // tile rows
-    constexpr int NS = kStages<MI>;
-    constexpr int STAGE = kStage<MI>;
-    constexpr int NA = MI == 4 ? 2 : 1, NB = 2, NL = NA + NB;   // loads per wave and stage
+    constexpr int KS = kKS<MODE>, SUB = KS / 16;         // substeps of a stage: one MFMA deep
+    constexpr int NS = kStages<MODE, MI>;
+    constexpr int STAGE = kStage<MODE, MI>, A_BYTES = kABytes<MODE, MI>;
+    // loads per wave and stage (a 64-row tile of 32 K has 4 KB of A: waves 4..7
+    // load what waves 0..3 do)
+    constexpr int AI = A_BYTES / 1024, NA = AI < kWaves ? 1 : AI / kWaves, NB = BN * KS * 2 / 1024 / kWaves, NL = NA + NB;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -158,15 +165,18 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
     const int nk = min(nk_all, kb + kper) - kb;
     const int kend = (int)min(p.K, (int64_t)(kb + nk) * KS);
 
+    // K-contiguous rows of a stage: 16-byte chunks, rows of a load, swizzle
+    constexpr int kChunks = KS / 8, kRows = 64 / kChunks;
+    auto row_swz = [](int r) { return KS == 64 ? (r >> 1) & 7 : (r >> 2) & 3; };
+
     // ---- per-lane load offsets (bytes from the stage's base) and K position ----
     const uint16_t* abase = p.a + (A_KS ? m0 : m0 * p.lda);
     const uint16_t* bbase = p.b + (MODE == kGatedDx ? n0 * p.ldb : MODE == kGatedDw ? n0 : 0);
-    uint32_t a_off[2], b_off[2];
-    int a_k[2], b_k[2];
+    uint32_t a_off[NA], b_off[NB];
+    int a_k[NA], b_k[NB];
 #pragma unroll
     for (int t = 0; t < NA; ++t) {
-        // (64-row tiles have 4 KB of A: waves 4..7 load what waves 0..3 do)
-        const int u = MI == 4 ? 2 * wave + t : MI == 2 ? wave : (wave & 3);
+        const int u = (NA * wave + t) % AI;
         if (A_KS) {
             constexpr int CH = AW / 8;                   // chunks per K row
             const int k = u * (64 / CH) + lane / CH, pc = lane % CH;
@@ -174,15 +184,15 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
             a_k[t] = k;
             a_off[t] = 8 * c < rows ? (uint32_t)(k * p.lda * 2 + 16 * c) : kBeyond;
         } else {
-            const int r = 16 * u + (lane >> 2);
-            const int c = (lane & 3) ^ ((r >> 2) & 3);
+            const int r = u * kRows + lane / kChunks;
+            const int c = (lane % kChunks) ^ row_swz(r);
             a_k[t] = 8 * c;
             a_off[t] = r < rows ? (uint32_t)(r * p.lda * 2 + 16 * c) : kBeyond;
         }
     }
 #pragma unroll
     for (int t = 0; t < NB; ++t) {
-        const int u = 2 * wave + t;
+        const int u = NB * wave + t;
         if (B_KS) {
             const int k = 2 * u + (lane >> 5), pc = lane & 31;
             const int c = pc ^ kstrided_swz<BN>(k);
@@ -199,8 +209,8 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
             }
             b_off[t] = ok ? (uint32_t)((k * p.ldb + col) * 2) : kBeyond;
         } else {
-            const int r = 16 * u + (lane >> 2);
-            const int c = (lane & 3) ^ ((r >> 2) & 3);
+            const int r = u * kRows + lane / kChunks;
+            const int c = (lane % kChunks) ^ row_swz(r);
             b_k[t] = 8 * c;
             b_off[t] = n0 + r < p.ncols ? (uint32_t)(r * p.ldb * 2 + 16 * c) : kBeyond;
         }
@@ -218,14 +228,14 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
         uint8_t* base = smem + st * STAGE;
 #pragma unroll
         for (int t = 0; t < NA; ++t) {
-            const int u = MI == 4 ? 2 * wave + t : MI == 2 ? wave : (wave & 3);
+            const int u = (NA * wave + t) % AI;
             const uint32_t off = a_k[t] < left ? a_off[t] : kBeyond;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + u * 1024), 16, off, 0, 0, 0);
         }
 #pragma unroll
         for (int t = 0; t < NB; ++t) {
             const uint32_t off = b_k[t] < left ? b_off[t] : kBeyond;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(base + kABytes<MI> + (2 * wave + t) * 1024), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(base + A_BYTES + (NB * wave + t) * 1024), 16,
                                                      off, 0, 0, 0);
         }
         pa += a_step;
@@ -241,17 +251,17 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
     const int tk = 8 * h + ((lane & 15) >> 2);                     // transposing loads: K row
     const int tc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);      // chunk inside a 32-column block
     uint32_t fa_off[MI], fb_off[2], fc_a, fc_b;
-    fc_a = (uint32_t)(16 * (h ^ ((l32 >> 2) & 3)));                // K-contiguous: chunk of substep 0
+    fc_a = (uint32_t)(16 * (h ^ row_swz(l32)));                // K-contiguous: chunk of substep 0
     fc_b = fc_a;
 #pragma unroll
     for (int i = 0; i < MI; ++i)
         fa_off[i] = A_KS ? (uint32_t)(tk * AW * 2 + 16 * ((4 * (wm * MI + i) + tc) ^ kstrided_swz<AW>(tk)) + 8 * (lane & 1))
-                         : (uint32_t)((wm * 32 * MI + 32 * i + l32) * 64);
+                         : (uint32_t)((wm * 32 * MI + 32 * i + l32) * 2 * KS);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-        fb_off[j] = kABytes<MI> +
+        fb_off[j] = A_BYTES +
                     (B_KS ? (uint32_t)(tk * BN * 2 + 16 * ((4 * (wn * 2 + j) + tc) ^ kstrided_swz<BN>(tk)) + 8 * (lane & 1))
-                          : (uint32_t)((wn * 64 + 32 * j + l32) * 64));
+                          : (uint32_t)((wn * 64 + 32 * j + l32) * 2 * KS));
 
     auto read_tr = [&](uint32_t off, int ldw, int s) -> bf16x8_t {
         const uint8_t* q = smem + off + s * 16 * ldw;
@@ -288,11 +298,11 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
     };
 
     // ---- main loop ------------------------------------------------------------------
-    // Step r: substep 0's fragments are in registers. Substep 1's are read
-    // under substep 0's MFMAs; then this wave's loads of stage r + 1 are
-    // waited for (those of the NS - 2 later stages stay in flight), the
-    // barrier makes everyone's visible and says that everyone has read stage
-    // r, whose buffer stage r + NS refills. Loads past the last stage read
+    // Step r: substep 0's fragments are in registers. Each next substep's are
+    // read under a substep's MFMAs; before the last substep's MFMAs this wave's
+    // loads of stage r + 1 are waited for (those of the NS - 2 later stages stay
+    // in flight), the barrier makes everyone's visible and says that everyone
+    // has read stage r, whose buffer stage r + NS refills. Loads past the last stage read
     // zeros, so the count of outstanding loads is the same in every step.
 #pragma unroll
     for (int s = 0; s < NS; ++s) issue(s);
@@ -307,24 +317,27 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
     constexpr int SPREAD = NM > 2 ? NM - 2 : 1;
     constexpr int PER = (NR + SPREAD - 1) / SPREAD;
     auto step = [&](int st) {
-        read(st, 1, 1);
-        mfma(0);
 #pragma unroll
-        for (int k = 0; k < NM; ++k) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);       // one MFMA
-            __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);     // its share of the LDS reads
+        for (int t = 0; t + 1 < SUB; ++t) {
+            read(st, t + 1, (t + 1) & 1);
+            mfma(t & 1);
+#pragma unroll
+            for (int k = 0; k < NM; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);       // one MFMA
+                __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);     // its share of the LDS reads
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 2) * NL, 0));
         lds_barrier();
         read(st + 1 == NS ? 0 : st + 1, 0, 0);
         issue(st);
-        mfma(1);
+        mfma((SUB - 1) & 1);
 #pragma unroll
         for (int k = 0; k < NM; ++k) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
-            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);       // one load into LDS
+            __builtin_amdgcn_sched_group_barrier(0x010, (NL + NM - 1) / NM, 0);     // loads into LDS
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -401,12 +414,30 @@ void gated_kernel(GatedGemm p) {
 
 // Partial sums of the forward, in chunk order, then the epilogue of the tile
 // routine. One thread per 4 columns.
-__global__ __launch_bounds__(256) void gated_reduce_kernel(GatedGemm p) {
+constexpr int kReduceThreads = 64;
+__global__ __launch_bounds__(kReduceThreads) void gated_reduce_kernel(GatedGemm p) {
     const int64_t I4 = p.I / 4, n = p.M * I4, plane = p.M * 2 * p.I;
-    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
+    for (int64_t t = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x; t < n; t += (int64_t)gridDim.x * kReduceThreads) {
         const int64_t row = t / I4, col = 4 * (t - row * I4);
-        const float4_t* src = reinterpret_cast<const float4_t*>(p.partial + row * 2 * p.I + col);
-        const float4_t g = sum_planes<8>(src, p.ksplit, plane / 4), u = sum_planes<8>(src + I4, p.ksplit, plane / 4);
+        // up to 16 loads in flight (gate and up of 8 chunks): a small batch has few
+        // threads here and is bound by their latency
+        const float* src = p.partial + row * 2 * p.I + col;
+        float4_t g = *reinterpret_cast<const float4_t*>(src), u = *reinterpret_cast<const float4_t*>(src + p.I);
+        for (int c0 = 1; c0 < p.ksplit; c0 += 8) {
+            float4_t vg[8], vu[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j < p.ksplit) {
+                    vg[j] = *reinterpret_cast<const float4_t*>(src + (c0 + j) * plane);
+                    vu[j] = *reinterpret_cast<const float4_t*>(src + (c0 + j) * plane + p.I);
+                }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j < p.ksplit) {
+                    g += vg[j];
+                    u += vu[j];
+                }
+        }
         float a[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) a[k] = silu_mul(g[k], u[k]);
@@ -479,9 +510,9 @@ template <int MODE, int MI>
 hipError_t launch_tiles(const GatedGemm& p, hipStream_t s) {
     const int64_t grid = (p.M + 64 * MI - 1) / (64 * MI) * ((p.ncols + p.tile_cols - 1) / p.tile_cols) * p.ksplit;
     static std::atomic<int> lds_set[kMaxDevices];
-    hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&gated_kernel<MODE, MI>), kLds<MI>, lds_set);
+    hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&gated_kernel<MODE, MI>), kLds<MODE, MI>, lds_set);
     if (e != hipSuccess) return e;
-    gated_kernel<MODE, MI><<<(unsigned)grid, NT, kLds<MI>, s>>>(p);
+    gated_kernel<MODE, MI><<<(unsigned)grid, NT, kLds<MODE, MI>, s>>>(p);
     return hipGetLastError();
 }
 
@@ -497,23 +528,28 @@ hipError_t launch_mode(const GatedGemm& p, int mi, hipStream_t s) {
 }  // namespace
 
 // Tile height and K chunks of a product M x cols x K (cols / tile_cols column
-// tiles): the pair with the smallest estimate of rounds x stages of one
-// work-group, plus the partial sums' traffic.
-GatedPlan gated_plan(int64_t M, int64_t ncols, int64_t tile_cols, int64_t outcols, int64_t K) {
-    const int64_t nk = (K + KS - 1) / KS, ntn = (ncols + tile_cols - 1) / tile_cols;
+// tiles): the pair with the smallest estimate, in microseconds, of rounds of
+// work-groups x (stages + start and epilogue), plus the partial sums' kernel
+// and traffic. A stage takes longer the more CUs are at work (they share the
+// caches and the power); its times are fits to sweeps over tile heights and
+// chunks at 1 to 4096 rows, where the choice is within a few percent of the
+// best one.
+GatedPlan gated_plan(int mode, int64_t M, int64_t ncols, int64_t tile_cols, int64_t outcols, int64_t K) {
+    const int64_t kstage = mode == kGatedDx ? kKS<kGatedDx> : kKS<kGatedFwd>;
+    const int64_t nk = (K + kstage - 1) / kstage, ntn = (ncols + tile_cols - 1) / tile_cols;
     GatedPlan best = {4, 1};
     double best_t = 1e30;
     for (int mi = 4; mi >= 1; mi /= 2) {
         const int64_t tiles = (M + 64 * mi - 1) / (64 * mi) * ntn;
-        // microseconds of one stage of a tile (matrix cores, or its loads)
-        const double stage = mi == 4 ? 0.60 : mi == 2 ? 0.34 : 0.25;
         for (int64_t ks = 1; ks <= 32 && ks <= nk; ++ks) {
             const int64_t per = (nk + ks - 1) / ks;
             if ((nk + per - 1) / per != ks) continue;        // no empty chunk
-            if (ks > 1 && tiles * ks > 512) break;
+            if (ks > 1 && tiles * ks > 256) break;
             const int64_t rounds = (tiles * ks + 255) / 256;
-            double t = rounds * (per * stage + 3.0);
-            if (ks > 1) t += 3.0 + (double)ks * M * outcols * 4 * 2 / 4e6;
+            const double f = tiles * ks < 256 ? tiles * ks / 256.0 : 1.0;
+            const double stage = mi == 4 ? 0.25 + 0.60 * f : mi == 2 ? 0.21 + 0.24 * f : 0.25 + 0.13 * f;   // of 32 K
+            double t = rounds * (per * (kstage / 32) * stage + 2.5);
+            if (ks > 1) t += 2.5 + (double)ks * M * outcols * 4 * 2 / 8e6;
             if (t < best_t) {
                 best_t = t;
                 best = {mi, (int)ks};
@@ -532,7 +568,8 @@ hipError_t launch_gated(const GatedGemm& p, int mode, int mi, hipStream_t s) {
 }
 
 hipError_t launch_gated_reduce(const GatedGemm& p, hipStream_t s) {
-    gated_reduce_kernel<<<grid_for(p.M * p.I / 4), 256, 0, s>>>(p);
+    const int64_t g = (p.M * p.I / 4 + kReduceThreads - 1) / kReduceThreads;
+    gated_reduce_kernel<<<(unsigned)(g < 16384 ? g : 16384), kReduceThreads, 0, s>>>(p);
     return hipGetLastError();
 }
 

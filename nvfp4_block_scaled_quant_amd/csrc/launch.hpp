@@ -330,7 +330,7 @@ struct GatedGemm {
     float* partial;            // out's; forward: (T, 2I))
 };
 struct GatedPlan { int mi, ksplit; };   // tiles of 64 mi rows, K chunks
-GatedPlan gated_plan(int64_t M, int64_t ncols, int64_t tile_cols, int64_t outcols, int64_t K);
+GatedPlan gated_plan(int mode, int64_t M, int64_t ncols, int64_t tile_cols, int64_t outcols, int64_t K);
 hipError_t launch_gated(const GatedGemm& p, int mode, int mi, hipStream_t s);
 // forward with ksplit > 1: sums, activation and stores
 hipError_t launch_gated_reduce(const GatedGemm& p, hipStream_t s);
