@@ -704,9 +704,10 @@ int nvfp4_gated_forward(const uint16_t* x, const uint16_t* w13, int64_t T, int64
     p.I = I;
     p.out = act;
     p.gate_up = gate_up;
+    p.mi = plan.mi;
     p.ksplit = plan.ksplit;
     p.partial = static_cast<float*>(workspace);
-    NVFP4_TRY(launch_gated(p, kGatedFwd, plan.mi, stream));
+    NVFP4_TRY(launch_gated_forward(p, stream));
     if (plan.ksplit > 1) NVFP4_TRY(launch_gated_reduce(p, stream));
     return NVFP4_OK;
 }
@@ -753,6 +754,7 @@ int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_
     gx.ncols = H;
     gx.tile_cols = kGatedBN;
     gx.out = dx;
+    gx.mi = px.mi;
     gx.ksplit = px.ksplit;
     gx.partial = reinterpret_cast<float*>(ws);
     ws += gated_partial_bytes(px, T, H);
@@ -765,17 +767,13 @@ int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_
     gw.ncols = 2 * I;
     gw.tile_cols = kGatedBN;
     gw.out = dw13;
+    gw.mi = pw.mi;
     gw.ksplit = pw.ksplit;
     gw.partial = reinterpret_cast<float*>(ws);
     NVFP4_TRY(launch_gated_dgu(d_act, gate_up, T, I, dgu, stream));
-    if (dx) {
-        NVFP4_TRY(launch_gated(gx, kGatedDx, px.mi, stream));
-        if (px.ksplit > 1) NVFP4_TRY(launch_gated_sum(gx.partial, px.ksplit, T * H, dx, stream));
-    }
-    if (dw13) {
-        NVFP4_TRY(launch_gated(gw, kGatedDw, pw.mi, stream));
-        if (pw.ksplit > 1) NVFP4_TRY(launch_gated_sum(gw.partial, pw.ksplit, H * 2 * I, dw13, stream));
-    }
+    NVFP4_TRY(launch_gated_backward(dx ? &gx : nullptr, dw13 ? &gw : nullptr, stream));
+    if (dx && px.ksplit > 1) NVFP4_TRY(launch_gated_sum(gx.partial, px.ksplit, T * H, dx, stream));
+    if (dw13 && pw.ksplit > 1) NVFP4_TRY(launch_gated_sum(gw.partial, pw.ksplit, H * 2 * I, dw13, stream));
     return NVFP4_OK;
 }
 

@@ -412,6 +412,23 @@ void gated_kernel(GatedGemm p) {
     gated_tile<MODE, MI>(p, blockIdx.x, smem);
 }
 
+// The backward's two products in one launch (they only share inputs): their
+// work-groups fill the GPU together, and neither waits for the other's last
+// ones. The first n_first work-groups are of the product with the longer tiles.
+template <int MODE>
+__device__ __forceinline__ void gated_any_tile(const GatedGemm& p, int block, uint8_t* smem) {
+    if (p.mi == 4) gated_tile<MODE, 4>(p, block, smem);
+    else if (p.mi == 2) gated_tile<MODE, 2>(p, block, smem);
+    else gated_tile<MODE, 1>(p, block, smem);
+}
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void gated_backward_kernel(GatedGemm gx, GatedGemm gw, int nx, int nw, bool dx_first) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const int b = blockIdx.x;
+    if (dx_first ? b < nx : b >= nw) gated_any_tile<kGatedDx>(gx, dx_first ? b : b - nw, smem);
+    else gated_any_tile<kGatedDw>(gw, dx_first ? b - nx : b, smem);
+}
+
 // Partial sums of the forward, in chunk order, then the epilogue of the tile
 // routine. One thread per 4 columns.
 constexpr int kReduceThreads = 64;
@@ -506,9 +523,16 @@ unsigned grid_for(int64_t n) {
     return (unsigned)(g < 1 ? 1 : g < 2048 ? g : 2048);
 }
 
+int64_t work_groups(const GatedGemm& p) {
+    return (p.M + 64 * p.mi - 1) / (64 * p.mi) * ((p.ncols + p.tile_cols - 1) / p.tile_cols) * p.ksplit;
+}
+
+template <int MODE>
+int lds_of(int mi) { return mi == 4 ? kLds<MODE, 4> : mi == 2 ? kLds<MODE, 2> : kLds<MODE, 1>; }
+
 template <int MODE, int MI>
 hipError_t launch_tiles(const GatedGemm& p, hipStream_t s) {
-    const int64_t grid = (p.M + 64 * MI - 1) / (64 * MI) * ((p.ncols + p.tile_cols - 1) / p.tile_cols) * p.ksplit;
+    const int64_t grid = work_groups(p);
     static std::atomic<int> lds_set[kMaxDevices];
     hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&gated_kernel<MODE, MI>), kLds<MODE, MI>, lds_set);
     if (e != hipSuccess) return e;
@@ -517,12 +541,19 @@ hipError_t launch_tiles(const GatedGemm& p, hipStream_t s) {
 }
 
 template <int MODE>
-hipError_t launch_mode(const GatedGemm& p, int mi, hipStream_t s) {
-    switch (mi) {
+hipError_t launch_mode(const GatedGemm& p, hipStream_t s) {
+    switch (p.mi) {
         case 1: return launch_tiles<MODE, 1>(p, s);
         case 2: return launch_tiles<MODE, 2>(p, s);
         default: return launch_tiles<MODE, 4>(p, s);
     }
+}
+
+// microseconds of one work-group of a product, the whole launch keeping a
+// share f of the CUs busy (see gated_plan)
+double tile_us(int mi, double f, int64_t k32) {
+    const double stage = mi == 4 ? 0.25 + 0.60 * f : mi == 2 ? 0.21 + 0.24 * f : 0.25 + 0.13 * f;
+    return k32 * stage + 2.5;
 }
 
 }  // namespace
@@ -546,9 +577,7 @@ GatedPlan gated_plan(int mode, int64_t M, int64_t ncols, int64_t tile_cols, int6
             if ((nk + per - 1) / per != ks) continue;        // no empty chunk
             if (ks > 1 && tiles * ks > 256) break;
             const int64_t rounds = (tiles * ks + 255) / 256;
-            const double f = tiles * ks < 256 ? tiles * ks / 256.0 : 1.0;
-            const double stage = mi == 4 ? 0.25 + 0.60 * f : mi == 2 ? 0.21 + 0.24 * f : 0.25 + 0.13 * f;   // of 32 K
-            double t = rounds * (per * (kstage / 32) * stage + 2.5);
+            double t = rounds * tile_us(mi, tiles * ks < 256 ? tiles * ks / 256.0 : 1.0, per * (kstage / 32));
             if (ks > 1) t += 2.5 + (double)ks * M * outcols * 4 * 2 / 8e6;
             if (t < best_t) {
                 best_t = t;
@@ -559,12 +588,19 @@ GatedPlan gated_plan(int mode, int64_t M, int64_t ncols, int64_t tile_cols, int6
     return best;
 }
 
-hipError_t launch_gated(const GatedGemm& p, int mode, int mi, hipStream_t s) {
-    switch (mode) {
-        case kGatedFwd: return launch_mode<kGatedFwd>(p, mi, s);
-        case kGatedDx: return launch_mode<kGatedDx>(p, mi, s);
-        default: return launch_mode<kGatedDw>(p, mi, s);
-    }
+hipError_t launch_gated_forward(const GatedGemm& p, hipStream_t s) { return launch_mode<kGatedFwd>(p, s); }
+
+hipError_t launch_gated_backward(const GatedGemm* gx, const GatedGemm* gw, hipStream_t s) {
+    if (!gw) return launch_mode<kGatedDx>(*gx, s);
+    if (!gx) return launch_mode<kGatedDw>(*gw, s);
+    const int lx = lds_of<kGatedDx>(gx->mi), lw = lds_of<kGatedDw>(gw->mi), lds = lx > lw ? lx : lw;
+    const int64_t nx = work_groups(*gx), nw = work_groups(*gw);
+    const bool dx_first = gx->mi * (gx->K / gx->ksplit) >= gw->mi * (gw->K / gw->ksplit);
+    static std::atomic<int> lds_set[kMaxDevices];
+    hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&gated_backward_kernel), lds, lds_set);
+    if (e != hipSuccess) return e;
+    gated_backward_kernel<<<(unsigned)(nx + nw), NT, lds, s>>>(*gx, *gw, (int)nx, (int)nw, dx_first);
+    return hipGetLastError();
 }
 
 hipError_t launch_gated_reduce(const GatedGemm& p, hipStream_t s) {

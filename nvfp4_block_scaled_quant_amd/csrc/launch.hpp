@@ -326,12 +326,15 @@ struct GatedGemm {
     int64_t M, K, ncols, tile_cols, I;
     uint16_t* out;             // act (T, I), dx (T, H) or dw13 (H, 2I)
     uint16_t* gate_up;         // forward: null, or (T, 2I)
-    int ksplit;                // > 1: chunk c writes partial[c] instead (rows as
-    float* partial;            // out's; forward: (T, 2I))
+    int mi, ksplit;            // tiles of 64 mi rows, K chunks; with ksplit > 1 chunk
+    float* partial;            // c writes partial[c] instead (rows as out's;
+                               // forward: (T, 2I))
 };
 struct GatedPlan { int mi, ksplit; };   // tiles of 64 mi rows, K chunks
 GatedPlan gated_plan(int mode, int64_t M, int64_t ncols, int64_t tile_cols, int64_t outcols, int64_t K);
-hipError_t launch_gated(const GatedGemm& p, int mode, int mi, hipStream_t s);
+hipError_t launch_gated_forward(const GatedGemm& p, hipStream_t s);
+// dx and dw13 in one launch, or (the other null) one of them
+hipError_t launch_gated_backward(const GatedGemm* gx, const GatedGemm* gw, hipStream_t s);
 // forward with ksplit > 1: sums, activation and stores
 hipError_t launch_gated_reduce(const GatedGemm& p, hipStream_t s);
 // out = bf16(sum over chunks of partial[c][0 .. n)), n % 4 == 0
