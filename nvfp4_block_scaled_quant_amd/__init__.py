@@ -408,31 +408,42 @@ def moe_forward_noalloc(x, topk_ids, topk_weights, w13, w13_sf, w13_alpha, w2, w
     return y
 
 
-class _NoGuard:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_NO_GUARD = _NoGuard()
-
-
-def _on(index):
-    """Makes the operands' device the current one for a call (the library
-    launches on the current device)."""
-    return _NO_GUARD if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
-
-
-def _operand(t, dtype, shape, name, dev):
-    """Address of an operand of exactly this dtype, shape and device (the
-    messages are _need's)."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev
+def _operand(t, dtype, shape, name, index):
+    """Address of an operand of exactly this dtype and shape on device `index`
+    (the messages are _need's)."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index
             or not t.is_contiguous()):
-        _need(t, dtype, name, len(shape), dev)
+        _need(t, dtype, name, len(shape), torch.device("cuda", index))
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
+
+
+def _scalar(t, name, index):
+    """Address of a tensor that holds (at least) one float32 on device `index`."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.get_device() != index
+            or not t.is_contiguous()):
+        _need(t, torch.float32, name, None, torch.device("cuda", index))
+    if t.numel() < 1:
+        raise ValueError(f"{name} must hold one float32")
+    return t.data_ptr()
+
+
+def _result(t, shape, dtype, name, index):
+    """A caller-given output (checked as an operand), or a new one on device
+    `index`."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=index)
+    _operand(t, dtype, shape, name, index)
+    return t
+
+
+def _scratch(t, nbytes, index):
+    """_workspace on device `index`: the tensor, its address and size."""
+    if t is None:
+        t = torch.empty(nbytes, dtype=torch.uint8, device=index)
+    else:
+        _workspace(t, nbytes, torch.device("cuda", index))
+    return t, t.data_ptr(), _nbytes(t)
 
 
 def gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, adapter_ids,
@@ -444,14 +455,15 @@ def gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, ad
     (L, R, K), lora_b bf16 (L, N, R), R a multiple of 8 up to 256; lora_scale
     float32 (L,); lora_rank: None, or int32 (L,): adapter a uses its first
     lora_rank[a] ranks."""
-    _need(x, torch.bfloat16, "x", 2)
-    dev = x.device
-    _need(bq, torch.uint8, "bq", 4, dev)
-    _need(lora_a, torch.bfloat16, "lora_a", 3, dev)
-    _need(a_gs, torch.float32, "a_gs", None, dev)
-    _need(b_alpha, torch.float32, "b_alpha", None, dev)
-    if a_gs.numel() < 1 or b_alpha.numel() < 1:
-        raise ValueError("gemm_lora: a_gs and b_alpha must hold one float32 each")
+    bf16, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
+    _need(x, bf16, "x", 2)
+    _need(bq, u8, "bq", 4)
+    _need(lora_a, bf16, "lora_a", 3)
+    index = x.get_device()
+    if index != torch._C._cuda_getDevice():                 # the library launches on the current device
+        with torch.cuda.device(index):
+            return gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, adapter_ids,
+                             lora_rank, out, workspace)
     M, K = x.shape
     blocks = bq.shape[0]
     N = blocks * 16
@@ -461,20 +473,17 @@ def gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, ad
     if R % 8 or not 8 <= R <= 256 or not 1 <= L <= 8192:
         raise ValueError("gemm_lora: R must be a multiple of 8 from 8 to 256, and L from 1 to 8192")
     steps = (K + 127) // 128                                # packed_shapes
-    u8, bf16 = torch.uint8, torch.bfloat16
-    ptrs = (_operand(aq, u8, (M, K // 2), "aq", dev), _operand(asf, u8, (M, K // 16), "asf", dev),
-            a_gs.data_ptr(), _operand(bq, u8, (blocks, 2 * steps, 16, 32), "bq", dev),
-            _operand(bsf, u8, (blocks, (steps + 3) // 4, 16, 32), "bsf", dev), b_alpha.data_ptr(),
-            x.data_ptr(), _operand(lora_a, bf16, (L, R, K), "lora_a", dev),
-            _operand(lora_b, bf16, (L, N, R), "lora_b", dev),
-            _operand(lora_scale, torch.float32, (L,), "lora_scale", dev),
-            None if lora_rank is None else _operand(lora_rank, torch.int32, (L,), "lora_rank", dev),
-            _operand(adapter_ids, torch.int32, (M,), "adapter_ids", dev))
-    with _on(dev.index):
-        out = _out(out, (M, N), bf16, dev, "out")
-        ws = _workspace(workspace, _lib.nvfp4_gemm_lora_workspace(M, N, K, L, R), dev)
-        _check(_lib.nvfp4_gemm_lora(*ptrs, M, N, K, L, R, out.data_ptr(), ws.data_ptr(), _nbytes(ws),
-                                    torch._C._cuda_getCurrentRawStream(dev.index)), "nvfp4_gemm_lora")
+    ptrs = (_operand(aq, u8, (M, K // 2), "aq", index), _operand(asf, u8, (M, K // 16), "asf", index),
+            _scalar(a_gs, "a_gs", index), _operand(bq, u8, (blocks, 2 * steps, 16, 32), "bq", index),
+            _operand(bsf, u8, (blocks, (steps + 3) // 4, 16, 32), "bsf", index),
+            _scalar(b_alpha, "b_alpha", index), x.data_ptr(), _operand(lora_a, bf16, (L, R, K), "lora_a", index),
+            _operand(lora_b, bf16, (L, N, R), "lora_b", index), _operand(lora_scale, f32, (L,), "lora_scale", index),
+            None if lora_rank is None else _operand(lora_rank, i32, (L,), "lora_rank", index),
+            _operand(adapter_ids, i32, (M,), "adapter_ids", index))
+    out = _result(out, (M, N), bf16, "out", index)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.nvfp4_gemm_lora_workspace(M, N, K, L, R), index)
+    _check(_lib.nvfp4_gemm_lora(*ptrs, M, N, K, L, R, out.data_ptr(), ws_ptr, ws_bytes,
+                                torch._C._cuda_getCurrentRawStream(index)), "nvfp4_gemm_lora")
     return out
 
 
@@ -497,14 +506,15 @@ def gated_forward(x, w13, act=None, gate_up=None, workspace=None):
     or a bf16 (T, 2I) tensor that receives the rounded gate | up values that
     gated_backward takes."""
     T, H, I = _gated_sizes(x, w13)
-    dev = x.device
-    gu = None if gate_up is None else _operand(gate_up, torch.bfloat16, (T, 2 * I), "gate_up", dev)
-    with _on(dev.index):
-        act = _out(act, (T, I), torch.bfloat16, dev, "act")
-        ws = _workspace(workspace, _lib.nvfp4_gated_workspace(T, H, I), dev)
-        _check(_lib.nvfp4_gated_forward(x.data_ptr(), w13.data_ptr(), T, H, I, act.data_ptr(), gu, ws.data_ptr(),
-                                        _nbytes(ws), torch._C._cuda_getCurrentRawStream(dev.index)),
-               "nvfp4_gated_forward")
+    index, bf16 = x.get_device(), torch.bfloat16
+    if index != torch._C._cuda_getDevice():                 # the library launches on the current device
+        with torch.cuda.device(index):
+            return gated_forward(x, w13, act, gate_up, workspace)
+    gu = None if gate_up is None else _operand(gate_up, bf16, (T, 2 * I), "gate_up", index)
+    act = _result(act, (T, I), bf16, "act", index)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.nvfp4_gated_workspace(T, H, I), index)
+    _check(_lib.nvfp4_gated_forward(x.data_ptr(), w13.data_ptr(), T, H, I, act.data_ptr(), gu, ws_ptr, ws_bytes,
+                                    torch._C._cuda_getCurrentRawStream(index)), "nvfp4_gated_forward")
     return act
 
 
@@ -514,23 +524,25 @@ def gated_backward(d_act, x, w13, gate_up, dx=None, dw13=None, need_dx=True, nee
     gate_up -> (dx bf16 (T, H), dw13 bf16 (H, 2I)). need_dx / need_dw13 =
     False skips that product and returns None in its place."""
     T, H, I = _gated_sizes(x, w13)
-    dev, bf16 = x.device, torch.bfloat16
-    d_ptr = _operand(d_act, bf16, (T, I), "d_act", dev)
-    gu_ptr = _operand(gate_up, bf16, (T, 2 * I), "gate_up", dev)
+    index, bf16 = x.get_device(), torch.bfloat16
+    if index != torch._C._cuda_getDevice():                 # the library launches on the current device
+        with torch.cuda.device(index):
+            return gated_backward(d_act, x, w13, gate_up, dx, dw13, need_dx, need_dw13, workspace)
+    d_ptr = _operand(d_act, bf16, (T, I), "d_act", index)
+    gu_ptr = _operand(gate_up, bf16, (T, 2 * I), "gate_up", index)
     if not (need_dx or need_dw13):
         raise ValueError("gated_backward: nothing to compute")
     if (dx is not None and not need_dx) or (dw13 is not None and not need_dw13):
         raise ValueError("gated_backward: an output is given for a gradient that is not computed")
-    with _on(dev.index):
-        if need_dx:
-            dx = _out(dx, (T, H), bf16, dev, "dx")
-        if need_dw13:
-            dw13 = _out(dw13, (H, 2 * I), bf16, dev, "dw13")
-        ws = _workspace(workspace, _lib.nvfp4_gated_backward_workspace(T, H, I), dev)
-        _check(_lib.nvfp4_gated_backward(d_ptr, x.data_ptr(), w13.data_ptr(), gu_ptr, T, H, I,
-                                         dx.data_ptr() if need_dx else None, dw13.data_ptr() if need_dw13 else None,
-                                         ws.data_ptr(), _nbytes(ws), torch._C._cuda_getCurrentRawStream(dev.index)),
-               "nvfp4_gated_backward")
+    if need_dx:
+        dx = _result(dx, (T, H), bf16, "dx", index)
+    if need_dw13:
+        dw13 = _result(dw13, (H, 2 * I), bf16, "dw13", index)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.nvfp4_gated_backward_workspace(T, H, I), index)
+    _check(_lib.nvfp4_gated_backward(d_ptr, x.data_ptr(), w13.data_ptr(), gu_ptr, T, H, I,
+                                     dx.data_ptr() if need_dx else None, dw13.data_ptr() if need_dw13 else None,
+                                     ws_ptr, ws_bytes, torch._C._cuda_getCurrentRawStream(index)),
+           "nvfp4_gated_backward")
     return dx, dw13
 
 

@@ -649,7 +649,6 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
     p.out_bf16 = out;
     p.partial = reinterpret_cast<float*>(ws + w.gemm + gemm_ws_partial_offset(M, K));
     p.lora = lo;
-    p.full_tiles = gemm_full_tiles(M, (N + kGemmBN - 1) / kGemmBN, 256, 0.58);
     NVFP4_TRY(launch_gemm(p, stream));
     if (p.ksplit > 1) NVFP4_TRY(launch_lora_reduce(lo, p.partial, p.ksplit, a_gs, b_alpha, out, stream));
     return NVFP4_OK;

@@ -131,22 +131,8 @@ void gemm_kernel(GemmParams p) {
     // N-tile, then K chunk (with ksplit > 1, chunk c sums the c-th range of K
     // steps into its own partial sums): the dense shapes have few tiles, which
     // the XCD order would put on one XCD.
-    // kGemmLora (one chunk): the first p.full_tiles row tiles are 256 rows high,
-    // the rest 128, so that the last round of work-groups is short.
-    int tile_idx, nt, chunk = 0, dbm = BM;
-    int64_t first_row = 0;
-    if (MODE == kGemmLora) {
-        const int n_full = p.full_tiles * ntn;
-        int b = blockIdx.x, mt = p.full_tiles;
-        if (b >= n_full) {
-            b -= n_full;
-            first_row = (int64_t)p.full_tiles * BM;
-            dbm = BM / 2;
-            mt = (int)((p.M - first_row + dbm - 1) / dbm);
-        }
-        tile_idx = b % mt;
-        nt = b / mt;
-    } else if (MODE == kGemmDense) {
+    int tile_idx, nt, chunk = 0;
+    if (kDense<MODE>) {
         const int mt = (int)((p.M + dense_tile_rows(p.M, N) - 1) / dense_tile_rows(p.M, N));
         tile_idx = blockIdx.x % mt;
         const int rest = blockIdx.x / mt;
@@ -162,8 +148,8 @@ void gemm_kernel(GemmParams p) {
     int expert, row_start, row_count;
     if (kDense<MODE>) {
         expert = 0;
-        if (MODE == kGemmDense) dbm = (int)dense_tile_rows(p.M, N);
-        row_start = (int)first_row + tile_idx * dbm;
+        const int dbm = (int)dense_tile_rows(p.M, N);
+        row_start = tile_idx * dbm;
         row_count = (int)min((int64_t)dbm, p.M - row_start);
         if (row_count <= 0) return;
     } else {
@@ -640,7 +626,11 @@ void gemm_kernel(GemmParams p) {
             const __amdgpu_buffer_rsrc_t rv = make_rsrc(lo.vs + (int64_t)row_start * 2 * lo.R, (int64_t)row_count * 4 * lo.R);
             const int lr = lane >> 3;       // a load covers 8 rows
             const uint32_t frag = 16 * (h ^ ((l32 >> 1) & 7));    // chunk of rank step 0; step t: ^ 32 t
-            for (int r0 = 0; r0 < lo.R; r0 += 64) {
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) any |= __builtin_amdgcn_ballot_w64(id[i] >= 0) != 0;
+            // (every load into LDS is waited for inside: an adapter follows it)
+            for (int r0 = 0; r0 < lo.R && any; r0 += 64) {
                 auto chunk_of = [&](int row) { return 8 * ((lane & 7) ^ ((row >> 1) & 7)); };
 #pragma unroll
                 for (int t = 0; t < MI; ++t) {
@@ -694,7 +684,7 @@ void gemm_kernel(GemmParams p) {
                             float16_t d;
 #pragma unroll
                             for (int r = 0; r < 16; ++r) d[r] = 0.0f;
-#pragma unroll 1
+#pragma unroll 2
                             for (int t = 0; t < steps; ++t) {
                                 const uint32_t at = frag ^ (32u * t);
                                 u32x4 b = *reinterpret_cast<const u32x4*>(br + j * 32 * 128 + at);
@@ -772,9 +762,8 @@ void gemm_kernel(GemmParams p) {
 template <int MODE>
 hipError_t launch_mode(const GemmParams& p, hipStream_t s) {
     const int64_t ntn = (MODE == kGemmL1) ? (p.I + 127) / 128 : (p.N + BN - 1) / BN;
-    const int64_t mt = MODE == kGemmLora ? p.full_tiles + (p.M - p.full_tiles * BM + BM / 2 - 1) / (BM / 2)
-                       : kDense<MODE>    ? (p.M + dense_tile_rows(p.M, p.N) - 1) / dense_tile_rows(p.M, p.N)
-                                         : p.max_tiles;
+    const int64_t mt = kDense<MODE> ? (p.M + dense_tile_rows(p.M, p.N) - 1) / dense_tile_rows(p.M, p.N)
+                                            : p.max_tiles;
     // grouped: whole groups of 8 tiles (one per XCD); dense: every (tile, N-tile, K chunk)
     const int64_t grid = kDense<MODE> ? mt * ntn * p.ksplit : (mt + 7) / 8 * 8 * ntn;
     if (grid <= 0) return hipSuccess;
@@ -832,27 +821,6 @@ int dense_ksplit(int64_t M, int64_t N, int64_t K) {
     // none is empty
     const int64_t per = (nk + s - 1) / s;
     return (int)((nk + per - 1) / per);
-}
-
-int64_t gemm_full_tiles(int64_t M, int64_t ntn, int64_t cus, double half) {
-    // r CUs are one full tile ahead after the full ones; half tiles fill the
-    // others first, then all
-    int64_t best = M / 256;
-    double best_t = 1e30;
-    for (int64_t f = (M + 255) / 256; f >= 0; --f) {
-        const int64_t rest = M - f * 256 > 0 ? (M - f * 256 + 127) / 128 * ntn : 0;
-        const int64_t n = f * ntn, q = n / cus, r = n % cus;
-        const int64_t room = r ? 2 * (cus - r) : 0;       // half tiles that fit beside the last full ones
-        double t;
-        if (r && rest <= room) t = (double)q + (rest > cus - r ? 2 * half : half > 1 ? half : 1.0);
-        else t = (double)q + (r ? (2 * half > 1 ? 2 * half : 1.0) : 0.0) + (double)((rest - room + cus - 1) / cus) * half;
-        if (f * 256 > M && f * 256 - M >= 128 && f > 0) t += 1e-3;   // a last tile that is half empty anyway
-        if (t < best_t - 1e-9) {
-            best_t = t;
-            best = f;
-        }
-    }
-    return best;
 }
 
 hipError_t launch_splitk_reduce(const float* partial, int ksplit, int64_t M, int64_t N, const float* a_gs,

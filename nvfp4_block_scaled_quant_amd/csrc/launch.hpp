@@ -273,7 +273,6 @@ struct GemmParams {
     // kGemmLora: the dense GEMM over the rows grouped by adapter, whose
     // epilogue adds the adapters (one K chunk)
     LoraParams lora;
-    int64_t full_tiles;        // kGemmLora: row tiles of 256 rows (the rest: 128)
 };
 
 hipError_t launch_gemm(const GemmParams& p, hipStream_t s);
@@ -290,11 +289,6 @@ __host__ __device__ inline int64_t dense_tile_rows(int64_t M, int64_t N) {
     const int64_t t256 = (M + kGemmBM - 1) / kGemmBM * ((N + kGemmBN - 1) / kGemmBN);
     return t256 < 128 ? kGemmBM / 2 : kGemmBM;
 }
-
-// Number of 256-row tiles of a GEMM of M rows and ntn column tiles, the rest
-// of the rows in 128-row tiles at `half` of a full tile's time, that ends
-// first when `cus` CUs take the full tiles and then the half ones.
-int64_t gemm_full_tiles(int64_t M, int64_t ntn, int64_t cus, double half);
 
 // out[m][n] = bf16((a_gs[0] * b_alpha[0]) * sum over chunks c, in order, of
 // partial[c][m][n]) for (M, N), N % 4 == 0.
