@@ -78,9 +78,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, 0x7FFFFFFF, kRsrcWord3);
 }
 
-// silu(g) * u in float32. e = e^-|g| is at most 1, so neither sign overflows.
+// e^-|g|, at most 1, so neither sign of g overflows. Below -200 it is zero
+// anyway; exp_split's own steps overflow beyond about 2^127.
+__device__ __forceinline__ float exp_neg_abs(float g) { return exp_split(fmaxf(-__builtin_fabsf(g), -200.0f)); }
+
+// silu(g) * u in float32.
 __device__ __forceinline__ float sigmoid_f32(float g) {
-    const float e = exp_split(-__builtin_fabsf(g));
+    const float e = exp_neg_abs(g);
     return (g >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
 }
 __device__ __forceinline__ float silu_mul(float g, float u) { return g * sigmoid_f32(g) * u; }
@@ -500,7 +504,7 @@ __global__ __launch_bounds__(256) void gated_dgu_kernel(const uint16_t* __restri
                 const float dv = bf16_to_f32((d[k] >> (16 * b)) & 0xFFFFu), gv = bf16_to_f32((g[k] >> (16 * b)) & 0xFFFFu);
                 const float uv = bf16_to_f32((u[k] >> (16 * b)) & 0xFFFFu);
                 // 1 - s = sigmoid(-g): formed without cancellation
-                const float e = exp_split(-__builtin_fabsf(gv)), q = __builtin_amdgcn_rcpf(1.0f + e);
+                const float e = exp_neg_abs(gv), q = __builtin_amdgcn_rcpf(1.0f + e);
                 const float s = gv >= 0.0f ? q : e * q, s1 = gv >= 0.0f ? e * q : q;
                 du[b] = dv * (gv * s);
                 dg[b] = dv * uv * (s * (1.0f + gv * s1));

@@ -132,6 +132,78 @@ def test_large_gates(nv):
     check_backward(d_act, x, w13, gate_up, dx, dw13)
 
 
+def test_gates_at_the_end_of_the_range(nv):
+    """Gates up to the largest finite bf16: silu is the gate or zero, the
+    derivative one or zero (the products stay in range with small up values)."""
+    import torch
+    T, H, I = 3, 16, 32
+    big = float(torch.finfo(torch.bfloat16).max)
+    gates = torch.tensor([big, -big, 2.4e38, -2.4e38, 1e38, -1e38, 300.0, -300.0] * 4)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    x[:, :2] = 1.0
+    w13 = torch.zeros((H, 2 * I), dtype=torch.bfloat16, device="cuda")
+    w13[0, :I] = gates.to(torch.bfloat16).cuda()
+    w13[1, I:] = 2.0 ** -10
+    gate_up = torch.empty((T, 2 * I), dtype=torch.bfloat16, device="cuda")
+    act = nv.gated_forward(x, w13, gate_up=gate_up)
+    on = (gates > 0).cuda()
+    ref = torch.where(on, gate_up[:, :I].double() * 2.0 ** -10, torch.zeros((), dtype=torch.float64, device="cuda"))
+    assert bool(((act.double() - ref).abs() <= HALF * ref.abs() + 1e-36).all())
+    d_act = torch.ones((T, I), dtype=torch.bfloat16, device="cuda")
+    ones = torch.zeros((H, 2 * I), dtype=torch.bfloat16, device="cuda")
+    ones[0, :I] = 1.0                               # dx[:, 0] = sum of dgate = 16 gates x 2^-10
+    dx, _ = nv.gated_backward(d_act, x, ones, gate_up, need_dw13=False)
+    assert bool((dx[:, 0].double() == 16 * 2.0 ** -10).all())
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 64, 32), (70, 272, 144), (300, 528, 1040)])
+def test_nothing_beside_the_outputs_is_written(nv, T, H, I):
+    """Outputs and a workspace of exactly the asked size inside larger buffers:
+    what lies before and behind them stays."""
+    import torch
+    x, w13, d_act = _inputs(T, H, I, 31)
+    lib = nv._lib
+    guard = 4096
+    bufs = []
+
+    def inside(shape, dtype=torch.bfloat16):
+        n = 1
+        for d in shape:
+            n *= d
+        size = n * torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((size + 2 * guard,), 0x5A, dtype=torch.uint8, device="cuda")
+        bufs.append((buf, size))
+        return buf[guard:guard + size].view(dtype).view(shape)
+
+    act, gate_up, dx, dw13 = inside((T, I)), inside((T, 2 * I)), inside((T, H)), inside((H, 2 * I))
+    ws = inside((lib.nvfp4_gated_workspace(T, H, I),), torch.uint8)
+    wsb = inside((lib.nvfp4_gated_backward_workspace(T, H, I),), torch.uint8)
+    nv.gated_forward(x, w13, act=act, gate_up=gate_up, workspace=ws)
+    nv.gated_backward(d_act, x, w13, gate_up, dx=dx, dw13=dw13, workspace=wsb)
+    check_forward(x, w13, act, gate_up)
+    check_backward(d_act, x, w13, gate_up, dx, dw13)
+    for buf, size in bufs:
+        assert bool((buf[:guard] == 0x5A).all()) and bool((buf[guard + size:] == 0x5A).all())
+
+
+def test_two_streams_at_once(nv):
+    """Calls in flight together on two streams, each with its own workspace."""
+    import torch
+    cases = [(33, 1024, 512, 41), (200, 2048, 256, 42)]
+    data = [_inputs(T, H, I, s) for T, H, I, s in cases]
+    alone = [nv.gated_forward(x, w).clone() for x, w, _ in data]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    out = [[], []]
+    for _ in range(8):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                out[k].append(nv.gated_forward(data[k][0], data[k][1]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(o, alone[k]) for o in out[k])
+
+
 @pytest.mark.parametrize("T,H,I", [(5, 528, 64), (300, 272, 144)])
 def test_rows_are_separate(nv, T, H, I):
     """NaN and infinity in one row of x and d_act stay in that row of act and

@@ -178,6 +178,53 @@ def test_streams_and_graph(nv, M):
         assert torch.equal(run(nv, t), out)
 
 
+@pytest.mark.parametrize("M,N,K,L,R", [(1, 16, 16, 1, 8), (50, 272, 528, 6, 72), (100, 528, 1040, 6, 24),
+                                       (600, 784, 272, 9, 136), (2100, 4112, 144, 5, 16)])
+def test_nothing_beside_the_output_is_written(nv, M, N, K, L, R):
+    """The output and a workspace of exactly the asked size inside larger
+    buffers: what lies before and behind them stays, and what the workspace
+    held does not matter."""
+    import torch
+    s = make(nv, M, N, K, L, R, 17)
+    guard = 4096
+    n_ws = nv._lib.nvfp4_gemm_lora_workspace(M, N, K, L, R)
+    for fill in (0x5A, 0xFF):                       # 0xFF: NaN in every float type
+        out = torch.full((2 * M * N + 2 * guard,), fill, dtype=torch.uint8, device="cuda")
+        ws = torch.full((n_ws + 2 * guard,), fill, dtype=torch.uint8, device="cuda")
+        y = out[guard:-guard].view(torch.bfloat16).view(M, N)
+        run(nv, s, out=y, workspace=ws[guard:-guard])
+        check(s, y)
+        for buf in (out, ws):
+            assert bool((buf[:guard] == fill).all()) and bool((buf[-guard:] == fill).all())
+
+
+@pytest.mark.parametrize("M", [1, 30, 64, 200, 900])
+def test_one_adapter_and_every_row_its_own(nv, M):
+    """The two ends: one adapter for all rows, and as many adapters as rows."""
+    import torch
+    for L, ids in ((1, torch.zeros(M)), (M, torch.randperm(M, generator=torch.Generator().manual_seed(M)))):
+        s = make(nv, M, 272, 272, L, 16, M + L, ids=ids)
+        check(s, run(nv, s))
+
+
+def test_two_streams_at_once(nv):
+    """Calls in flight together on two streams, each with its own workspace: one
+    that streams the weights, one tiled."""
+    import torch
+    sets = [make(nv, 40, 512, 2048, 6, 32, 51), make(nv, 300, 512, 1024, 4, 16, 52)]
+    alone = [run(nv, s).clone() for s in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    out = [[], []]
+    for _ in range(8):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                out[k].append(run(nv, sets[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(o, alone[k]) for o in out[k])
+
+
 def test_refusals(nv):
     import torch
     s = make(nv, 4, 32, 64, 2, 8, 1)
