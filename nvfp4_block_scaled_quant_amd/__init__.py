@@ -408,14 +408,17 @@ def moe_forward_noalloc(x, topk_ids, topk_weights, w13, w13_sf, w13_alpha, w2, w
     return y
 
 
-def _operand(t, dtype, shape, name, index):
-    """Address of an operand of exactly this dtype and shape on device `index`
-    (the messages are _need's)."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index
-            or not t.is_contiguous()):
-        _need(t, dtype, name, len(shape), torch.device("cuda", index))
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+def _operands(index, *specs):
+    """Addresses of operands (tensor, dtype, shape, name) of exactly these
+    dtypes and shapes on device `index` (the messages are _need's)."""
+    ptrs = []
+    for t, dtype, shape, name in specs:
+        if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index
+                or not t.is_contiguous()):
+            _need(t, dtype, name, len(shape), torch.device("cuda", index))
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        ptrs.append(t.data_ptr())
+    return ptrs
 
 
 def _scalar(t, name, index):
@@ -428,12 +431,12 @@ def _scalar(t, name, index):
     return t.data_ptr()
 
 
-def _result(t, shape, dtype, name, index):
-    """A caller-given output (checked as an operand), or a new one on device
-    `index`."""
+def _result(t, like, shape, name, index):
+    """A caller-given output (checked as an operand), or a new one of `like`'s
+    dtype and device."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=index)
-    _operand(t, dtype, shape, name, index)
+        return like.new_empty(shape)
+    _operands(index, (t, like.dtype, shape, name))
     return t
 
 
@@ -441,8 +444,8 @@ def _scratch(t, nbytes, index):
     """_workspace on device `index`: the tensor, its address and size."""
     if t is None:
         t = torch.empty(nbytes, dtype=torch.uint8, device=index)
-    else:
-        _workspace(t, nbytes, torch.device("cuda", index))
+        return t, t.data_ptr(), nbytes
+    _workspace(t, nbytes, torch.device("cuda", index))
     return t, t.data_ptr(), _nbytes(t)
 
 
@@ -473,16 +476,17 @@ def gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, ad
     if R % 8 or not 8 <= R <= 256 or not 1 <= L <= 8192:
         raise ValueError("gemm_lora: R must be a multiple of 8 from 8 to 256, and L from 1 to 8192")
     steps = (K + 127) // 128                                # packed_shapes
-    ptrs = (_operand(aq, u8, (M, K // 2), "aq", index), _operand(asf, u8, (M, K // 16), "asf", index),
-            _scalar(a_gs, "a_gs", index), _operand(bq, u8, (blocks, 2 * steps, 16, 32), "bq", index),
-            _operand(bsf, u8, (blocks, (steps + 3) // 4, 16, 32), "bsf", index),
-            _scalar(b_alpha, "b_alpha", index), x.data_ptr(), _operand(lora_a, bf16, (L, R, K), "lora_a", index),
-            _operand(lora_b, bf16, (L, N, R), "lora_b", index), _operand(lora_scale, f32, (L,), "lora_scale", index),
-            None if lora_rank is None else _operand(lora_rank, i32, (L,), "lora_rank", index),
-            _operand(adapter_ids, i32, (M,), "adapter_ids", index))
-    out = _result(out, (M, N), bf16, "out", index)
+    p_aq, p_asf, p_bq, p_bsf, p_a, p_b, p_scale, p_ids = _operands(
+        index, (aq, u8, (M, K // 2), "aq"), (asf, u8, (M, K // 16), "asf"),
+        (bq, u8, (blocks, 2 * steps, 16, 32), "bq"), (bsf, u8, (blocks, (steps + 3) // 4, 16, 32), "bsf"),
+        (lora_a, bf16, (L, R, K), "lora_a"), (lora_b, bf16, (L, N, R), "lora_b"),
+        (lora_scale, f32, (L,), "lora_scale"), (adapter_ids, i32, (M,), "adapter_ids"))
+    p_rank = None if lora_rank is None else _operands(index, (lora_rank, i32, (L,), "lora_rank"))[0]
+    p_gs, p_alpha = _scalar(a_gs, "a_gs", index), _scalar(b_alpha, "b_alpha", index)
+    out = _result(out, x, (M, N), "out", index)
     ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.nvfp4_gemm_lora_workspace(M, N, K, L, R), index)
-    _check(_lib.nvfp4_gemm_lora(*ptrs, M, N, K, L, R, out.data_ptr(), ws_ptr, ws_bytes,
+    _check(_lib.nvfp4_gemm_lora(p_aq, p_asf, p_gs, p_bq, p_bsf, p_alpha, x.data_ptr(), p_a, p_b, p_scale, p_rank,
+                                p_ids, M, N, K, L, R, out.data_ptr(), ws_ptr, ws_bytes,
                                 torch._C._cuda_getCurrentRawStream(index)), "nvfp4_gemm_lora")
     return out
 
@@ -506,12 +510,12 @@ def gated_forward(x, w13, act=None, gate_up=None, workspace=None):
     or a bf16 (T, 2I) tensor that receives the rounded gate | up values that
     gated_backward takes."""
     T, H, I = _gated_sizes(x, w13)
-    index, bf16 = x.get_device(), torch.bfloat16
+    index = x.get_device()
     if index != torch._C._cuda_getDevice():                 # the library launches on the current device
         with torch.cuda.device(index):
             return gated_forward(x, w13, act, gate_up, workspace)
-    gu = None if gate_up is None else _operand(gate_up, bf16, (T, 2 * I), "gate_up", index)
-    act = _result(act, (T, I), bf16, "act", index)
+    gu = None if gate_up is None else _operands(index, (gate_up, torch.bfloat16, (T, 2 * I), "gate_up"))[0]
+    act = _result(act, x, (T, I), "act", index)
     ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.nvfp4_gated_workspace(T, H, I), index)
     _check(_lib.nvfp4_gated_forward(x.data_ptr(), w13.data_ptr(), T, H, I, act.data_ptr(), gu, ws_ptr, ws_bytes,
                                     torch._C._cuda_getCurrentRawStream(index)), "nvfp4_gated_forward")
@@ -528,16 +532,15 @@ def gated_backward(d_act, x, w13, gate_up, dx=None, dw13=None, need_dx=True, nee
     if index != torch._C._cuda_getDevice():                 # the library launches on the current device
         with torch.cuda.device(index):
             return gated_backward(d_act, x, w13, gate_up, dx, dw13, need_dx, need_dw13, workspace)
-    d_ptr = _operand(d_act, bf16, (T, I), "d_act", index)
-    gu_ptr = _operand(gate_up, bf16, (T, 2 * I), "gate_up", index)
+    d_ptr, gu_ptr = _operands(index, (d_act, bf16, (T, I), "d_act"), (gate_up, bf16, (T, 2 * I), "gate_up"))
     if not (need_dx or need_dw13):
         raise ValueError("gated_backward: nothing to compute")
     if (dx is not None and not need_dx) or (dw13 is not None and not need_dw13):
         raise ValueError("gated_backward: an output is given for a gradient that is not computed")
     if need_dx:
-        dx = _result(dx, (T, H), bf16, "dx", index)
+        dx = _result(dx, x, (T, H), "dx", index)
     if need_dw13:
-        dw13 = _result(dw13, (H, 2 * I), bf16, "dw13", index)
+        dw13 = _result(dw13, x, (H, 2 * I), "dw13", index)
     ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.nvfp4_gated_backward_workspace(T, H, I), index)
     _check(_lib.nvfp4_gated_backward(d_ptr, x.data_ptr(), w13.data_ptr(), gu_ptr, T, H, I,
                                      dx.data_ptr() if need_dx else None, dw13.data_ptr() if need_dw13 else None,
