@@ -662,20 +662,20 @@ bool gated_shape_ok(int64_t T, int64_t H, int64_t I) {
     return T <= (int64_t)1 << 24 && H <= (int64_t)1 << 20 && I <= (int64_t)1 << 20;
 }
 
-// the three products' plans; workspace: dgu, then the backward's partial sums
-GatedPlan gated_fwd_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(kGatedFwd, T, I, kGatedBN / 2, 2 * I, H); }
-GatedPlan gated_dx_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(kGatedDx, T, H, kGatedBN, H, 2 * I); }
-GatedPlan gated_dw_plan(int64_t T, int64_t H, int64_t I) { return gated_plan(kGatedDw, H, 2 * I, kGatedBN, 2 * I, T); }
-
 size_t gated_partial_bytes(const GatedPlan& g, int64_t rows, int64_t cols) {
     return g.ksplit > 1 ? align_up((size_t)g.ksplit * (size_t)rows * (size_t)cols * 4) : 0;
+}
+
+// backward: [dgate | dup], then both products' partial sums
+size_t gated_backward_bytes(int64_t T, int64_t H, int64_t I, const GatedPlan& px, const GatedPlan& pw) {
+    return align_up((size_t)T * (size_t)I * 4) + gated_partial_bytes(px, T, H) + gated_partial_bytes(pw, H, 2 * I);
 }
 
 }  // namespace
 
 size_t nvfp4_gated_workspace(int64_t T, int64_t H, int64_t I) {
     if (!gated_shape_ok(T, H, I)) return 0;
-    const size_t n = T > 0 ? gated_partial_bytes(gated_fwd_plan(T, H, I), T, 2 * I) : 0;
+    const size_t n = T > 0 ? gated_partial_bytes(gated_forward_plan(T, H, I), T, 2 * I) : 0;
     return n ? n : kAlign;
 }
 
@@ -690,7 +690,7 @@ int nvfp4_gated_forward(const uint16_t* x, const uint16_t* w13, int64_t T, int64
         return NVFP4_EWORKSPACE;
     int dv = check_device();
     if (dv) return dv;
-    const GatedPlan plan = gated_fwd_plan(T, H, I);
+    const GatedPlan plan = gated_forward_plan(T, H, I);
     GatedGemm p = {};
     p.a = x;
     p.lda = H;
@@ -714,8 +714,9 @@ int nvfp4_gated_forward(const uint16_t* x, const uint16_t* w13, int64_t T, int64
 size_t nvfp4_gated_backward_workspace(int64_t T, int64_t H, int64_t I) {
     if (!gated_shape_ok(T, H, I)) return 0;
     if (T == 0) return kAlign;
-    return align_up((size_t)T * (size_t)I * 4) + gated_partial_bytes(gated_dx_plan(T, H, I), T, H) +
-           gated_partial_bytes(gated_dw_plan(T, H, I), H, 2 * I);
+    GatedPlan px, pw;
+    gated_backward_plan(T, H, I, px, pw);
+    return gated_backward_bytes(T, H, I, px, pw);
 }
 
 int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_t* w13, const uint16_t* gate_up,
@@ -725,10 +726,12 @@ int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_
     if (!gated_shape_ok(T, H, I)) return NVFP4_ESHAPE;
     if (!dx && !dw13) return NVFP4_EINVAL;
     if (!aligned(dx, 16) || !aligned(dw13, 16)) return NVFP4_EINVAL;
+    GatedPlan px = {}, pw = {};
     if (T > 0) {
         if (!d_act || !gate_up || (dx && !w13) || (dw13 && !x)) return NVFP4_EINVAL;
         if (!aligned(d_act, 16) || !aligned(x, 16) || !aligned(w13, 16) || !aligned(gate_up, 16)) return NVFP4_EINVAL;
-        if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < nvfp4_gated_backward_workspace(T, H, I))
+        gated_backward_plan(T, H, I, px, pw);
+        if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < gated_backward_bytes(T, H, I, px, pw))
             return NVFP4_EWORKSPACE;
     } else if (!dw13) {
         return NVFP4_OK;
@@ -739,7 +742,6 @@ int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_
         NVFP4_TRY(launch_zero_bytes(dw13, H * I * 4, stream));
         return NVFP4_OK;
     }
-    const GatedPlan px = gated_dx_plan(T, H, I), pw = gated_dw_plan(T, H, I);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     uint16_t* dgu = reinterpret_cast<uint16_t*>(ws);
     ws += align_up((size_t)T * (size_t)I * 4);

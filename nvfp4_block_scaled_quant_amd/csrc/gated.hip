@@ -554,7 +554,7 @@ hipError_t launch_mode(const GatedGemm& p, hipStream_t s) {
 }
 
 // microseconds of one work-group of a product, the whole launch keeping a
-// share f of the CUs busy (see gated_plan)
+// share f of the CUs busy (see the plans below)
 double tile_us(int mi, double f, int64_t k32) {
     const double stage = mi == 4 ? 0.25 + 0.60 * f : mi == 2 ? 0.21 + 0.24 * f : 0.25 + 0.13 * f;
     return k32 * stage + 2.5;
@@ -562,34 +562,79 @@ double tile_us(int mi, double f, int64_t k32) {
 
 }  // namespace
 
-// Tile height and K chunks of a product M x cols x K (cols / tile_cols column
-// tiles): the pair with the smallest estimate, in microseconds, of rounds of
-// work-groups x (stages + start and epilogue), plus the partial sums' kernel
-// and traffic. A stage takes longer the more CUs are at work (they share the
+// Tile height and K chunks of a product: the pair with the smallest estimate, in
+// microseconds, of the last work-group's end plus the partial sums' kernel and
+// traffic. A stage takes longer the more CUs are at work (they share the
 // caches and the power); its times are fits to sweeps over tile heights and
 // chunks at 1 to 4096 rows, where the choice is within a few percent of the
 // best one.
-GatedPlan gated_plan(int mode, int64_t M, int64_t ncols, int64_t tile_cols, int64_t outcols, int64_t K) {
-    const int64_t kstage = mode == kGatedDx ? kKS<kGatedDx> : kKS<kGatedFwd>;
-    const int64_t nk = (K + kstage - 1) / kstage, ntn = (ncols + tile_cols - 1) / tile_cols;
-    GatedPlan best = {4, 1};
-    double best_t = 1e30;
+namespace {
+
+struct Shape { int64_t M, ncols, tile_cols, outcols, K; int kstage; };
+
+// Visits (tile height, K chunks, work-groups, stages of 32 K of one, cost of the
+// partial sums) of a product.
+template <typename F>
+void each_plan(const Shape& s, int max_chunks, F f) {
+    const int64_t nk = (s.K + s.kstage - 1) / s.kstage, ntn = (s.ncols + s.tile_cols - 1) / s.tile_cols;
     for (int mi = 4; mi >= 1; mi /= 2) {
-        const int64_t tiles = (M + 64 * mi - 1) / (64 * mi) * ntn;
-        for (int64_t ks = 1; ks <= 32 && ks <= nk; ++ks) {
+        const int64_t tiles = (s.M + 64 * mi - 1) / (64 * mi) * ntn;
+        for (int64_t ks = 1; ks <= max_chunks && ks <= nk && (ks == 1 || tiles * ks <= 256); ++ks) {
             const int64_t per = (nk + ks - 1) / ks;
             if ((nk + per - 1) / per != ks) continue;        // no empty chunk
-            if (ks > 1 && tiles * ks > 256) break;
-            const int64_t rounds = (tiles * ks + 255) / 256;
-            double t = rounds * tile_us(mi, tiles * ks < 256 ? tiles * ks / 256.0 : 1.0, per * (kstage / 32));
-            if (ks > 1) t += 2.5 + (double)ks * M * outcols * 4 * 2 / 8e6;
-            if (t < best_t) {
-                best_t = t;
-                best = {mi, (int)ks};
-            }
+            f(GatedPlan{mi, (int)ks}, tiles * ks, per * (s.kstage / 32),
+              ks > 1 ? 2.5 + (double)ks * s.M * s.outcols * 4 * 2 / 8e6 : 0.0);
         }
     }
+}
+
+// End of n1 jobs of w1 and then n2 of w2 <= w1, dealt in this order to 256 CUs as
+// they get free.
+double makespan(int64_t n1, double w1, int64_t n2, double w2) {
+    const int64_t q = n1 / 256, r = n1 % 256;               // r CUs are one job ahead
+    if (n2 == 0) return (q + (r > 0)) * w1;
+    const double a = q * w1, b = a + (r ? w1 : 0.0);        // when the CUs get free: 256 - r at a, r at b
+    const double even = (a * (256 - r) + b * r + n2 * w2) / 256;
+    double t = even > b ? even : b;                         // no CU does better than the even share
+    for (;; t += w2 / 4) {
+        const int64_t fits = (256 - r) * (int64_t)((t - a) / w2 + 1e-9) + r * (int64_t)((t - b) / w2 + 1e-9);
+        if (fits >= n2) return t;
+    }
+}
+
+}  // namespace
+
+GatedPlan gated_forward_plan(int64_t T, int64_t H, int64_t I) {
+    GatedPlan best = {4, 1};
+    double best_t = 1e30;
+    each_plan({T, I, kGatedBN / 2, 2 * I, H, kKS<kGatedFwd>}, 32, [&](GatedPlan g, int64_t n, int64_t k32, double extra) {
+        const double t = makespan(n, tile_us(g.mi, n < 256 ? n / 256.0 : 1.0, k32), 0, 0.0) + extra;
+        if (t < best_t) {
+            best_t = t;
+            best = g;
+        }
+    });
     return best;
+}
+
+void gated_backward_plan(int64_t T, int64_t H, int64_t I, GatedPlan& px, GatedPlan& pw) {
+    // dx and dw13 share a launch: the pair whose work-groups, the longer ones
+    // first, fill the CUs best
+    const Shape sx = {T, H, kGatedBN, H, 2 * I, kKS<kGatedDx>}, sw = {H, 2 * I, kGatedBN, 2 * I, T, kKS<kGatedDw>};
+    double best_t = 1e30;
+    each_plan(sx, 8, [&](GatedPlan gx, int64_t nx, int64_t kx, double ex) {
+        if (gx.ksplit == 5 || gx.ksplit == 7) return;
+        each_plan(sw, 4, [&](GatedPlan gw, int64_t nw, int64_t kw, double ew) {
+            const double f = nx + nw < 256 ? (nx + nw) / 256.0 : 1.0;
+            const double wx = tile_us(gx.mi, f, kx), ww = tile_us(gw.mi, f, kw);
+            const double t = (wx >= ww ? makespan(nx, wx, nw, ww) : makespan(nw, ww, nx, wx)) + ex + ew;
+            if (t < best_t) {
+                best_t = t;
+                px = gx;
+                pw = gw;
+            }
+        });
+    });
 }
 
 hipError_t launch_gated_forward(const GatedGemm& p, hipStream_t s) { return launch_mode<kGatedFwd>(p, s); }
@@ -599,7 +644,7 @@ hipError_t launch_gated_backward(const GatedGemm* gx, const GatedGemm* gw, hipSt
     if (!gx) return launch_mode<kGatedDw>(*gw, s);
     const int lx = lds_of<kGatedDx>(gx->mi), lw = lds_of<kGatedDw>(gw->mi), lds = lx > lw ? lx : lw;
     const int64_t nx = work_groups(*gx), nw = work_groups(*gw);
-    const bool dx_first = gx->mi * (gx->K / gx->ksplit) >= gw->mi * (gw->K / gw->ksplit);
+    const bool dx_first = tile_us(gx->mi, 1.0, gx->K / gx->ksplit / 32) >= tile_us(gw->mi, 1.0, gw->K / gw->ksplit / 32);
     static std::atomic<int> lds_set[kMaxDevices];
     hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&gated_backward_kernel), lds, lds_set);
     if (e != hipSuccess) return e;

@@ -325,7 +325,8 @@ struct GatedGemm {
                                // forward: (T, 2I))
 };
 struct GatedPlan { int mi, ksplit; };   // tiles of 64 mi rows, K chunks
-GatedPlan gated_plan(int mode, int64_t M, int64_t ncols, int64_t tile_cols, int64_t outcols, int64_t K);
+GatedPlan gated_forward_plan(int64_t T, int64_t H, int64_t I);
+void gated_backward_plan(int64_t T, int64_t H, int64_t I, GatedPlan& dx, GatedPlan& dw13);
 hipError_t launch_gated_forward(const GatedGemm& p, hipStream_t s);
 // dx and dw13 in one launch, or (the other null) one of them
 hipError_t launch_gated_backward(const GatedGemm* gx, const GatedGemm* gw, hipStream_t s);
