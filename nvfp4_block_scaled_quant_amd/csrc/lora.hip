@@ -581,12 +581,9 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
 template <int MT, int CB>
 __global__ __launch_bounds__(MT == 4 ? NT + 256 : NT) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : MT == 4 ? 3 : 2)))
 void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict__ aqp,
-                                                         const uint8_t* __restrict__ asfp,
-                                                         const uint8_t* __restrict__ bq,
-                                                         const uint8_t* __restrict__ bsf,
-                                                         const float* __restrict__ a_gs,
-                                                         const float* __restrict__ b_alpha,
-                                                         uint16_t* __restrict__ out) {
+                        const uint8_t* __restrict__ asfp, const uint8_t* __restrict__ bq,
+                        const uint8_t* __restrict__ bsf, const float* __restrict__ a_gs,
+                        const float* __restrict__ b_alpha, uint16_t* __restrict__ out) {
     constexpr int LD = 16 * CB + 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
     float (*delta)[LD] = reinterpret_cast<float (*)[LD]>(dyn);                       // [16 MT]
@@ -610,7 +607,11 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
     };
     // buffer loads: one lane offset per operand, the rest in scalar offsets
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(bq, p.N * ldq), rws = make_rsrc(bsf, p.N * ldwsf);
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(aqp, (int64_t)16 * MT * ldq), ras = make_rsrc(asfp, (int64_t)16 * MT * ldwsf);
+    // (A has the row blocks that M has rows for; one further on, whose rows are
+    // not used, is the last of them again)
+    const int last = (int)((p.M - 1) / 16);
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(aqp, (int64_t)16 * (last + 1) * ldq);
+    const __amdgpu_buffer_rsrc_t ras = make_rsrc(asfp, (int64_t)16 * (last + 1) * ldwsf);
     const uint32_t w_off = (q >> 1) * kWqHalf + c * 32 + (q & 1) * 16, sf_off = c * 32 + q * 8, a_off = lane * 16;
     auto load_w = [&](int g, Group& r) {
 #pragma unroll
@@ -627,11 +628,12 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
     auto load_a = [&](int g, int half, Half& r) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            r.as[m] = __builtin_amdgcn_raw_buffer_load_b32(ras, sf_off, (uint32_t)(m * quads + g) * 512 + 4 * half, 0);
+            const int mb = min(m, last);
+            r.as[m] = __builtin_amdgcn_raw_buffer_load_b32(ras, sf_off, (uint32_t)(mb * quads + g) * 512 + 4 * half, 0);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int st = min(4 * g + 2 * half + u, steps - 1);
-                r.a[m][u] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_off, (uint32_t)(m * steps + st) * 1024, 0);
+                r.a[m][u] = __builtin_amdgcn_raw_buffer_load_b128(ra, a_off, (uint32_t)(mb * steps + st) * 1024, 0);
             }
         }
     };
