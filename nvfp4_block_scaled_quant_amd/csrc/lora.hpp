@@ -9,7 +9,8 @@ namespace nvfp4 {
 
 // Eight ranks k .. k + 7 of row `row` of v as hi + low in bf16: v is the sum of
 // its partial sums in order, hi its rounding and low the rounding of what is
-// left, so hi + low is within 2^-17 of v.
+// left, so hi + low is within 2^-17 of v. Where hi is infinite low is zero, so
+// that an infinite v stays one (infinity less itself is not a number).
 __device__ __forceinline__ void lora_v_operand(const LoraParams& lo, int64_t row, int k, u32x4& hi, u32x4& low) {
     typedef float float8_t __attribute__((ext_vector_type(8)));
     const float8_t v = sum_planes<kLoraMaxPlanes - 1>(reinterpret_cast<const float8_t*>(lo.v + row * lo.R + k), lo.planes,
@@ -18,7 +19,8 @@ __device__ __forceinline__ void lora_v_operand(const LoraParams& lo, int64_t row
     for (int e = 0; e < 4; ++e) {
         const float v0 = v[2 * e], v1 = v[2 * e + 1];
         hi[e] = pack_bf16x2_rne(v0, v1);
-        low[e] = pack_bf16x2_rne(v0 - bf16_to_f32(hi[e] & 0xFFFFu), v1 - bf16_to_f32(hi[e] >> 16));
+        const float h0 = bf16_to_f32(hi[e] & 0xFFFFu), h1 = bf16_to_f32(hi[e] >> 16);
+        low[e] = pack_bf16x2_rne(__builtin_isinf(h0) ? 0.0f : v0 - h0, __builtin_isinf(h1) ? 0.0f : v1 - h1);
     }
 }
 

@@ -138,6 +138,37 @@ def test_broken_requests_stay_alone(nv, M):
     assert bool(again[s["adapter_ids"] == 3][:, ::3].isnan().all())
 
 
+@pytest.mark.parametrize("M", [9, 64, 100, 700])
+def test_shrunk_rows_that_overflow_stay_infinite(nv, M):
+    """v = scale * x A^T beyond float32: the sum with B of one sign is that
+    infinity, in rows of the adapter alone."""
+    import torch
+    N, K = 272, 528
+    s = make(nv, M, N, K, 3, 8, M + 1, ids=torch.arange(M) % 4 - 1)
+    out = run(nv, s).clone()
+    check(s, out)
+    s["lora_a"][1] = s["x"][(s["adapter_ids"] == 1).nonzero()[0, 0]].sign()     # a positive sum in that row
+    s["lora_scale"][1] = 3e38
+    s["lora_b"][1] = s["lora_b"][1].abs() + 0.01
+    s["lora_b"][1, ::2] *= -1
+    again = run(nv, s)
+    rows = s["adapter_ids"] == 1
+    assert torch.equal(again[~rows], out[~rows])
+    row = again[rows][0].float()
+    assert bool((row[1::2] == float("inf")).all()) and bool((row[::2] == float("-inf")).all())
+
+
+@pytest.mark.parametrize("M", [33, 47, 48, 49])
+def test_row_blocks_of_a_partly_filled_tile(nv, M):
+    """Three of four 16-row blocks in use; a workspace of exactly the needed
+    size, bytes of NaN patterns before every run."""
+    import torch
+    N, K, L, R = 160, 1040, 4, 16
+    s = make(nv, M, N, K, L, R, M)
+    ws = torch.full((nv._lib.nvfp4_gemm_lora_workspace(M, N, K, L, R),), 0xFF, dtype=torch.uint8, device="cuda")
+    check(s, run(nv, s, workspace=ws))
+
+
 def test_a_request_does_not_depend_on_its_batch_mates_ids(nv):
     """The same rows beside other ids: rows whose id did not change keep their
     bits."""
