@@ -312,6 +312,18 @@ __device__ __forceinline__ void gated_tile(const GatedGemm& p, int block, uint8_
     for (int s = 0; s < NS; ++s) issue(s);
     __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 1) * NL, 0));
     lds_barrier();
+    // A wave whose rows or columns all lie outside the matrix only brings its
+    // share of the stages: the tile's other waves have the matrix cores alone
+    // (301 rows: 31.9 -> 31.2 us; 1001 x 4112 x 1360 backward: 63.3 -> 62.6).
+    if (wm * 32 * MI >= rows || n0 + wn * (MODE == kGatedFwd ? 32 : 64) >= p.ncols) {
+        for (int r = 0, st = 0; r < nk; ++r, st = st + 1 == NS ? 0 : st + 1) {
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 2) * NL, 0));
+            lds_barrier();
+            issue(st);
+        }
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+        return;
+    }
     read(0, 0, 0);
     // LDS reads of one substep, spread over its first MFMAs (one instruction
     // group each), so that the matrix core starts at once and the reads land
@@ -482,10 +494,11 @@ __global__ __launch_bounds__(256) void gated_sum_kernel(const float* __restrict_
 }
 
 // [dg | du] from the saved bf16 gate | up and d_act. It is rounded to bf16,
-// the matrix cores' operand type: independent relative errors of at most 2^-9
+// the matrix cores' operand type: independent relative errors of at most 2^-8
 // per element, which a sum over them carries as one such error, the size of
 // the outputs' own rounding. 8 columns a thread: 3 reads and 2 writes of 16
-// bytes, nothing to reuse, bound by memory.
+// bytes, nothing to reuse, bound by memory: 16 us at T 4096, I 2048 (84 MB,
+// 5.2 TB/s).
 __global__ __launch_bounds__(256) void gated_dgu_kernel(const uint16_t* __restrict__ d_act,
                                                         const uint16_t* __restrict__ gate_up, int64_t T, int64_t I,
                                                         uint16_t* __restrict__ dgu) {
