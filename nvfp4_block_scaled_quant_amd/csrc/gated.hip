@@ -22,16 +22,31 @@
 // wave w owns rows 32 MI (w / 4) .. and columns 64 (w % 4) .. +64. In the
 // forward a wave's 64 columns are 32 gate columns and the matching 32 up
 // columns, so both projections of an output meet in one lane and the
-// activation and the product are its epilogue. Stages of 32 or 64 K
-// elements move from memory to LDS by buffer loads that write LDS directly, into
-// a ring of stages. Every load is issued with either an offset
-// inside the operand or one beyond the buffer (which reads zeros): K tails,
-// rows beyond M and columns beyond N are zeros in both operands, so nothing
-// else (a NaN beside the tile) enters a sum.
+// activation and the product are its epilogue. Stages of 32 or 64 K elements
+// move from memory to LDS by buffer loads that write LDS directly, into a ring
+// of stages. Every load is issued with either an offset inside the operand or
+// one beyond the buffer (which reads zeros): K tails, rows beyond M and columns
+// beyond N are zeros in both operands, so nothing else (a NaN beside the tile)
+// enters a sum.
 //
 // Few tiles: K is cut into chunks that fill the GPU, each work-group writes
 // float32 partial sums, and a second kernel adds them in chunk order (the
 // result does not depend on scheduling) before the one rounding.
+//
+// What bounds it, and what it measured (H 7168, I 2048 but for the last line):
+//   T 1, 23      the weights, 58.7 MB once: 12.3 us (4.8 TB/s) and 13.5 us, and
+//                4 us for the chunks' sums
+//   T 301        the caches: every stage of a tile is 24 KB for 1/2 us of matrix
+//                work; 26 us + 6 us for the chunks' sums
+//   T 4096       the matrix cores at the clock that they get under load, 2.0 GHz:
+//                forward 195 us (1.23 PFLOP/s; no LDS bank conflicts, the
+//                matrix pipes busy 59 % of the cycles), both products of the
+//                backward 410 us (1.17 PFLOP/s)
+//   1001 rows, H 4112, I 1360   the ends: 499 tiles of unequal lengths on 256 CUs,
+//                and both widths end 16 columns into a tile; backward 59 us
+// Four waves of 128 x 128 outputs, which read LDS less often, were slower (218
+// us against 194 for the forward: one wave per SIMD leaves no one to issue while
+// it waits).
 #include <type_traits>
 
 #include "common.hpp"
@@ -82,7 +97,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base) {
 // anyway; exp_split's own steps overflow beyond about 2^127.
 __device__ __forceinline__ float exp_neg_abs(float g) { return exp_split(fmaxf(-__builtin_fabsf(g), -200.0f)); }
 
-// silu(g) * u in float32.
+// 1 / (1 + e^-g) by e^-|g|, and silu(g) * u, in float32.
 __device__ __forceinline__ float sigmoid_f32(float g) {
     const float e = exp_neg_abs(g);
     return (g >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
@@ -135,9 +150,8 @@ __device__ __forceinline__ TileId map_tile(int b, int total, int mt, int ntn) {
 // LDS layout of a stage of KS K elements. K-contiguous: rows of 2 KS bytes,
 // 16-byte chunk c of row r stored at c ^ ((r >> 1) & 7) (KS = 64; c ^ ((r >> 2) &
 // 3) for 32), so the 16 rows a 16-lane group reads cover all 64 banks. K-strided:
-// KS K rows of 2 W bytes; 16-byte chunk c of
-// row k at c ^ swz(k), so the 4 K rows x 64 bytes that 32 lanes of a
-// transposing load read cover all banks.
+// KS K rows of 2 W bytes; 16-byte chunk c of row k at c ^ swz(k), so the 4 K rows
+// x 64 bytes that 32 lanes of a transposing load read cover all banks.
 template <int W> __device__ __forceinline__ int kstrided_swz(int k) {
     return W >= 128 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
 }
@@ -430,7 +444,8 @@ void gated_kernel(GatedGemm p) {
 
 // The backward's two products in one launch (they only share inputs): their
 // work-groups fill the GPU together, and neither waits for the other's last
-// ones. The first n_first work-groups are of the product with the longer tiles.
+// ones. The product with the longer tiles comes first. (129 rows, H 2048, I 1408:
+// 31 -> 26 us for the whole backward; the same at 4096 rows.)
 template <int MODE>
 __device__ __forceinline__ void gated_any_tile(const GatedGemm& p, int block, uint8_t* smem) {
     if (p.mi == 4) gated_tile<MODE, 4>(p, block, smem);
@@ -446,7 +461,8 @@ void gated_backward_kernel(GatedGemm gx, GatedGemm gw, int nx, int nw, bool dx_f
 }
 
 // Partial sums of the forward, in chunk order, then the epilogue of the tile
-// routine. One thread per 4 columns.
+// routine. One thread per 4 columns: 3.9 us up to 23 rows (latency), 5.8 us at
+// 301 (25 MB of sums, which the caches still hold).
 constexpr int kReduceThreads = 64;
 __global__ __launch_bounds__(kReduceThreads) void gated_reduce_kernel(GatedGemm p) {
     const int64_t I4 = p.I / 4, n = p.M * I4, plane = p.M * 2 * p.I;
@@ -484,7 +500,8 @@ __global__ __launch_bounds__(kReduceThreads) void gated_reduce_kernel(GatedGemm 
     }
 }
 
-// out = bf16(sum of the chunks' partial sums, in chunk order), 4 columns a thread.
+// out = bf16(sum of the chunks' partial sums, in chunk order), 4 columns a
+// thread: 3.9 us at 129 x 2048 (latency).
 __global__ __launch_bounds__(256) void gated_sum_kernel(const float* __restrict__ partial, int ksplit, int64_t n4,
                                                         uint16_t* __restrict__ out) {
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n4; t += (int64_t)gridDim.x * 256) {

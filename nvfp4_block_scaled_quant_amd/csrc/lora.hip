@@ -21,6 +21,19 @@
 // fragments straight from memory has every lane in another row than its
 // neighbours, 16 bytes an address, and ran at a quarter of the rate. Ranges of
 // K are separate partial sums, added in order by the reader.
+//
+// What it measured (N 6144, K 7168; beside it the projection alone):
+//   1 row,     L 8,  R 16   shrink 6.5 us, stream 9.5: latency, the launches
+//   61 rows,   L 32, R 32   shrink 8.6 (15 MB of adapters, x and A), stream 18.5
+//                           (25 MB of weights; their conversion and that of
+//                           four row blocks of A: the vector units are active
+//                           half the cycles, the matrix pipes a fifth, and 64
+//                           CUs have no columns)
+//   256 rows,  L 6,  R 16   shrink 11, tiled GEMM 28, chunks' sum and expand 11
+//                           (nvfp4_gemm 38 in all)
+//   4093 rows, L 8,  R 64   sort 7, shrink 35 (59 MB of x and 16 MB of A read, 59
+//                           MB of f16 written), join 5, GEMM with the expand 320
+//                           (without it 292): the matrix cores
 #include <type_traits>
 
 #include "common.hpp"
@@ -300,9 +313,9 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
 }
 
 // ---------------------------------------------------------------------------
-// Rows by adapter. One work-group counts, scans and places; the rows of one
-// adapter come in no particular order (a row's result does not depend on its
-// place). Where at least 16 lanes of a wave share an adapter, as in runs of
+// Rows by adapter. One work-group counts, scans and places (7 us at 4093 rows,
+// 16 to 20 at 16384); the rows of one adapter come in no particular order (a
+// row's result does not depend on its place). Where at least 16 lanes of a wave share an adapter, as in runs of
 // rows, one of them counts for all: an LDS atomic takes one address at a time.
 constexpr int ST = 1024;
 
@@ -523,7 +536,8 @@ struct Expand {
 };
 
 // K chunks: out = bf16(alpha * (their sum, in order) + adapters), for one tile
-// of 64 listed rows and 32 columns.
+// of 64 listed rows and 32 columns. 11.3 us at 256 x 6144 and 5 chunks (31 MB of
+// sums, held by the caches; the sum alone takes 6.6).
 constexpr int RT = 256;
 __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles, const float* __restrict__ partial,
                                                          int ksplit, const float* __restrict__ a_gs,
@@ -577,7 +591,9 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
 // flight, and nothing of the projection goes through memory again: the waves'
 // sums meet in LDS (added in wave order), where the expand's are too. The other
 // waves do the expand meanwhile (loads return in order: in a wave that streams,
-// the adapters' operands would arrive after its weights).
+// the adapters' operands would arrive after its weights). 9.5 us for one row of
+// 6144 x 7168 (24.8 MB of weights: 2.6 TB/s, most of it start and end), 18.5 us
+// for 61 rows; the tiled form with its two further kernels took 49 us there.
 template <int MT, int CB>
 __global__ __launch_bounds__(MT == 4 ? NT + 256 : NT) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : MT == 4 ? 3 : 2)))
 void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict__ aqp,
