@@ -554,9 +554,9 @@ struct LoraLayout {
 LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     LoraLayout w = {};
     const int64_t m = M > 0 ? M : 1;
-    const bool stream = lora_streams(m);
+    const bool stream = lora_streams(m, N);
     w.ksplit = dense_ksplit(m, N, K);
-    w.planes = lora_planes(m, K, L, R);
+    w.planes = lora_planes(m, N, K, L, R);
     w.aqp = align_up((size_t)w.planes * (size_t)m * (size_t)R * 4);
     if (stream) {
         w.asfp = w.aqp + align_up((size_t)lora_stream_aq_bytes(m, K));
@@ -612,7 +612,7 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
     lo.N = N;
     lo.L = (int)L;
     lo.R = (int)R;
-    if (lora_streams(M)) {
+    if (lora_streams(M, N)) {
         NVFP4_TRY(launch_lora_shrink(lo, kLoraAsIs, nullptr, nullptr, aq, asf, ws + w.aqp, ws + w.asfp, nullptr, stream));
         NVFP4_TRY(launch_lora_stream(lo, ws + w.aqp, ws + w.asfp, bq, bsf, a_gs, b_alpha, out, stream));
         return NVFP4_OK;

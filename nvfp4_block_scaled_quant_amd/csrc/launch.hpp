@@ -181,9 +181,10 @@ enum GemmMode { kGemmDense = 0, kGemmL1 = 1, kGemmL2 = 2, kGemmLora = 3 };
 // scale[a] * x A_a^T are written only for rows that have an adapter and are
 // zero from the adapter's rank on: v, `planes` partial sums (planes, M, R) in
 // float32, and for the fused epilogue vs (M, 2R) bf16 in the listed order: the
-// rounding of each sum, then the rounding of what is left (2^-17 together). b is (L, N, R) bf16. perm / ids list the rows grouped by
-// adapter: row perm[i] has adapter ids[i] (-1: none); perm null: the rows in
-// order, and ids (M) the caller's (outside [0, L): none).
+// rounding of each sum, then the rounding of what is left (2^-17 together). b is
+// (L, N, R) bf16. perm / ids list the rows grouped by adapter: row perm[i] has
+// adapter ids[i] (-1: none); perm null: the rows in order, and ids (M) the
+// caller's (outside [0, L): none).
 struct LoraParams {
     const uint16_t* x;         // (M, K)
     const uint16_t* a;         // (L, R, K)
@@ -201,22 +202,30 @@ struct LoraParams {
 constexpr int64_t kLoraMaxRank = 256;
 constexpr int64_t kLoraMaxAdapters = 8192;
 constexpr int kLoraRows = 64;     // rows of a tile of the adapters' kernels
-constexpr int kLoraStreamRows = 64;
+constexpr int kLoraStreamRows = 512;
 constexpr int kLoraMaxPlanes = 8;
-// How the rows are listed by adapter: streamed batches not at all (their one
-// tile gathers its rows), small ones by the shrink's own work-groups, larger
-// ones by a launch of its own.
+// How the rows are listed by adapter: streamed batches not at all (each tile
+// gathers its rows), small ones by the shrink's own work-groups, larger ones by
+// a launch of its own.
 enum LoraOrder { kLoraAsIs = 0, kLoraRank = 1, kLoraSort = 2 };
 constexpr int kLoraRankRows = 256;
 // Whether M rows take the weight-streaming kernel (then A is laid out by
-// launch_lora_shrink) or the tiled GEMM.
-inline bool lora_streams(int64_t M) { return M <= kLoraStreamRows; }
+// launch_lora_shrink) or the tiled GEMM. Work-groups stream 32 columns for 64
+// rows, one on a CU: up to two of them a CU it is faster (128 rows of 2048 x
+// 4096, 128 work-groups: 21 us against 35; of 6144 x 7168, 384: 41.7 against
+// 44; 512 rows of 2048 x 2048, 512: 19 to 22 against 34), with three it is not
+// (160 rows of 6144 x 7168, 576: 59 against 44). More rows would read an
+// adapter too often, once per 64 rows that have it (1024 rows of 1024 x 4096
+// with 40 adapters at random: 63 against 41).
+inline bool lora_streams(int64_t M, int64_t N) {
+    return M <= kLoraRows || (M <= kLoraStreamRows && (M + 63) / 64 * ((N + 31) / 32) <= 512);
+}
 // bytes of the streaming kernel's A operand: rows padded to 16, K to whole
 // groups of four steps for the scales
 inline int64_t lora_stream_aq_bytes(int64_t M, int64_t K) { return (M + 15) / 16 * 16 * pitch_q(K); }
 inline int64_t lora_stream_asf_bytes(int64_t M, int64_t K) { return (M + 15) / 16 * 16 * pitch_wsf(K); }
 // number of partial sums (K ranges) of the shrink into v
-int lora_planes(int64_t M, int64_t K, int64_t L, int64_t R);
+int lora_planes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
 // perm (M), sid (M) from the caller's ids (kLoraSort)
 hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int64_t L, int32_t* perm, int32_t* sid, hipStream_t s);
 // p.v. order kLoraRank: also perm and sid (p.ids are the caller's, and
@@ -229,7 +238,7 @@ hipError_t launch_lora_join(const LoraParams& p, hipStream_t s);
 // out = bf16(alpha * sum over chunks of partial[c] (M, N) + adapters)
 hipError_t launch_lora_reduce(const LoraParams& p, const float* partial, int ksplit, const float* a_gs,
                               const float* b_alpha, uint16_t* out, hipStream_t s);
-// out = bf16(alpha * A W + adapters) for lora_streams(M)
+// out = bf16(alpha * A W + adapters) for lora_streams(M, N)
 hipError_t launch_lora_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t* asfp, const uint8_t* bq,
                               const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out,
                               hipStream_t s);

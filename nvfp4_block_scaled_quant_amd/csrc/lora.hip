@@ -3,9 +3,10 @@
 // with A_a (R, K) and B_a (N, R) in bf16. The product with A_a ("shrink") gives
 // v[m] = scale[a] x[m] A_a^T in float32; the product with B_a ("expand") is added
 // to the projection before its one rounding. Per batch size:
-//   up to 64 rows   shrink (beside it A laid out for streaming), then one kernel
+//   up to 64 rows, and up to 512 of narrow projections (lora_streams)
+//                   shrink (beside it A laid out for streaming), then one kernel
 //                   that streams the weights and adds the adapters
-//   more rows       the rows are listed by adapter, shrink (beside it A's f16
+//   else            the rows are listed by adapter, shrink (beside it A's f16
 //                   form), the tiled GEMM; the expand is in its epilogue, or,
 //                   where K is cut into chunks, in the kernel that adds them
 // A row's arithmetic does not depend on its place in a tile or on the other
@@ -585,8 +586,8 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
 }
 
 // ---------------------------------------------------------------------------
-// Up to 64 rows: the projection as a weight stream. A work-group owns 16 CB
-// columns and all rows; its first nk waves share K in whole groups of four
+// The projection as a weight stream. A work-group owns 16 CB columns and 16 MT
+// rows (all of them up to 64; more are parts of 64 rows); its first nk waves share K in whole groups of four
 // 128-element steps, so every wave has a kilobyte per step and column block in
 // flight, and nothing of the projection goes through memory again: the waves'
 // sums meet in LDS (added in wave order), where the expand's are too. The other
@@ -596,7 +597,7 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
 // for 61 rows; the tiled form with its two further kernels took 49 us there.
 template <int MT, int CB>
 __global__ __launch_bounds__(MT == 4 ? NT + 256 : NT) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : MT == 4 ? 3 : 2)))
-void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict__ aqp,
+void lora_stream_kernel(LoraParams p, int parts, int nk, int per, const uint8_t* __restrict__ aqp,
                         const uint8_t* __restrict__ asfp, const uint8_t* __restrict__ bq,
                         const uint8_t* __restrict__ bsf, const float* __restrict__ a_gs,
                         const float* __restrict__ b_alpha, uint16_t* __restrict__ out) {
@@ -610,8 +611,13 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
     const int c = lane & 15, q = lane >> 4;
     const int64_t ldq = pitch_q(p.K), ldwsf = pitch_wsf(p.K);
     const int steps = (int)(ldq / 64), quads = (int)(ldwsf / 32);
-    const int64_t blk0 = (int64_t)blockIdx.x * CB;              // 16-column blocks
-    const int64_t blocks = p.N / 16;
+    const int64_t blocks = p.N / 16;                            // 16-column blocks
+    // the row parts of one column range follow each other on one XCD, whose L2
+    // serves its weights to the second
+    const int64_t blk0 = (int64_t)(blockIdx.x / (8 * parts) * 8 + blockIdx.x % 8) * CB;
+    if (blk0 >= blocks) return;
+    const int blk_a = (int)(blockIdx.x / 8 % parts) * MT;       // its first 16-row block
+    const int row0 = 16 * blk_a, rows = min(16 * MT, (int)p.M - row0);
 
     struct Group {
         u32x4 w[CB][4];
@@ -644,7 +650,7 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
     auto load_a = [&](int g, int half, Half& r) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const int mb = min(m, last);
+            const int mb = min(blk_a + m, last);
             r.as[m] = __builtin_amdgcn_raw_buffer_load_b32(ras, sf_off, (uint32_t)(mb * quads + g) * 512 + 4 * half, 0);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -724,11 +730,11 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
         // the few instructions of the expand go ahead of the streams' many
         __builtin_amdgcn_s_setprio(3);
         const int t = tid - 64 * nk, nt = 64 * (nw - nk);
-        int id = lane < p.M ? p.ids[lane] : -1;
+        int id = lane < rows ? p.ids[row0 + lane] : -1;
         if (id >= p.L) id = -1;
         Expand<CB, LD> expand(p, id, blk0 * 16, wave - nk, nw - nk);
         // (rows without an adapter have no v: what is joined for them is not used)
-        join_v(p, (int)p.M, [](int r) { return r; }, t, nt, lv);
+        join_v(p, rows, [&](int r) { return row0 + r; }, t, nt, lv);
         for (int i = t; i < 16 * MT * LD; i += nt) (&delta[0][0])[i] = 0.0f;
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
@@ -742,13 +748,13 @@ void lora_stream_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict
     for (int e = tid; e < 16 * MT * 8 * CB; e += nthreads) {
         const int r = e / (8 * CB), n = 2 * (e % (8 * CB));
         const int64_t col = blk0 * 16 + n;
-        if (r >= p.M || col >= p.N) continue;
+        if (r >= rows || col >= p.N) continue;
         float s0 = red[0][r][n], s1 = red[0][r][n + 1];
         for (int w = 1; w < nk; ++w) {
             s0 += red[w][r][n];
             s1 += red[w][r][n + 1];
         }
-        *reinterpret_cast<uint32_t*>(out + (int64_t)r * p.N + col) =
+        *reinterpret_cast<uint32_t*>(out + (int64_t)(row0 + r) * p.N + col) =
             pack_bf16x2_rne(alpha * s0 + delta[r][n], alpha * s1 + delta[r][n + 1]);
     }
 }
@@ -760,12 +766,14 @@ hipError_t launch_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t*
     // work-groups share a CU, else four and up to eight
     const int expand = p.M <= 2 ? 1 : 4, most = MT == 4 ? NW : NW - expand;
     const int quads = (int)(pitch_wsf(p.K) / 32), per = (quads + most - 1) / most, nk = (quads + per - 1) / per;
-    const int64_t grid = (p.N / 16 + CB - 1) / CB;
-    const int lds = (1 + nk) * 16 * MT * (16 * CB + 4) * 4 + (int)p.M * lds_v_pitch(p.R) * 2;
+    const int64_t cols = (p.N / 16 + CB - 1) / CB, parts = (p.M + 16 * MT - 1) / (16 * MT);
+    const int64_t grid = parts == 1 ? cols : (cols + 7) / 8 * 8 * parts;
+    const int rows = (int)(p.M < 16 * MT ? p.M : 16 * MT);
+    const int lds = (1 + nk) * 16 * MT * (16 * CB + 4) * 4 + rows * lds_v_pitch(p.R) * 2;
     static std::atomic<int> lds_set[kMaxDevices];
     hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&lora_stream_kernel<MT, CB>), lds, lds_set);
     if (e != hipSuccess) return e;
-    lora_stream_kernel<MT, CB><<<(unsigned)grid, 64 * (nk + expand), lds, s>>>(p, nk, per, aqp, asfp, bq, bsf, a_gs,
+    lora_stream_kernel<MT, CB><<<(unsigned)grid, 64 * (nk + expand), lds, s>>>(p, (int)parts, nk, per, aqp, asfp, bq, bsf, a_gs,
                                                                               b_alpha, out);
     return hipGetLastError();
 }
@@ -776,12 +784,14 @@ hipError_t launch_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t*
 // hold x rank blocks; K ranges (at most 8, each at least 4 blocks of 64) bring
 // the launch to about two work-groups per CU. Listed tiles hold few adapters,
 // which the host cannot know; counting one per tile, with room for the tiles
-// where two meet, is right for runs of rows.
-int lora_planes(int64_t M, int64_t K, int64_t L, int64_t R) {
+// where two meet, is right for runs of rows. A streamed tile's rows are not
+// listed: each may have its own.
+int lora_planes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     const int64_t tiles = (M + kLoraRows - 1) / kLoraRows, rbs = (R + kRankBlock - 1) / kRankBlock;
-    const int64_t here = tiles > 1 ? 1 : (M < L ? M : L);
+    const int64_t rows = M < kLoraRows ? M : kLoraRows;
+    const int64_t here = lora_streams(M, N) ? (rows < L ? rows : L) : 1;
     const int64_t nb = (K + 63) / 64;
-    int64_t n = (tiles > 1 ? 416 : 512) / (tiles * rbs * here);
+    int64_t n = (lora_streams(M, N) ? 512 : 416) / (tiles * rbs * here);
     if (n > nb / 4) n = nb / 4;
     if (n > kLoraMaxPlanes) n = kLoraMaxPlanes;
     if (n < 1) n = 1;
@@ -797,9 +807,10 @@ hipError_t launch_lora_sort(const int32_t* ids, int64_t M, int64_t L, int32_t* p
 hipError_t launch_lora_shrink(const LoraParams& p, LoraOrder order, int32_t* perm, int32_t* sid, const uint8_t* aq,
                               const uint8_t* asf, uint8_t* aqp, uint8_t* asfp, uint16_t* ah, hipStream_t s) {
     const int64_t tiles = (p.M + kLoraRows - 1) / kLoraRows, rbs = (p.R + kRankBlock - 1) / kRankBlock;
-    // work-groups that share a tile's adapters: as many as it can hold when it
-    // is the only tile; listed rows put few adapters into a tile
-    int64_t slots = p.M < p.L ? p.M : p.L;
+    // work-groups that share a tile's adapters: as many as it can hold; listed
+    // rows put few adapters into a tile
+    int64_t slots = p.M < kLoraRows ? p.M : kLoraRows;
+    if (slots > p.L) slots = p.L;
     const int64_t most = tiles <= 4 ? 8 : tiles <= 16 ? 4 : tiles <= 64 ? 2 : 1;
     if (order != kLoraAsIs && slots > most) slots = most;
     const int64_t blocks = tiles * slots * p.planes * rbs;

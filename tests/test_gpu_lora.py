@@ -85,7 +85,11 @@ def check(s, out):
     (64, 512, 4096, 64, 128), (65, 528, 512, 65, 16), (128, 512, 256, 3, 256), (129, 1040, 528, 9, 40),
     (256, 768, 640, 6, 16), (300, 512, 256, 20, 64), (513, 6144, 512, 2, 16), (1300, 6144, 144, 7, 136),
     (4093, 4096, 128, 300, 8), (31, 1040, 2064, 9, 24), (32, 16, 7168, 2, 256), (8, 528, 144, 8, 64),
-    (16, 1296, 12304, 3, 8), (700, 1024, 2048, 48, 32), (5000, 256, 128, 8192, 8)])
+    (16, 1296, 12304, 3, 8), (700, 1024, 2048, 48, 32), (5000, 256, 128, 8192, 8),
+    # narrow projections of several 64-row parts, and the widths beyond which
+    # such batches are tiled instead
+    (512, 2048, 528, 4, 16), (449, 2064, 272, 12, 24), (200, 16, 16, 5, 8), (128, 8192, 272, 4, 16), (128, 8224, 272, 4, 16),
+    (65, 8224, 272, 65, 16), (129, 5488, 528, 9, 40), (255, 4112, 640, 6, 256), (300, 3296, 512, 20, 64)])
 def test_random_ids(nv, M, N, K, L, R):
     import torch
     s = make(nv, M, N, K, L, R, M + N + K + L + R)
@@ -95,8 +99,8 @@ def test_random_ids(nv, M, N, K, L, R):
     assert torch.equal(run(nv, s), out)
 
 
-@pytest.mark.parametrize("M", [7, 64, 200, 1500])
-def test_runs_of_rows(nv, M):
+@pytest.mark.parametrize("M,N", [(7, 528), (64, 528), (200, 528), (200, 4144), (1500, 528)])
+def test_runs_of_rows(nv, M, N):
     """Requests as runs of rows, some without an adapter; ranks of their own,
     0 and beyond R among them."""
     import torch
@@ -105,24 +109,24 @@ def test_runs_of_rows(nv, M):
     ids = torch.full((M,), -1)
     for n, (a, b) in enumerate(zip(cuts[:-1], cuts[1:])):
         ids[a:b] = (n * 5) % (L + 1) - 1
-    s = make(nv, M, 528, 1040, L, R, M, ids=ids, ranks=[48, 0, 7, 33, 100, -3])
+    s = make(nv, M, N, 1040, L, R, M, ids=ids, ranks=[48, 0, 7, 33, 100, -3])
     check(s, run(nv, s))
 
 
-@pytest.mark.parametrize("M", [3, 40, 300])
-def test_no_row_has_an_adapter(nv, M):
+@pytest.mark.parametrize("M,N", [(3, 256), (40, 256), (300, 256), (100, 8224), (600, 256)])
+def test_no_row_has_an_adapter(nv, M, N):
     """Only the shared projection: what nvfp4_gemm gives up to summation order."""
     import torch
-    s = make(nv, M, 256, 512, 4, 16, M, ids=torch.tensor([-1, 4, 2 ** 30, -2 ** 31]).repeat(M)[:M])
+    s = make(nv, M, N, 512, 4, 16, M, ids=torch.tensor([-1, 4, 2 ** 30, -2 ** 31]).repeat(M)[:M])
     check(s, run(nv, s))
 
 
-@pytest.mark.parametrize("M", [9, 64, 100, 700])
-def test_broken_requests_stay_alone(nv, M):
+@pytest.mark.parametrize("M,N", [(9, 272), (64, 272), (100, 272), (100, 8224), (700, 272)])
+def test_broken_requests_stay_alone(nv, M, N):
     """NaN and infinity in one request's adapter, and in what is stored beyond
     the ranks, reach no other row."""
     import torch
-    L, R, N, K = 5, 24, 272, 528
+    L, R, K = 5, 24, 528
     s = make(nv, M, N, K, L, R, 3 * M, ids=torch.arange(M) % (L + 1) - 1, ranks=[24, 9, 16, 24, 1])
     out = run(nv, s).clone()
     check(s, out)
@@ -138,12 +142,12 @@ def test_broken_requests_stay_alone(nv, M):
     assert bool(again[s["adapter_ids"] == 3][:, ::3].isnan().all())
 
 
-@pytest.mark.parametrize("M", [9, 64, 100, 700])
-def test_shrunk_rows_that_overflow_stay_infinite(nv, M):
+@pytest.mark.parametrize("M,N", [(9, 272), (64, 272), (100, 272), (100, 8224), (700, 272)])
+def test_shrunk_rows_that_overflow_stay_infinite(nv, M, N):
     """v = scale * x A^T beyond float32: the sum with B of one sign is that
     infinity, in rows of the adapter alone."""
     import torch
-    N, K = 272, 528
+    K = 528
     s = make(nv, M, N, K, 3, 8, M + 1, ids=torch.arange(M) % 4 - 1)
     out = run(nv, s).clone()
     check(s, out)
@@ -182,10 +186,10 @@ def test_a_request_does_not_depend_on_its_batch_mates_ids(nv):
     assert torch.equal(run(nv, s)[same], out[same])
 
 
-@pytest.mark.parametrize("M", [1, 20, 150])
-def test_streams_and_graph(nv, M):
+@pytest.mark.parametrize("M,N", [(1, 512), (20, 512), (150, 512), (150, 5488), (600, 512)])
+def test_streams_and_graph(nv, M, N):
     import torch
-    N, K, L, R = 512, 1024, 4, 16
+    K, L, R = 1024, 4, 16
     s = make(nv, M, N, K, L, R, 5)
     out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
     ws = torch.empty((nv._lib.nvfp4_gemm_lora_workspace(M, N, K, L, R),), dtype=torch.uint8, device="cuda")
@@ -209,7 +213,7 @@ def test_streams_and_graph(nv, M):
         assert torch.equal(run(nv, t), out)
 
 
-@pytest.mark.parametrize("M,N,K,L,R", [(1, 16, 16, 1, 8), (50, 272, 528, 6, 72), (100, 528, 1040, 6, 24),
+@pytest.mark.parametrize("M,N,K,L,R", [(1, 16, 16, 1, 8), (50, 272, 528, 6, 72), (100, 528, 1040, 6, 24), (100, 8224, 272, 6, 24),
                                        (600, 784, 272, 9, 136), (2100, 4112, 144, 5, 16)])
 def test_nothing_beside_the_output_is_written(nv, M, N, K, L, R):
     """The output and a workspace of exactly the asked size inside larger
@@ -242,7 +246,7 @@ def test_two_streams_at_once(nv):
     """Calls in flight together on two streams, each with its own workspace: one
     that streams the weights, one tiled."""
     import torch
-    sets = [make(nv, 40, 512, 2048, 6, 32, 51), make(nv, 300, 512, 1024, 4, 16, 52)]
+    sets = [make(nv, 40, 512, 2048, 6, 32, 51), make(nv, 600, 512, 1024, 4, 16, 52)]
     alone = [run(nv, s).clone() for s in sets]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
