@@ -612,6 +612,10 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
     lo.N = N;
     lo.L = (int)L;
     lo.R = (int)R;
+    if (lora_is_token(M, N, K, R)) {
+        NVFP4_TRY(launch_lora_token(lo, aq, asf, bq, bsf, a_gs, b_alpha, out, stream));
+        return NVFP4_OK;
+    }
     if (lora_streams(M, N)) {
         NVFP4_TRY(launch_lora_shrink(lo, kLoraAsIs, nullptr, nullptr, aq, asf, ws + w.aqp, ws + w.asfp, nullptr, stream));
         NVFP4_TRY(launch_lora_stream(lo, ws + w.aqp, ws + w.asfp, bq, bsf, a_gs, b_alpha, out, stream));

@@ -220,6 +220,15 @@ constexpr int kLoraRankRows = 256;
 inline bool lora_streams(int64_t M, int64_t N) {
     return M <= kLoraRows || (M <= kLoraStreamRows && (M + 63) / 64 * ((N + 31) / 32) <= 512);
 }
+constexpr int kLoraTokenRows = 4;
+// Whether one launch does it all: a few rows of small adapters (every
+// work-group reads their A_a: at most half a megabyte, and four turns of its
+// eight waves), one round of work-groups. One row of 6144 x 7168, R 8 to 32: 14
+// to 16.5 us, in two launches 16 to 17.5; twice as many turns (4 rows of R 64)
+// 20 against 17, two rounds (N 12288, K 4096) 18.4 against 17.3.
+inline bool lora_is_token(int64_t M, int64_t N, int64_t K, int64_t R) {
+    return M <= kLoraTokenRows && N <= 8192 && M * R <= 128 && M * R * K <= 262144;
+}
 // bytes of the streaming kernel's A operand: rows padded to 16, K to whole
 // groups of four steps for the scales
 inline int64_t lora_stream_aq_bytes(int64_t M, int64_t K) { return (M + 15) / 16 * 16 * pitch_q(K); }
@@ -242,6 +251,11 @@ hipError_t launch_lora_reduce(const LoraParams& p, const float* partial, int ksp
 hipError_t launch_lora_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t* asfp, const uint8_t* bq,
                               const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out,
                               hipStream_t s);
+
+// out = bf16(alpha * A W + adapters) for lora_is_token
+hipError_t launch_lora_token(const LoraParams& p, const uint8_t* aq, const uint8_t* asf, const uint8_t* bq,
+                             const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out,
+                             hipStream_t s);
 
 struct GemmParams {
     int mode;

@@ -3,6 +3,8 @@
 // with A_a (R, K) and B_a (N, R) in bf16. The product with A_a ("shrink") gives
 // v[m] = scale[a] x[m] A_a^T in float32; the product with B_a ("expand") is added
 // to the projection before its one rounding. Per batch size:
+//   up to 4 rows of small adapters (lora_is_token)
+//                   everything in one launch
 //   up to 64 rows, and up to 512 of narrow projections (lora_streams)
 //                   shrink (beside it A laid out for streaming), then one kernel
 //                   that streams the weights and adds the adapters
@@ -24,7 +26,9 @@
 // K are separate partial sums, added in order by the reader.
 //
 // What it measured (N 6144, K 7168; beside it the projection alone):
-//   1 row,     L 8,  R 16   shrink 6.5 us, stream 9.5: latency, the launches
+//   1 row,     L 8,  R 16   one launch, 14 us (see there); shrink and stream
+//                           were 6.5 and 9.5
+//   13 rows of 7168 x 2048, L 16, R 64   shrink 5.9, stream 9.3: latency
 //   61 rows,   L 32, R 32   shrink 8.6 (15 MB of adapters, x and A), stream 18.5
 //                           (25 MB of weights; their conversion and that of
 //                           four row blocks of A: the vector units are active
@@ -759,6 +763,224 @@ void lora_stream_kernel(LoraParams p, int parts, int nk, int per, const uint8_t*
     }
 }
 
+// ---------------------------------------------------------------------------
+// A few rows and small adapters (lora_is_token): everything in one launch. The
+// weights are streamed as above by the first nk waves, with A laid out in LDS;
+// the other eight waves of every work-group compute all of v again (M R K
+// products, read from the L2: less than what a second launch and the trip of v
+// through memory cost) while the weights arrive, and add the adapters.
+// v = x A_a^T by rows: four ranks and one range of K per wave and turn, lanes
+// along K, so that loads are whole rows; float32 sums, v is not rounded.
+// One row of 6144 x 7168, R 16: 14 us. A is in LDS after 3.2, v known after 7.2,
+// the first weights (which share the CU's loads with 230 KB of A_a and 60 KB of
+// x) at 8.5, the last product at 11.
+constexpr int kTokenWaves = 8;
+constexpr int kTokenAhead = 4;      // B_a: chunks of 8 ranks loaded before v is known
+
+// K ranges of v's sums: as many as keep the eight waves busy
+__host__ __device__ inline int token_ranges(int M, int R) {
+    const int groups = M * R / 4;
+    return groups >= kTokenWaves ? 1 : kTokenWaves / groups;
+}
+
+template <int CB>
+__global__ __launch_bounds__(2 * NT) __attribute__((amdgpu_waves_per_eu(4)))
+void lora_token_kernel(LoraParams p, int nk, int per, const uint8_t* __restrict__ aq, const uint8_t* __restrict__ asf,
+                       const uint8_t* __restrict__ bq, const uint8_t* __restrict__ bsf,
+                       const float* __restrict__ a_gs, const float* __restrict__ b_alpha, uint16_t* __restrict__ out) {
+    constexpr int LD = 16 * CB + 4;
+    extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int M = (int)p.M, R = p.R, K = (int)p.K;
+    const int ldq = (int)pitch_q(K), ldwsf = (int)pitch_wsf(K);
+    const int steps = ldq / 64, quads = ldwsf / 32, ranges = token_ranges(M, R);
+    uint8_t* la = dyn;                                                      // A: rows of ldq bytes, then their
+    uint8_t* ls = la + M * ldq;                                             // scales in the weights' order
+    float* lv = reinterpret_cast<float*>(ls + M * ldwsf);                   // v: [ranges][M][R]
+    float (*red)[kLoraTokenRows][LD] = reinterpret_cast<float (*)[kLoraTokenRows][LD]>(lv + ranges * M * R);    // [nk]
+    const int64_t blocks = p.N / 16, blk0 = (int64_t)blockIdx.x * CB;       // 16-column blocks
+
+    if (wave < nk) {
+        struct Group {
+            u32x4 w[CB][4];
+            u32x2 ws[CB];
+        };
+        const int g0 = wave * per, g1 = min(quads, g0 + per);
+        const __amdgpu_buffer_rsrc_t rw = make_rsrc(bq, p.N * ldq), rws = make_rsrc(bsf, p.N * ldwsf);
+        const uint32_t w_off = (q >> 1) * kWqHalf + c * 32 + (q & 1) * 16, sf_off = c * 32 + q * 8;
+        auto load_w = [&](int g, Group& r) {
+            const bool on = g < g1;          // else zeros, and nothing is read
+            if (!on) g = 0;
+#pragma unroll
+            for (int f = 0; f < CB; ++f) {
+                const uint32_t blk = (uint32_t)(blk0 + f < blocks ? blk0 + f : blocks - 1);
+                r.ws[f] = __builtin_amdgcn_raw_buffer_load_b64(rws, on ? sf_off : kBeyond, blk * 16 * (uint32_t)ldwsf + (uint32_t)g * kWsfQuad, kStreamNT);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int st = min(4 * g + u, steps - 1);       // beyond the last step the scales are zero
+                    r.w[f][u] = __builtin_amdgcn_raw_buffer_load_b128(rw, on ? w_off : kBeyond, blk * 16 * (uint32_t)ldq + (uint32_t)st * kWqStep, kStreamNT);
+                }
+            }
+        };
+        // A's groups of 16, zero beyond K: thread by thread, its loads before the
+        // weights' (loads return in order)
+        const int nt = 64 * nk, per_row = quads * 32;
+        constexpr int AHEAD = 4;
+        auto stage = [&](int i0, bool first, Group* r0, Group* r1, int g0, int g1) {
+            u32x2 a[AHEAD];
+            uint32_t sf[AHEAD];
+            const __amdgpu_buffer_rsrc_t ra = make_rsrc(aq, (int64_t)M * K / 2), rs = make_rsrc(asf, (int64_t)M * K / 16);
+#pragma unroll
+            for (int t = 0; t < AHEAD; ++t) {
+                const int i = i0 + t * nt, row = i / per_row, g = i - row * per_row;
+                const bool on = row < M && 16 * g < K;
+                a[t] = __builtin_amdgcn_raw_buffer_load_b64(ra, on ? (uint32_t)(row * (K / 2) + 8 * g) : kBeyond, 0, 0);
+                sf[t] = __builtin_amdgcn_raw_buffer_load_b8(rs, on ? (uint32_t)(row * (K / 16) + g) : kBeyond, 0, 0);
+            }
+            if (first) {
+                load_w(g0, *r0);
+                load_w(g1, *r1);
+            }
+#pragma unroll
+            for (int t = 0; t < AHEAD; ++t) {
+                const int i = i0 + t * nt, row = i / per_row, g = i - row * per_row;
+                if (row >= M) continue;
+                if (8 * g < ldq) *reinterpret_cast<u32x2*>(la + row * ldq + 8 * g) = a[t];
+                ls[row * ldwsf + (g >> 5) * 32 + ((g >> 1) & 3) * 8 + ((g >> 3) & 3) * 2 + (g & 1)] = (uint8_t)sf[t];
+            }
+        };
+        Group r0, r1;
+        stage(tid, true, &r0, &r1, g0, g0 + 1);
+        for (int i = tid + AHEAD * nt; i < M * per_row; i += AHEAD * nt) stage(i, false, nullptr, nullptr, 0, 0);
+        lds_sync();
+        float4_t acc[CB];
+#pragma unroll
+        for (int f = 0; f < CB; ++f) acc[f] = (float4_t){0.f, 0.f, 0.f, 0.f};
+        // (rows beyond M are the last one again, and not used)
+        const int row = min(c, M - 1);
+        const uint8_t* ar = la + row * ldq + 16 * q;
+        const uint8_t* sr = ls + row * ldwsf + 8 * q;
+        auto compute = [&](int g, const Group& r) {
+            const u32x2 as = *reinterpret_cast<const u32x2*>(sr + 32 * g);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const u32x4 a = *reinterpret_cast<const u32x4*>(ar + 64 * min(4 * g + u, steps - 1));
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int sh = 16 * (u & 1) + 8 * (s >> 1);
+                    const half8_t ha = dequant8(a[s], scale_pair((as[u >> 1] >> sh) & 0xFFu));
+#pragma unroll
+                    for (int f = 0; f < CB; ++f)
+                        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            ha, dequant8(r.w[f][u][s], scale_pair((r.ws[f][u >> 1] >> sh) & 0xFFu)), acc[f], 0, 0, 0);
+                }
+            }
+        };
+        for (int g = g0;;) {
+            compute(g, r0);
+            if (++g >= g1) break;
+            load_w(g + 1, r0);
+            compute(g, r1);
+            if (++g >= g1) break;
+            load_w(g + 1, r1);
+        }
+        if (q == 0) {
+#pragma unroll
+            for (int f = 0; f < CB; ++f)
+#pragma unroll
+                for (int i = 0; i < kLoraTokenRows; ++i) red[wave][i][16 * f + c] = acc[f][i];
+        }
+        lds_sync();
+        return;
+    }
+
+    // one output per thread: row orow, column n of the work-group's
+    const int t = tid - 64 * nk, tw = wave - nk;
+    const int orow = t / (16 * CB), n = t - orow * 16 * CB;
+    const int64_t col = blk0 * 16 + n;
+    int oid = -1, rank = 0;
+    if (orow < M && col < p.N) oid = p.ids[orow];
+    if (oid >= p.L) oid = -1;
+    if (oid >= 0) rank = p.rank ? min(max(p.rank[oid], 0), R) : R;
+    const uint16_t* brow = oid >= 0 ? p.b + ((int64_t)oid * p.N + col) * R : p.b;
+    const float scale = oid >= 0 ? p.scale[oid] : 0.0f;
+    u32x4 b[kTokenAhead];
+#pragma unroll
+    for (int j = 0; j < kTokenAhead; ++j) b[j] = *reinterpret_cast<const u32x4*>(brow + (8 * j < R ? 8 * j : 0));
+
+    // v
+    const int R4 = R / 4, units = M * R4 * ranges, slabs = (K + 511) / 512, span = (slabs + ranges - 1) / ranges;
+    for (int u = tw; u < units; u += kTokenWaves) {
+        const int range = u / (M * R4), rest = u - range * M * R4, row = rest / R4, j0 = 4 * (rest - row * R4);
+        const int id = p.ids[row];
+        if (id < 0 || id >= p.L) continue;                  // its v is not used
+        const int rk = p.rank ? min(max(p.rank[id], 0), R) : R;
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + (int64_t)row * K, (int64_t)K * 2);
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + (int64_t)id * R * K, (int64_t)R * K * 2);
+        const int s0 = range * span, s1 = min(slabs, s0 + span);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        constexpr int U = 4;                                // slabs of 512 K values in flight
+        for (int s = s0; s < s1; s += U) {
+            u32x4 x[U], a[U][4];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int at = 512 * (s + k) + 8 * lane;
+                const bool on = s + k < s1 && at < K;
+                x[k] = __builtin_amdgcn_raw_buffer_load_b128(rx, on ? (uint32_t)at * 2 : kBeyond, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    a[k][j] = __builtin_amdgcn_raw_buffer_load_b128(
+                        ra, on && j0 + j < rk ? (uint32_t)((j0 + j) * K + at) * 2 : kBeyond, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x0 = bf16_to_f32(x[k][e] & 0xFFFFu), x1 = bf16_to_f32(x[k][e] >> 16);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sum[j] = __builtin_fmaf(x0, bf16_to_f32(a[k][j][e] & 0xFFFFu), sum[j]);
+                        sum[j] = __builtin_fmaf(x1, bf16_to_f32(a[k][j][e] >> 16), sum[j]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int off = 32; off; off >>= 1) sum[j] += __shfl_xor(sum[j], off, 64);
+            if (lane == 0) lv[(range * M + row) * R + j0 + j] = j0 + j < rk ? sum[j] : 0.0f;
+        }
+    }
+    lds_sync();         // A is in place (the streaming waves')
+    lds_sync();         // red and v are
+    if (orow >= M || col >= p.N) return;
+    float delta = 0.0f;
+    auto add = [&](u32x4 w, int j0) {
+        w = lora_mask_rank(w, j0, rank);
+        const float* v = lv + orow * R + j0;
+        for (int r = 0; r < ranges; ++r, v += M * R) {
+            const float4_t v0 = *reinterpret_cast<const float4_t*>(v), v1 = *reinterpret_cast<const float4_t*>(v + 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                delta = __builtin_fmaf(e < 4 ? v0[e & 3] : v1[e & 3], bf16_to_f32(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu), delta);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < kTokenAhead; ++j)
+        if (8 * j < rank) add(b[j], 8 * j);
+    for (int j0 = 8 * kTokenAhead; j0 < rank; j0 += 8) add(*reinterpret_cast<const u32x4*>(brow + j0), j0);
+    float part[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) part[w] = red[w < nk ? w : 0][orow][n];
+    float sum = part[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) sum += w < nk ? part[w] : 0.0f;
+    const float y = a_gs[0] * b_alpha[0] * sum + (rank > 0 ? scale * delta : 0.0f);
+    out[(int64_t)orow * p.N + col] = (uint16_t)pack_bf16x2_rne(y, 0.0f);
+}
+
 template <int MT, int CB>
 hipError_t launch_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t* asfp, const uint8_t* bq,
                          const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out, hipStream_t s) {
@@ -853,6 +1075,26 @@ hipError_t launch_lora_stream(const LoraParams& p, const uint8_t* aqp, const uin
     if (p.M <= 16) return launch_stream<1, 1>(p, aqp, asfp, bq, bsf, a_gs, b_alpha, out, s);
     if (p.M <= 32) return launch_stream<2, 2>(p, aqp, asfp, bq, bsf, a_gs, b_alpha, out, s);
     return launch_stream<4, 2>(p, aqp, asfp, bq, bsf, a_gs, b_alpha, out, s);
+}
+
+hipError_t launch_lora_token(const LoraParams& p, const uint8_t* aq, const uint8_t* asf, const uint8_t* bq,
+                             const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out,
+                             hipStream_t s) {
+    const int quads = (int)(pitch_wsf(p.K) / 32), per = (quads + NW - 1) / NW, nk = (quads + per - 1) / per;
+    const int64_t blocks = p.N / 16;
+    const int cb = blocks <= 256 ? 1 : 2;
+    const int lds = (int)(p.M * (pitch_q(p.K) + pitch_wsf(p.K))) + token_ranges((int)p.M, p.R) * (int)p.M * p.R * 4 +
+                    nk * kLoraTokenRows * (16 * cb + 4) * 4;
+    auto launch = [&](auto width) {
+        constexpr int CB = decltype(width)::value;
+        static std::atomic<int> lds_set[kMaxDevices];
+        hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&lora_token_kernel<CB>), lds, lds_set);
+        if (e != hipSuccess) return e;
+        lora_token_kernel<CB><<<(unsigned)((blocks + CB - 1) / CB), 64 * (nk + kTokenWaves), lds, s>>>(
+            p, nk, per, aq, asf, bq, bsf, a_gs, b_alpha, out);
+        return hipGetLastError();
+    };
+    return cb == 1 ? launch(std::integral_constant<int, 1>{}) : launch(std::integral_constant<int, 2>{});
 }
 
 }  // namespace nvfp4

@@ -89,7 +89,11 @@ def check(s, out):
     # narrow projections of several 64-row parts, and the widths beyond which
     # such batches are tiled instead
     (512, 2048, 528, 4, 16), (449, 2064, 272, 12, 24), (200, 16, 16, 5, 8), (128, 8192, 272, 4, 16), (128, 8224, 272, 4, 16),
-    (65, 8224, 272, 65, 16), (129, 5488, 528, 9, 40), (255, 4112, 640, 6, 256), (300, 3296, 512, 20, 64)])
+    (65, 8224, 272, 65, 16), (129, 5488, 528, 9, 40), (255, 4112, 640, 6, 256), (300, 3296, 512, 20, 64),
+    # a few rows in one launch, and just too much for it
+    (3, 1040, 2064, 5, 16), (4, 8192, 1040, 6, 24), (4, 4112, 4096, 3, 8), (1, 8192, 16368, 2, 8), (1, 4112, 512, 2, 256),
+    (1, 48, 1024, 4, 128), (2, 272, 1024, 4, 64), (1, 8208, 1040, 2, 16), (2, 6144, 7168, 3, 16), (1, 80, 16400, 2, 8), (1, 272, 16400, 2, 16),
+    (4, 272, 1024, 4, 40), (3, 528, 2048, 2, 40), (4, 528, 2048, 2, 32), (1, 272, 32752, 1, 8)])
 def test_random_ids(nv, M, N, K, L, R):
     import torch
     s = make(nv, M, N, K, L, R, M + N + K + L + R)
@@ -99,7 +103,7 @@ def test_random_ids(nv, M, N, K, L, R):
     assert torch.equal(run(nv, s), out)
 
 
-@pytest.mark.parametrize("M,N", [(7, 528), (64, 528), (200, 528), (200, 4144), (1500, 528)])
+@pytest.mark.parametrize("M,N", [(2, 528), (7, 528), (64, 528), (200, 528), (200, 4144), (1500, 528)])
 def test_runs_of_rows(nv, M, N):
     """Requests as runs of rows, some without an adapter; ranks of their own,
     0 and beyond R among them."""
@@ -121,7 +125,7 @@ def test_no_row_has_an_adapter(nv, M, N):
     check(s, run(nv, s))
 
 
-@pytest.mark.parametrize("M,N", [(9, 272), (64, 272), (100, 272), (100, 8224), (700, 272)])
+@pytest.mark.parametrize("M,N", [(4, 272), (9, 272), (64, 272), (100, 272), (100, 8224), (700, 272)])
 def test_broken_requests_stay_alone(nv, M, N):
     """NaN and infinity in one request's adapter, and in what is stored beyond
     the ranks, reach no other row."""
@@ -142,7 +146,7 @@ def test_broken_requests_stay_alone(nv, M, N):
     assert bool(again[s["adapter_ids"] == 3][:, ::3].isnan().all())
 
 
-@pytest.mark.parametrize("M,N", [(9, 272), (64, 272), (100, 272), (100, 8224), (700, 272)])
+@pytest.mark.parametrize("M,N", [(4, 272), (9, 272), (64, 272), (100, 272), (100, 8224), (700, 272)])
 def test_shrunk_rows_that_overflow_stay_infinite(nv, M, N):
     """v = scale * x A^T beyond float32: the sum with B of one sign is that
     infinity, in rows of the adapter alone."""
