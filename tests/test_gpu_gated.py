@@ -2,7 +2,7 @@
 definition in float64.
 
 Tolerances. A bf16 output is one rounding of a float32 result: at most half a
-step, 2^-8 relative (2^-9 for most values). The float32 sum of n exact products
+step, 2^-8 relative. The float32 sum of n exact products
 carries at most n * 2^-24 * sum |a b|; half the worst case is far above what
 random signs give. The gradients' sums take [dgate | dup] rounded to bf16: each
 term moves by at most 2^-8 of itself, so the sum by at most 2^-8 * sum |a b|.
@@ -317,3 +317,26 @@ def test_refusals(nv):
         nv.gated_backward(d, x, w13, gu, need_dx=False, need_dw13=False)
     with pytest.raises(ValueError):
         nv.gated_backward(d, x, w13, gu, dx=torch.zeros((4, 32), **bf), need_dx=False)
+
+
+@pytest.mark.parametrize("T,H,I", [(140001, 16, 16384), (140001, 16384, 16)])
+def test_offsets_beyond_32_bits(nv, T, H, I):
+    """Operands and outputs of more than 4 GiB: rows of both ends, and the
+    weight gradient's rows and columns of both ends."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(T + H)
+
+    def normal(shape, std):
+        return torch.randn(shape, generator=g, device="cuda", dtype=torch.bfloat16) * std
+
+    x, w13, d_act = normal((T, H), 1.5), normal((H, 2 * I), 2.5 / (1.5 * H ** 0.5)), normal((T, I), 0.5)
+    gate_up = torch.empty((T, 2 * I), dtype=torch.bfloat16, device="cuda")
+    act = nv.gated_forward(x, w13, gate_up=gate_up)
+    dx, dw13 = nv.gated_backward(d_act, x, w13, gate_up)
+    rows = torch.tensor([0, 1, T // 2, T - 2, T - 1], device="cuda")
+    check_forward(x[rows], w13, act[rows], gate_up[rows])
+    check_backward(d_act[rows], x[rows], w13, gate_up[rows], dx[rows], None)
+    h = torch.tensor([0, 7, H - 1], device="cuda")
+    c = torch.tensor([0, 5, I - 1], device="cuda")
+    both = torch.cat((c, I + c))
+    check_backward(d_act[:, c], x[:, h], w13[h][:, both], gate_up[:, both], None, dw13[h][:, both])

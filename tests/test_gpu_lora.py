@@ -316,3 +316,33 @@ def test_feed_forward_with_adapters(nv, T):
     gu = x.double() @ w13.double()
     ref = gu[:, :I] * torch.sigmoid(gu[:, :I]) * gu[:, I:]
     assert float((act.double() - ref).norm() / ref.norm()) < HALF
+
+
+def check_rows(s, out, rows):
+    """check on some rows of a result."""
+    check({**s, "x": s["x"][rows], "aq": s["aq"][rows], "asf": s["asf"][rows], "adapter_ids": s["adapter_ids"][rows]},
+          out[rows])
+
+
+def test_outputs_beyond_32_bits(nv):
+    """More than 4 GiB of output: rows of both ends and beside the 4 GiB border."""
+    import torch
+    M, N, K, L, R = 131100, 16416, 64, 3, 8
+    s = make(nv, M, N, K, L, R, 9)
+    out = run(nv, s)
+    border = 2 ** 31 // N
+    check_rows(s, out, torch.tensor([0, 1, border, border + 1, M // 2, M - 2, M - 1], device="cuda"))
+
+
+@pytest.mark.parametrize("M", [2, 40, 70, 300])
+def test_adapters_beyond_32_bits(nv, M):
+    """Adapters stored in more than 4 GiB, the last ones in use."""
+    import torch
+    N, K, L, R = 16384, 64, 600, 256
+    s = make(nv, M, N, K, 1, 8, M)
+    g = torch.Generator("cuda").manual_seed(M)
+    s["lora_b"] = torch.randn((L, N, R), generator=g, device="cuda", dtype=torch.bfloat16)
+    s["lora_a"] = torch.randn((L, R, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    s["lora_scale"] = torch.rand((L,), generator=g, device="cuda") * 0.1
+    s["adapter_ids"] = (L - 1 - 5 * (torch.arange(M, device="cuda") % 7)).to(torch.int32)
+    check(s, run(nv, s))
