@@ -34,7 +34,7 @@
 //                           four row blocks of A: the vector units are active
 //                           half the cycles, the matrix pipes a fifth, and 64
 //                           CUs have no columns)
-//   256 rows,  L 6,  R 16   shrink 11, tiled GEMM 28, chunks' sum and expand 11
+//   256 rows,  L 6,  R 16   shrink 11, tiled GEMM 28, chunks' sum and expand 10
 //                           (nvfp4_gemm 38 in all)
 //   4093 rows, L 8,  R 64   sort 7, shrink 35 (59 MB of x and 16 MB of A read, 59
 //                           MB of f16 written), join 5, GEMM with the expand 320
@@ -541,7 +541,7 @@ struct Expand {
 };
 
 // K chunks: out = bf16(alpha * (their sum, in order) + adapters), for one tile
-// of 64 listed rows and 32 columns. 11.3 us at 256 x 6144 and 5 chunks (31 MB of
+// of 64 listed rows and 32 columns. 10.3 us at 256 x 6144 and 5 chunks (31 MB of
 // sums, held by the caches; the sum alone takes 6.6).
 constexpr int RT = 256;
 __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles, const float* __restrict__ partial,
@@ -564,19 +564,36 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
     lds_sync();
     // each thread: four columns of tile rows tid / 8 and tid / 8 + 32
     const int col = 4 * (tid & 7);
-    float4_t sum[2];
     int row[2];
+    const float4_t* src[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         row[t] = __shfl(row_of, (tid >> 3) + 32 * t, 64);
         if (n0 + col >= p.N) row[t] = -1;
-        if (row[t] >= 0)
-            sum[t] = sum_planes<8>(reinterpret_cast<const float4_t*>(partial + (int64_t)row[t] * p.N + n0 + col), ksplit, p.M * p.N / 4);
+        src[t] = reinterpret_cast<const float4_t*>(row[t] >= 0 ? partial + (int64_t)row[t] * p.N + n0 + col : partial);
     }
     Expand<2, LD> expand(p, id, n0, wave, RT / 64);
     join_v(p, kLoraRows, [&](int r) { return rows[r]; }, tid, RT, lv);
+    // the first chunks' sums arrive under the expand (loaded without a branch:
+    // what is not there is chunk 0 again); before v they would hold it up
+    constexpr int PL = 6;
+    const int64_t plane = p.M * p.N / 4;
+    float4_t part[2][PL];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < PL; ++k) part[t][k] = src[t][k < ksplit ? k * plane : 0];
     lds_sync();
     expand.run(lv, delta);
+    float4_t sum[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        sum[t] = part[t][0];
+#pragma unroll
+        for (int k = 1; k < PL; ++k)
+            if (k < ksplit) sum[t] += part[t][k];
+        if (ksplit > PL) sum[t] += sum_planes<8>(src[t] + PL * plane, ksplit - PL, plane);
+    }
     lds_sync();
     const float alpha = a_gs[0] * b_alpha[0];
 #pragma unroll
