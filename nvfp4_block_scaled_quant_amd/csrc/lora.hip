@@ -34,7 +34,7 @@
 //                           four row blocks of A: the vector units are active
 //                           half the cycles, the matrix pipes a fifth, and 64
 //                           CUs have no columns)
-//   256 rows,  L 6,  R 16   shrink 11, tiled GEMM 28, chunks' sum and expand 10
+//   256 rows,  L 6,  R 16   shrink 9.4, tiled GEMM 28, chunks' sum and expand 10
 //                           (nvfp4_gemm 38 in all)
 //   4093 rows, L 8,  R 64   sort 7, shrink 35 (59 MB of x and 16 MB of A read, 59
 //                           MB of f16 written), join 5, GEMM with the expand 320
@@ -193,27 +193,30 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
     if (rank_rows) {
         // a small batch is listed here: by (adapter, row), rows without one
         // last; every work-group finds the same order by counting
+        // (two threads a row, each half of the keys; one took 1.5 us longer at 256
+        // rows)
+        static_assert(NT == 2 * kLoraRankRows, "two threads a row");
         __shared__ __attribute__((aligned(16))) int key[kLoraRankRows];
-        __shared__ int order[kLoraRankRows];
+        __shared__ int below[kLoraRankRows], order[kLoraRankRows];
+        const int r = tid % kLoraRankRows, part = tid / kLoraRankRows;
         int mine = 0x7FFFFFFF;
-        if (tid < kLoraRankRows) {
-            if (tid < M) {
-                const int a = p.ids[tid];
-                mine = (a >= 0 && a < L ? a : L) * kLoraRankRows + tid;
-            }
-            key[tid] = mine;
+        if (r < M) {
+            const int a = p.ids[r];
+            mine = (a >= 0 && a < L ? a : L) * kLoraRankRows + r;
         }
+        if (part == 0) key[r] = mine;
         lds_sync();
-        if (tid < M) {
-            int pos = 0;
-#pragma unroll 4
-            for (int j = 0; j < (int)M; j += 4) {
-                const u32x4 k = *reinterpret_cast<const u32x4*>(key + j);
+        int pos = 0;
+        const int half = (int)((M + 7) / 8 * 4), j1 = part ? (int)M : half;
+#pragma unroll 8
+        for (int j = part * half; j < j1; j += 4) {
+            const u32x4 k = *reinterpret_cast<const u32x4*>(key + j);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) pos += (int)k[e] < mine;
-            }
-            order[pos] = mine;
+            for (int e = 0; e < 4; ++e) pos += (int)k[e] < mine;
         }
+        if (part == 0) below[r] = pos;
+        lds_sync();
+        if (part == 1 && r < M) order[pos + below[r]] = mine;
         lds_sync();
         if (in) {
             row_of = order[m0 + lane] % kLoraRankRows;
@@ -230,6 +233,9 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
         row_of = p.perm ? p.perm[m0 + lane] : (int)(m0 + lane);
     }
     uint64_t todo = __builtin_amdgcn_ballot_w64(id >= 0);
+    // (by lane too: a scalar load of an adapter's would be waited for with the LDS)
+    const float my_scale = id >= 0 ? p.scale[id] : 0.0f;
+    const int my_rank = p.rank && id >= 0 ? min(max(p.rank[id], 0), R) : R;
     // blocks of 64 K values of this plane
     const int nb = (int)((K + 63) / 64), per = (nb + planes - 1) / planes;
     const int b0 = plane * per, b1 = min(nb, b0 + per);
@@ -237,13 +243,13 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
     // the tile's adapters in order of first appearance: this work-group takes
     // numbers slot, slot + slots, ...
     for (int d = 0; todo; ++d) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        const int lead = __builtin_ctzll(todo);
+        const int a = __builtin_amdgcn_readlane(id, lead);
         const uint64_t rows = __builtin_amdgcn_ballot_w64(id == a);
         todo &= ~rows;
         if (d % slots != slot) continue;
-        const int rk = p.rank ? min(max(p.rank[a], 0), R) : R;
+        const int rk = __builtin_amdgcn_readlane(my_rank, lead);
         const int n = __builtin_popcountll(rows);
-        const float sc = p.scale[a];
         lds_sync();                             // the previous adapter's readers are done
         if (wave == 0 && id == a) {
             const int at = __builtin_popcountll(rows & ((1ull << lane) - 1));
@@ -302,6 +308,7 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
             }
         }
         __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));      // no load into LDS outlives its adapter
+        const float sc = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_scale), lead));
         // acc[f][i] = D[gathered row 16 g + 4 q + i][rank 32 rh + 16 f + c]
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
