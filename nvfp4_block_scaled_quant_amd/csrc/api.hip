@@ -554,7 +554,7 @@ struct LoraLayout {
 LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     LoraLayout w = {};
     const int64_t m = M > 0 ? M : 1;
-    const bool stream = lora_streams(m, N);
+    const bool stream = lora_streams(m, N, K, L, R);
     w.ksplit = dense_ksplit(m, N, K);
     w.planes = lora_planes(m, N, K, L, R);
     w.aqp = align_up((size_t)w.planes * (size_t)m * (size_t)R * 4);
@@ -616,7 +616,7 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs, co
         NVFP4_TRY(launch_lora_token(lo, aq, asf, bq, bsf, a_gs, b_alpha, out, stream));
         return NVFP4_OK;
     }
-    if (lora_streams(M, N)) {
+    if (lora_streams(M, N, K, L, R)) {
         NVFP4_TRY(launch_lora_shrink(lo, kLoraAsIs, nullptr, nullptr, aq, asf, ws + w.aqp, ws + w.asfp, nullptr, stream));
         NVFP4_TRY(launch_lora_stream(lo, ws + w.aqp, ws + w.asfp, bq, bsf, a_gs, b_alpha, out, stream));
         return NVFP4_OK;

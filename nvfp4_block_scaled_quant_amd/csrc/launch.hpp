@@ -214,11 +214,15 @@ constexpr int kLoraRankRows = 256;
 // rows, one on a CU: up to two of them a CU it is faster (128 rows of 2048 x
 // 4096, 128 work-groups: 21 us against 35; of 6144 x 7168, 384: 41.7 against
 // 44; 512 rows of 2048 x 2048, 512: 19 to 22 against 34), with three it is not
-// (160 rows of 6144 x 7168, 576: 59 against 44). More rows would read an
-// adapter too often, once per 64 rows that have it (1024 rows of 1024 x 4096
-// with 40 adapters at random: 63 against 41).
-inline bool lora_streams(int64_t M, int64_t N) {
-    return M <= kLoraRows || (M <= kLoraStreamRows && (M + 63) / 64 * ((N + 31) / 32) <= 512);
+// (160 rows of 6144 x 7168, 576: 59 against 44). Its rows are not listed by
+// adapter, so each 64 rows may read every adapter again: where that is more
+// than 2^25 values it costs more than it saves (rows at random, L 48: 300 rows
+// of 1024 x 2048, R 128, 25 M: 34 us against 38; 512 rows of 2048 x 2048, R 64,
+// 44 M: 55 against 42).
+inline bool lora_streams(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
+    const int64_t parts = (M + kLoraRows - 1) / kLoraRows;
+    return parts <= 1 || (M <= kLoraStreamRows && parts * ((N + 31) / 32) <= 512 &&
+                          (parts - 1) * (L < kLoraRows ? L : kLoraRows) * R * K <= (int64_t)1 << 25);
 }
 constexpr int kLoraTokenRows = 4;
 // Whether one launch does it all: a few rows of small adapters (every
@@ -247,7 +251,7 @@ hipError_t launch_lora_join(const LoraParams& p, hipStream_t s);
 // out = bf16(alpha * sum over chunks of partial[c] (M, N) + adapters)
 hipError_t launch_lora_reduce(const LoraParams& p, const float* partial, int ksplit, const float* a_gs,
                               const float* b_alpha, uint16_t* out, hipStream_t s);
-// out = bf16(alpha * A W + adapters) for lora_streams(M, N)
+// out = bf16(alpha * A W + adapters) for lora_streams
 hipError_t launch_lora_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t* asfp, const uint8_t* bq,
                               const uint8_t* bsf, const float* a_gs, const float* b_alpha, uint16_t* out,
                               hipStream_t s);

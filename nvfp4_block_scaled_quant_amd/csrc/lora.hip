@@ -1035,9 +1035,10 @@ hipError_t launch_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t*
 int lora_planes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     const int64_t tiles = (M + kLoraRows - 1) / kLoraRows, rbs = (R + kRankBlock - 1) / kRankBlock;
     const int64_t rows = M < kLoraRows ? M : kLoraRows;
-    const int64_t here = lora_streams(M, N) ? (rows < L ? rows : L) : 1;
+    const bool listed = !lora_streams(M, N, K, L, R);
+    const int64_t here = listed ? 1 : rows < L ? rows : L;
     const int64_t nb = (K + 63) / 64;
-    int64_t n = (lora_streams(M, N) ? 512 : 416) / (tiles * rbs * here);
+    int64_t n = (listed ? 416 : 512) / (tiles * rbs * here);
     if (n > nb / 4) n = nb / 4;
     if (n > kLoraMaxPlanes) n = kLoraMaxPlanes;
     if (n < 1) n = 1;

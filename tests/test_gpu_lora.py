@@ -90,6 +90,8 @@ def check(s, out):
     # such batches are tiled instead
     (512, 2048, 528, 4, 16), (449, 2064, 272, 12, 24), (200, 16, 16, 5, 8), (128, 8192, 272, 4, 16), (128, 8224, 272, 4, 16),
     (65, 8224, 272, 65, 16), (129, 5488, 528, 9, 40), (255, 4112, 640, 6, 256), (300, 3296, 512, 20, 64),
+    # many adapters of high rank: tiled although narrow
+    (256, 512, 2048, 48, 128), (512, 272, 4096, 64, 64), (70, 528, 7168, 80, 80),
     # a few rows in one launch, and just too much for it
     (3, 1040, 2064, 5, 16), (4, 8192, 1040, 6, 24), (4, 4112, 4096, 3, 8), (1, 8192, 16368, 2, 8), (1, 4112, 512, 2, 256),
     (1, 48, 1024, 4, 128), (2, 272, 1024, 4, 64), (1, 8208, 1040, 2, 16), (2, 6144, 7168, 3, 16), (1, 80, 16400, 2, 8), (1, 272, 16400, 2, 16),
