@@ -460,33 +460,57 @@ def gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, ad
     lora_rank[a] ranks."""
     bf16, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
     _need(x, bf16, "x", 2)
-    _need(bq, u8, "bq", 4)
-    _need(lora_a, bf16, "lora_a", 3)
     index = x.get_device()
     if index != torch._C._cuda_getDevice():                 # the library launches on the current device
         with torch.cuda.device(index):
             return gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, adapter_ids,
                              lora_rank, out, workspace)
     M, K = x.shape
-    blocks = bq.shape[0]
-    N = blocks * 16
-    L, R, _ = lora_a.shape
-    if K % 16 or K == 0 or N == 0:
-        raise ValueError("gemm_lora: K must be a positive multiple of 16 and N positive")
-    if R % 8 or not 8 <= R <= 256 or not 1 <= L <= 8192:
-        raise ValueError("gemm_lora: R must be a multiple of 8 from 8 to 256, and L from 1 to 8192")
-    steps = (K + 127) // 128                                # packed_shapes
-    p_aq, p_asf, p_bq, p_bsf, p_a, p_b, p_scale, p_ids = _operands(
-        index, (aq, u8, (M, K // 2), "aq"), (asf, u8, (M, K // 16), "asf"),
-        (bq, u8, (blocks, 2 * steps, 16, 32), "bq"), (bsf, u8, (blocks, (steps + 3) // 4, 16, 32), "bsf"),
-        (lora_a, bf16, (L, R, K), "lora_a"), (lora_b, bf16, (L, N, R), "lora_b"),
-        (lora_scale, f32, (L,), "lora_scale"), (adapter_ids, i32, (M,), "adapter_ids"))
+    # One expression says whether all is well (a small batch's kernels take less
+    # time than checks one by one); if not, the checks say what is wrong.
+    try:
+        (L, R, _), blocks = lora_a.shape, bq.shape[0]
+        N, steps = blocks * 16, (K + 127) // 128            # packed_shapes
+        good = (aq.dtype is u8 and aq.shape == (M, K // 2) and aq.get_device() == index and aq.is_contiguous()
+                and asf.dtype is u8 and asf.shape == (M, K // 16) and asf.get_device() == index
+                and asf.is_contiguous()
+                and bq.dtype is u8 and bq.shape == (blocks, 2 * steps, 16, 32) and bq.get_device() == index
+                and bq.is_contiguous()
+                and bsf.dtype is u8 and bsf.shape == (blocks, (steps + 3) // 4, 16, 32)
+                and bsf.get_device() == index and bsf.is_contiguous()
+                and lora_a.dtype is bf16 and lora_a.shape == (L, R, K) and lora_a.get_device() == index
+                and lora_a.is_contiguous()
+                and lora_b.dtype is bf16 and lora_b.shape == (L, N, R) and lora_b.get_device() == index
+                and lora_b.is_contiguous()
+                and lora_scale.dtype is f32 and lora_scale.shape == (L,) and lora_scale.get_device() == index
+                and lora_scale.is_contiguous()
+                and adapter_ids.dtype is i32 and adapter_ids.shape == (M,) and adapter_ids.get_device() == index
+                and adapter_ids.is_contiguous()
+                and K % 16 == 0 and K > 0 and N > 0 and R % 8 == 0 and 8 <= R <= 256 and 1 <= L <= 8192)
+    except (AttributeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _need(bq, u8, "bq", 4)
+        _need(lora_a, bf16, "lora_a", 3)
+        blocks = bq.shape[0]
+        L, R, _ = lora_a.shape
+        N, steps = blocks * 16, (K + 127) // 128
+        if K % 16 or K == 0 or N == 0:
+            raise ValueError("gemm_lora: K must be a positive multiple of 16 and N positive")
+        if R % 8 or not 8 <= R <= 256 or not 1 <= L <= 8192:
+            raise ValueError("gemm_lora: R must be a multiple of 8 from 8 to 256, and L from 1 to 8192")
+        _operands(
+            index, (aq, u8, (M, K // 2), "aq"), (asf, u8, (M, K // 16), "asf"),
+            (bq, u8, (blocks, 2 * steps, 16, 32), "bq"), (bsf, u8, (blocks, (steps + 3) // 4, 16, 32), "bsf"),
+            (lora_a, bf16, (L, R, K), "lora_a"), (lora_b, bf16, (L, N, R), "lora_b"),
+            (lora_scale, f32, (L,), "lora_scale"), (adapter_ids, i32, (M,), "adapter_ids"))
     p_rank = None if lora_rank is None else _operands(index, (lora_rank, i32, (L,), "lora_rank"))[0]
     p_gs, p_alpha = _scalar(a_gs, "a_gs", index), _scalar(b_alpha, "b_alpha", index)
     out = _result(out, x, (M, N), "out", index)
     ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.nvfp4_gemm_lora_workspace(M, N, K, L, R), index)
-    _check(_lib.nvfp4_gemm_lora(p_aq, p_asf, p_gs, p_bq, p_bsf, p_alpha, x.data_ptr(), p_a, p_b, p_scale, p_rank,
-                                p_ids, M, N, K, L, R, out.data_ptr(), ws_ptr, ws_bytes,
+    _check(_lib.nvfp4_gemm_lora(aq.data_ptr(), asf.data_ptr(), p_gs, bq.data_ptr(), bsf.data_ptr(), p_alpha,
+                                x.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), lora_scale.data_ptr(), p_rank,
+                                adapter_ids.data_ptr(), M, N, K, L, R, out.data_ptr(), ws_ptr, ws_bytes,
                                 torch._C._cuda_getCurrentRawStream(index)), "nvfp4_gemm_lora")
     return out
 
