@@ -430,8 +430,8 @@ int nvfp4_route_topk(const float* logits, int64_t T, int64_t E, int64_t topk,
  *                                                    * lora_b[a][n][r] )
  *   with a = adapter_ids[m]; rows whose id is outside [0, L) get the first
  *   term alone. One rounding; the sums are float32, and the shrunk row
- *   scale * x A^T enters the second product as the sum of two bf16 values
- *   (2^-17 relative).
+ *   scale * x A^T enters the second product in float32 or as the sum of two
+ *   bf16 values (2^-17 relative).
  *
  *   aq, asf, a_gs, bq, bsf, b_alpha, M, N, K, out   as nvfp4_gemm
  *   x            (M, K) bf16, what aq was quantized from
