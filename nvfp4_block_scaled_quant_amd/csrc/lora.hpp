@@ -9,16 +9,20 @@ namespace nvfp4 {
 
 // Eight ranks k .. k + 7 of row `row` of v as hi + low in bf16: v is the sum of
 // its partial sums in order, hi its rounding and low the rounding of what is
-// left, so hi + low is within 2^-17 of v. Where hi is infinite low is zero, so
-// that an infinite v stays one (infinity less itself is not a number).
+// left, so hi + low is within 2^-17 of v (2^-134 where that is more). A finite v
+// stays finite: hi ends at the largest bf16, where from 3.3961e38 on it would round
+// to infinity. Where v is infinite low is zero, so that it stays infinite (infinity
+// less itself is not a number).
 __device__ __forceinline__ void lora_v_operand(const LoraParams& lo, int64_t row, int k, u32x4& hi, u32x4& low) {
     typedef float float8_t __attribute__((ext_vector_type(8)));
     const float8_t v = sum_planes<kLoraMaxPlanes - 1>(reinterpret_cast<const float8_t*>(lo.v + row * lo.R + k), lo.planes,
                                                       lo.M * lo.R / 8);
+    constexpr float kMaxBf16 = 0x1.FEp127f;
+    auto in_range = [](float x) { return __builtin_isfinite(x) ? __builtin_amdgcn_fmed3f(x, -kMaxBf16, kMaxBf16) : x; };
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float v0 = v[2 * e], v1 = v[2 * e + 1];
-        hi[e] = pack_bf16x2_rne(v0, v1);
+        hi[e] = pack_bf16x2_rne(in_range(v0), in_range(v1));
         const float h0 = bf16_to_f32(hi[e] & 0xFFFFu), h1 = bf16_to_f32(hi[e] >> 16);
         low[e] = pack_bf16x2_rne(__builtin_isinf(h0) ? 0.0f : v0 - h0, __builtin_isinf(h1) ? 0.0f : v1 - h1);
     }
