@@ -667,6 +667,17 @@ void gemm_kernel(GemmParams p) {
                         todo[i] &= ~match[i];
                     }
                     const int steps = min(4, (rank - r0 + 15) / 16);
+                    // whether this wave's columns of B_a hold anything that is not
+                    // finite (see lora_finite). Looked up once: 3 us of 350 at 4093
+                    // rows, R 64; masks in every product took 6.
+                    bool wild = false;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            wild |= lora_any_infinite(*reinterpret_cast<const u32x4*>(
+                                smem_raw + V_B + (wn * 64 + 32 * j + l32) * 128 + (frag ^ (32u * t))));
+                    wild = __builtin_amdgcn_ballot_w64(wild) != 0;
 #pragma unroll
                     for (int i = 0; i < MI; ++i) {
                         const int blk = wm * MI + i;               // 32-row block of the tile
@@ -692,6 +703,7 @@ void gemm_kernel(GemmParams p) {
                                 const bf16x8_t lw = *reinterpret_cast<const bf16x8_t*>(vr + V_LOW + at);
                                 if (rank & 7) b = lora_mask_rank(b, r0 + 16 * t + 8 * h, rank);
                                 d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, __builtin_bit_cast(bf16x8_t, b), d, 0, 0, 0);
+                                if (wild) b = lora_finite(b);
                                 d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lw, __builtin_bit_cast(bf16x8_t, b), d, 0, 0, 0);
                             }
 #pragma unroll

@@ -521,9 +521,10 @@ struct Expand {
         for (int f = 0; f < CB; ++f) {
             u32x4 b = t.b[f];
             if (t.rank & 7) b = lora_mask_rank(b, t.k0 + 8 * q, t.rank);
-            const bf16x8_t bf = __builtin_bit_cast(bf16x8_t, b);
-            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi), bf, acc[f], 0, 0, 0);
-            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low), bf, acc[f], 0, 0, 0);
+            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi),
+                                                             __builtin_bit_cast(bf16x8_t, b), acc[f], 0, 0, 0);
+            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low),
+                                                             __builtin_bit_cast(bf16x8_t, lora_finite(b)), acc[f], 0, 0, 0);
         }
         if (!t.last) return;
 #pragma unroll

@@ -36,4 +36,24 @@ __device__ __forceinline__ u32x4 lora_mask_rank(u32x4 b, int k, int rank) {
     return b;
 }
 
+// B_a for the product with low: infinities and NaN are left out, as the product
+// with hi has them already (low may be zero or have the other sign, and would turn
+// an infinity into NaN). Per 16-bit half: one added to an exponent of all ones
+// gives the sign bit, whose arithmetic shift is the mask.
+typedef short short2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ short2_t lora_infinite_bits(uint32_t b) {
+    return __builtin_bit_cast(short2_t, b & 0x7F807F80u) + (short2_t)(short)0x80;
+}
+__device__ __forceinline__ u32x4 lora_finite(u32x4 b) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] &= ~__builtin_bit_cast(uint32_t, lora_infinite_bits(b[e]) >> (short2_t)(short)15);
+    return b;
+}
+__device__ __forceinline__ bool lora_any_infinite(u32x4 b) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) any |= __builtin_bit_cast(uint32_t, lora_infinite_bits(b[e]));
+    return (any & 0x80008000u) != 0;
+}
+
 }  // namespace nvfp4
