@@ -299,13 +299,12 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
     return v;
 }
 
-// Sum of n values of type V, `stride` V apart, in order. Up to B loads are in
-// flight before the first is added (a plain loop over few values would wait
+// sum plus n values of type V, `stride` V apart, added in order. Up to B loads are
+// in flight before the first is added (a plain loop over few values would wait
 // for each).
 template <int B, typename V>
-__device__ __forceinline__ V sum_planes(const V* __restrict__ src, int n, int64_t stride) {
-    V sum = src[0];
-    for (int c0 = 1; c0 < n; c0 += B) {
+__device__ __forceinline__ V add_planes(V sum, const V* __restrict__ src, int n, int64_t stride) {
+    for (int c0 = 0; c0 < n; c0 += B) {
         V v[B];
 #pragma unroll
         for (int j = 0; j < B; ++j)
@@ -315,6 +314,11 @@ __device__ __forceinline__ V sum_planes(const V* __restrict__ src, int n, int64_
             if (c0 + j < n) sum += v[j];
     }
     return sum;
+}
+// Sum of n values of type V, `stride` V apart, in order.
+template <int B, typename V>
+__device__ __forceinline__ V sum_planes(const V* __restrict__ src, int n, int64_t stride) {
+    return add_planes<B>(src[0], src + stride, n - 1, stride);
 }
 
 // Byte transpose of a 4x4 block held in 4 words: in r[i] byte j = M[i][j];

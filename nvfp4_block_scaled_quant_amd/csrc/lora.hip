@@ -600,7 +600,7 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
 #pragma unroll
         for (int k = 1; k < PL; ++k)
             if (k < ksplit) sum[t] += part[t][k];
-        if (ksplit > PL) sum[t] += sum_planes<8>(src[t] + PL * plane, ksplit - PL, plane);
+        sum[t] = add_planes<8>(sum[t], src[t] + PL * plane, ksplit - PL, plane);
     }
     lds_sync();
     const float alpha = a_gs[0] * b_alpha[0];
