@@ -408,6 +408,16 @@ def moe_forward_noalloc(x, topk_ids, topk_weights, w13, w13_sf, w13_alpha, w2, w
     return y
 
 
+def _refuse_recording(where, **tensors):
+    """The dense operators write their results without a graph: an input that
+    requires a gradient while gradients are recorded would lose it unnoticed."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise RuntimeError(f"{where}: {name} requires a gradient, which this call does not record; call it "
+                                   "under torch.no_grad() or inside a torch.autograd.Function")
+
+
 def _operands(index, *specs):
     """Addresses of operands (tensor, dtype, shape, name) of exactly these
     dtypes and shapes on device `index` (the messages are _need's)."""
@@ -457,8 +467,18 @@ def gemm_lora(aq, asf, a_gs, bq, bsf, b_alpha, x, lora_a, lora_b, lora_scale, ad
     x: the bf16 (M, K) activation that aq was quantized from; lora_a bf16
     (L, R, K), lora_b bf16 (L, N, R), R a multiple of 8 up to 256; lora_scale
     float32 (L,); lora_rank: None, or int32 (L,): adapter a uses its first
-    lora_rank[a] ranks."""
+    lora_rank[a] ranks. out overlaps no input. Has no gradient: inputs that
+    require one are refused while gradients are recorded."""
     bf16, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
+    try:
+        recorded = torch.is_grad_enabled() and (
+            x.requires_grad or lora_a.requires_grad or lora_b.requires_grad or lora_scale.requires_grad
+            or a_gs.requires_grad or b_alpha.requires_grad)
+    except AttributeError:                                  # not a tensor: the checks below name it
+        recorded = False
+    if recorded:
+        _refuse_recording("gemm_lora", x=x, lora_a=lora_a, lora_b=lora_b, lora_scale=lora_scale, a_gs=a_gs,
+                          b_alpha=b_alpha)
     _need(x, bf16, "x", 2)
     index = x.get_device()
     if index != torch._C._cuda_getDevice():                 # the library launches on the current device
@@ -532,7 +552,10 @@ def gated_forward(x, w13, act=None, gate_up=None, workspace=None):
     """act = silu(x @ w13[:, :I]) * (x @ w13[:, I:]) in one pass: x bf16
     (T, H), w13 bf16 (H, 2I) = [gate | up] -> act bf16 (T, I). gate_up: None,
     or a bf16 (T, 2I) tensor that receives the rounded gate | up values that
-    gated_backward takes."""
+    gated_backward takes. The result has no graph: while gradients are recorded,
+    inputs that require one are refused (a training program makes the two calls in
+    a torch.autograd.Function). Outputs overlap no input and each other."""
+    _refuse_recording("gated_forward", x=x, w13=w13)
     T, H, I = _gated_sizes(x, w13)
     index = x.get_device()
     if index != torch._C._cuda_getDevice():                 # the library launches on the current device
@@ -550,7 +573,10 @@ def gated_backward(d_act, x, w13, gate_up, dx=None, dw13=None, need_dx=True, nee
                    workspace=None):
     """Gradients of gated_forward: d_act bf16 (T, I), the forward's x, w13 and
     gate_up -> (dx bf16 (T, H), dw13 bf16 (H, 2I)). need_dx / need_dw13 =
-    False skips that product and returns None in its place."""
+    False skips that product and returns None in its place. [dgate | dup] enters
+    the products rounded to bf16. Has no gradient of its own: inputs that require
+    one are refused while gradients are recorded."""
+    _refuse_recording("gated_backward", d_act=d_act, x=x, w13=w13, gate_up=gate_up)
     T, H, I = _gated_sizes(x, w13)
     index, bf16 = x.get_device(), torch.bfloat16
     if index != torch._C._cuda_getDevice():                 # the library launches on the current device
