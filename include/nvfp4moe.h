@@ -444,7 +444,8 @@ int nvfp4_route_topk(const float* logits, int64_t T, int64_t E, int64_t topk,
  *   adapter_ids  (M) int32
  *   x, lora_a, lora_b 16-byte aligned; R % 8 == 0, 8 <= R <= 256, 1 <= L <=
  *   8192, M <= 2^22, 2 R K below 2^31, K % 16 == 0, N % 16 == 0 and
- *   nvfp4_gemm's limits, else NVFP4_ESHAPE.
+ *   nvfp4_gemm's limits, else NVFP4_ESHAPE. out and the workspace overlap no
+ *   input and each other.
  * A row depends on its own x, aq and adapter and on no other: NaN in one
  * request's row or adapter stays in that request's rows. Deterministic: the
  * order of every sum depends on the sizes alone, not on the ids.
