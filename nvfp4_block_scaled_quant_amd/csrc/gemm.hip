@@ -658,6 +658,8 @@ void gemm_kernel(GemmParams p) {
                         const uint32_t off = n0 + row < N && k < rank ? (uint32_t)(row * lo.R + k) * 2 : kBeyond;
                         __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void*)(smem_raw + V_B + (4 * wave + t) * 1024), 16, off, 0, 0, 0);
                     }
+                    // the barrier by itself promises nothing about loads into LDS
+                    __builtin_amdgcn_s_waitcnt(kWaitAll);
                     __syncthreads();
                     // matching rows of this wave's 32-row blocks: rows wm * 32 MI + 32 i
                     uint64_t match[4];
