@@ -719,7 +719,8 @@ size_t nvfp4_gated_backward_workspace(int64_t T, int64_t H, int64_t I) {
     if (!gated_shape_ok(T, H, I)) return 0;
     if (T == 0) return kAlign;
     GatedPlan px, pw;
-    gated_backward_plan(T, H, I, px, pw);
+    bool dx_first;
+    gated_backward_plan(T, H, I, px, pw, dx_first);
     return gated_backward_bytes(T, H, I, px, pw);
 }
 
@@ -731,10 +732,11 @@ int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_
     if (!dx && !dw13) return NVFP4_EINVAL;
     if (!aligned(dx, 16) || !aligned(dw13, 16)) return NVFP4_EINVAL;
     GatedPlan px = {}, pw = {};
+    bool dx_first = true;
     if (T > 0) {
         if (!d_act || !gate_up || (dx && !w13) || (dw13 && !x)) return NVFP4_EINVAL;
         if (!aligned(d_act, 16) || !aligned(x, 16) || !aligned(w13, 16) || !aligned(gate_up, 16)) return NVFP4_EINVAL;
-        gated_backward_plan(T, H, I, px, pw);
+        gated_backward_plan(T, H, I, px, pw, dx_first);
         if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < gated_backward_bytes(T, H, I, px, pw))
             return NVFP4_EWORKSPACE;
     } else if (!dw13) {
@@ -776,7 +778,7 @@ int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_
     gw.ksplit = pw.ksplit;
     gw.partial = reinterpret_cast<float*>(ws);
     NVFP4_TRY(launch_gated_dgu(d_act, gate_up, T, I, dgu, stream));
-    NVFP4_TRY(launch_gated_backward(dx ? &gx : nullptr, dw13 ? &gw : nullptr, stream));
+    NVFP4_TRY(launch_gated_backward(dx ? &gx : nullptr, dw13 ? &gw : nullptr, dx_first, stream));
     if (dx && px.ksplit > 1) NVFP4_TRY(launch_gated_sum(gx.partial, px.ksplit, T * H, dx, stream));
     if (dw13 && pw.ksplit > 1) NVFP4_TRY(launch_gated_sum(gw.partial, pw.ksplit, H * 2 * I, dw13, stream));
     return NVFP4_OK;

@@ -647,7 +647,7 @@ GatedPlan gated_forward_plan(int64_t T, int64_t H, int64_t I) {
     return best;
 }
 
-void gated_backward_plan(int64_t T, int64_t H, int64_t I, GatedPlan& px, GatedPlan& pw) {
+void gated_backward_plan(int64_t T, int64_t H, int64_t I, GatedPlan& px, GatedPlan& pw, bool& dx_first) {
     // dx and dw13 share a launch: the pair whose work-groups, the longer ones
     // first, fill the CUs best
     const Shape sx = {T, H, kGatedBN, H, 2 * I, kKS<kGatedDx>}, sw = {H, 2 * I, kGatedBN, 2 * I, T, kKS<kGatedDw>};
@@ -662,6 +662,7 @@ void gated_backward_plan(int64_t T, int64_t H, int64_t I, GatedPlan& px, GatedPl
                 best_t = t;
                 px = gx;
                 pw = gw;
+                dx_first = wx >= ww;
             }
         });
     });
@@ -669,12 +670,11 @@ void gated_backward_plan(int64_t T, int64_t H, int64_t I, GatedPlan& px, GatedPl
 
 hipError_t launch_gated_forward(const GatedGemm& p, hipStream_t s) { return launch_mode<kGatedFwd>(p, s); }
 
-hipError_t launch_gated_backward(const GatedGemm* gx, const GatedGemm* gw, hipStream_t s) {
+hipError_t launch_gated_backward(const GatedGemm* gx, const GatedGemm* gw, bool dx_first, hipStream_t s) {
     if (!gw) return launch_mode<kGatedDx>(*gx, s);
     if (!gx) return launch_mode<kGatedDw>(*gw, s);
     const int lx = lds_of<kGatedDx>(gx->mi), lw = lds_of<kGatedDw>(gw->mi), lds = lx > lw ? lx : lw;
     const int64_t nx = work_groups(*gx), nw = work_groups(*gw);
-    const bool dx_first = tile_us(gx->mi, 1.0, gx->K / gx->ksplit / 32) >= tile_us(gw->mi, 1.0, gw->K / gw->ksplit / 32);
     static std::atomic<int> lds_set[kMaxDevices];
     hipError_t e = ensure_dynamic_lds(reinterpret_cast<const void*>(&gated_backward_kernel), lds, lds_set);
     if (e != hipSuccess) return e;

@@ -353,10 +353,11 @@ struct GatedGemm {
 };
 struct GatedPlan { int mi, ksplit; };   // tiles of 64 mi rows, K chunks
 GatedPlan gated_forward_plan(int64_t T, int64_t H, int64_t I);
-void gated_backward_plan(int64_t T, int64_t H, int64_t I, GatedPlan& dx, GatedPlan& dw13);
+// (dx_first: the order in which one launch has the two products' work-groups)
+void gated_backward_plan(int64_t T, int64_t H, int64_t I, GatedPlan& dx, GatedPlan& dw13, bool& dx_first);
 hipError_t launch_gated_forward(const GatedGemm& p, hipStream_t s);
 // dx and dw13 in one launch, or (the other null) one of them
-hipError_t launch_gated_backward(const GatedGemm* gx, const GatedGemm* gw, hipStream_t s);
+hipError_t launch_gated_backward(const GatedGemm* gx, const GatedGemm* gw, bool dx_first, hipStream_t s);
 // forward with ksplit > 1: sums, activation and stores
 hipError_t launch_gated_reduce(const GatedGemm& p, hipStream_t s);
 // out = bf16(sum over chunks of partial[c][0 .. n)), n % 4 == 0
