@@ -597,7 +597,8 @@ double tile_us(int mi, double f, int64_t k32) {
 // traffic. A stage takes longer the more CUs are at work (they share the
 // caches and the power); its times are fits to sweeps over tile heights and
 // chunks at 1 to 4096 rows, where the choice is within a few percent of the
-// best one.
+// best one. (Wide layers too: H 4096 or 5120, I 13824 to 17920, 1 to 4096 rows,
+// forward and backward: within 2 % of the best of a sweep.)
 namespace {
 
 struct Shape { int64_t M, ncols, tile_cols, outcols, K; int kstage; };
@@ -653,7 +654,6 @@ void gated_backward_plan(int64_t T, int64_t H, int64_t I, GatedPlan& px, GatedPl
     const Shape sx = {T, H, kGatedBN, H, 2 * I, kKS<kGatedDx>}, sw = {H, 2 * I, kGatedBN, 2 * I, T, kKS<kGatedDw>};
     double best_t = 1e30;
     each_plan(sx, 8, [&](GatedPlan gx, int64_t nx, int64_t kx, double ex) {
-        if (gx.ksplit == 5 || gx.ksplit == 7) return;
         each_plan(sw, 4, [&](GatedPlan gw, int64_t nw, int64_t kw, double ew) {
             const double f = nx + nw < 256 ? (nx + nw) / 256.0 : 1.0;
             const double wx = tile_us(gx.mi, f, kx), ww = tile_us(gw.mi, f, kw);

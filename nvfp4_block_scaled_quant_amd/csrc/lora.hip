@@ -1032,7 +1032,9 @@ hipError_t launch_stream(const LoraParams& p, const uint8_t* aqp, const uint8_t*
 // the launch to about two work-groups per CU. Listed tiles hold few adapters,
 // which the host cannot know; counting one per tile, with room for the tiles
 // where two meet, is right for runs of rows. A streamed tile's rows are not
-// listed: each may have its own.
+// listed: each may have its own. The two counts are not sharp: with anything from
+// 256 to 1024 the whole operator took the same time within 2 % at 7 to 4093 rows;
+// with 128 it took 7 % longer at 61 rows (29.2 us against 27.2) and 3 % at 1500.
 int lora_planes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     const int64_t tiles = (M + kLoraRows - 1) / kLoraRows, rbs = (R + kRankBlock - 1) / kRankBlock;
     const int64_t rows = M < kLoraRows ? M : kLoraRows;
