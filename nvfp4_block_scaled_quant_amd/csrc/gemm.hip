@@ -670,8 +670,9 @@ void gemm_kernel(GemmParams p) {
                     }
                     const int steps = min(4, (rank - r0 + 15) / 16);
                     // whether this wave's columns of B_a hold anything that is not
-                    // finite (see lora_finite). Looked up once: 3 us of 350 at 4093
-                    // rows, R 64; masks in every product took 6.
+                    // finite (see lora_finite). Looked up once, and the products in
+                    // two forms: 1 to 3 us of 350 at 4093 rows, R 64; masks in every
+                    // product took 6, a test in every product 4.
                     bool wild = false;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
@@ -697,17 +698,21 @@ void gemm_kernel(GemmParams p) {
                             float16_t d;
 #pragma unroll
                             for (int r = 0; r < 16; ++r) d[r] = 0.0f;
+                            auto product = [&](auto finite) {
 #pragma unroll 2
-                            for (int t = 0; t < steps; ++t) {
-                                const uint32_t at = frag ^ (32u * t);
-                                u32x4 b = *reinterpret_cast<const u32x4*>(br + j * 32 * 128 + at);
-                                const bf16x8_t hi = *reinterpret_cast<const bf16x8_t*>(vr + at);
-                                const bf16x8_t lw = *reinterpret_cast<const bf16x8_t*>(vr + V_LOW + at);
-                                if (rank & 7) b = lora_mask_rank(b, r0 + 16 * t + 8 * h, rank);
-                                d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, __builtin_bit_cast(bf16x8_t, b), d, 0, 0, 0);
-                                if (wild) b = lora_finite(b);
-                                d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lw, __builtin_bit_cast(bf16x8_t, b), d, 0, 0, 0);
-                            }
+                                for (int t = 0; t < steps; ++t) {
+                                    const uint32_t at = frag ^ (32u * t);
+                                    u32x4 b = *reinterpret_cast<const u32x4*>(br + j * 32 * 128 + at);
+                                    const bf16x8_t hi = *reinterpret_cast<const bf16x8_t*>(vr + at);
+                                    const bf16x8_t lw = *reinterpret_cast<const bf16x8_t*>(vr + V_LOW + at);
+                                    if (rank & 7) b = lora_mask_rank(b, r0 + 16 * t + 8 * h, rank);
+                                    d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, __builtin_bit_cast(bf16x8_t, b), d, 0, 0, 0);
+                                    if (!decltype(finite)::value) b = lora_finite(b);
+                                    d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lw, __builtin_bit_cast(bf16x8_t, b), d, 0, 0, 0);
+                                }
+                            };
+                            if (wild) product(std::false_type{});
+                            else product(std::true_type{});
 #pragma unroll
                             for (int r = 0; r < 16; ++r)
                                 acc[i][j][r] += (mine >> (8 * (r >> 2) + (r & 3))) & 1u ? d[r] : 0.0f;
