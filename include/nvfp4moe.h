@@ -431,7 +431,7 @@ int nvfp4_route_topk(const float* logits, int64_t T, int64_t E, int64_t topk,
  *   with a = adapter_ids[m]; rows whose id is outside [0, L) get the first
  *   term alone. One rounding; the sums are float32, and the shrunk row
  *   scale * x A^T enters the second product in float32 or as the sum of two
- *   bf16 values (2^-17 relative).
+ *   bf16 values (within 2^-17 relative, or 2^-134 where that is more).
  *
  *   aq, asf, a_gs, bq, bsf, b_alpha, M, N, K, out   as nvfp4_gemm
  *   x            (M, K) bf16, what aq was quantized from
@@ -469,7 +469,8 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs,
  *
  *   gate = x @ w13[:, :I], up = x @ w13[:, I:]        float32 sums
  *   act  = bf16(silu(gate) * up), silu(z) = z / (1 + exp(-z)), float32 from
- *          the unrounded sums, one rounding
+ *          the unrounded sums, one rounding (exp(-|z|) below 2^-126, |z| from
+ *          87.4 on, counts as zero)
  *
  *   x        (T, H) bf16
  *   w13      (H, 2I) bf16, the math layout [gate | up] along the columns (one

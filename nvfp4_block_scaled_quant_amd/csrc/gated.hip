@@ -33,17 +33,18 @@
 // float32 partial sums, and a second kernel adds them in chunk order (the
 // result does not depend on scheduling) before the one rounding.
 //
-// What bounds it, and what it measured (H 7168, I 2048 but for the last line):
-//   T 1, 23      the weights, 58.7 MB once: 12.3 us (4.8 TB/s) and 13.5 us, and
+// What bounds it, and what it measured (medians; H 7168, I 2048 but for the last
+// line):
+//   T 1, 23      the weights, 58.7 MB once: 12.2 us (4.8 TB/s) and 13.5 us, and
 //                4 us for the chunks' sums
 //   T 301        the caches: every stage of a tile is 24 KB for 1/2 us of matrix
 //                work; 26 us + 6 us for the chunks' sums
 //   T 4096       the matrix cores at the clock that they get under load, 2.0 GHz:
-//                forward 195 us (1.23 PFLOP/s; no LDS bank conflicts, the
-//                matrix pipes busy 59 % of the cycles), both products of the
-//                backward 410 us (1.17 PFLOP/s)
+//                forward 192 to 198 us in calls back to back (1.2 PFLOP/s; no LDS
+//                bank conflicts, the matrix pipes busy 59 % of the cycles), both
+//                products of the backward 405 to 414 us (1.17 PFLOP/s)
 //   1001 rows, H 4112, I 1360   the ends: 499 tiles of unequal lengths on 256 CUs,
-//                and both widths end 16 columns into a tile; backward 59 us
+//                and both widths end 16 columns into a tile; products 57 to 61 us
 // Four waves of 128 x 128 outputs, which read LDS less often, were slower (218
 // us against 194 for the forward: one wave per SIMD leaves no one to issue while
 // it waits).
@@ -93,8 +94,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, 0x7FFFFFFF, kRsrcWord3);
 }
 
-// e^-|g|, at most 1, so neither sign of g overflows. Below -200 it is zero
-// anyway; exp_split's own steps overflow beyond about 2^127.
+// e^-|g|, at most 1, so neither sign of g overflows. It is zero from |g| = 87.4 on
+// (no subnormal results: silu there is below 2^-119 of u); exp_split's own steps
+// overflow beyond about 2^127.
 __device__ __forceinline__ float exp_neg_abs(float g) { return exp_split(fmaxf(-__builtin_fabsf(g), -200.0f)); }
 
 // 1 / (1 + e^-g) by e^-|g|, and silu(g) * u, in float32.

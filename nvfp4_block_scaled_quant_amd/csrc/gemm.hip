@@ -588,7 +588,8 @@ void gemm_kernel(GemmParams p) {
         } else if (MODE == kGemmLora) {
             // The adapters, on the matrix cores, into the same accumulators:
             // delta = v B_a^T per adapter that occurs in the tile (the rows are
-            // grouped by adapter: one or two) and 32-row block that has it, added
+            // grouped by adapter: one or two in runs of rows, up to one per row of
+            // the tile where many adapters have few rows) and 32-row block that has it, added
             // to the rows that have the adapter (the others' results are dropped
             // by a select, not multiplied by zero: a NaN of one adapter reaches no
             // other row). v enters as the sum of two bf16 values, B_a is bf16.

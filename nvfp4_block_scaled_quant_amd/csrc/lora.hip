@@ -25,20 +25,21 @@
 // neighbours, 16 bytes an address, and ran at a quarter of the rate. Ranges of
 // K are separate partial sums, added in order by the reader.
 //
-// What it measured (N 6144, K 7168; beside it the projection alone):
-//   1 row,     L 8,  R 16   one launch, 14 us (see there); shrink and stream
+// What it measured (medians of a kernel trace; N 6144, K 7168; beside it the
+// projection alone):
+//   1 row,     L 8,  R 16   one launch, 14.8 us (see there); shrink and stream
 //                           were 6.5 and 9.5
-//   13 rows of 7168 x 2048, L 16, R 64   shrink 5.9, stream 9.3: latency
-//   61 rows,   L 32, R 32   shrink 8.6 (15 MB of adapters, x and A), stream 18.5
+//   13 rows of 7168 x 2048, L 16, R 64   shrink 5.9, stream 10: latency
+//   61 rows,   L 32, R 32   shrink 8.4 (15 MB of adapters, x and A), stream 19
 //                           (25 MB of weights; their conversion and that of
 //                           four row blocks of A: the vector units are active
 //                           half the cycles, the matrix pipes a fifth, and 64
 //                           CUs have no columns)
-//   256 rows,  L 6,  R 16   shrink 9.4, tiled GEMM 28, chunks' sum and expand 10
-//                           (nvfp4_gemm 38 in all)
+//   256 rows,  L 6,  R 16   shrink 9.4, tiled GEMM 27.5, chunks' sum and expand
+//                           10.5 (nvfp4_gemm: 3.3, 27.8 and 6.3)
 //   4093 rows, L 8,  R 64   sort 7, shrink 35 (59 MB of x and 16 MB of A read, 59
 //                           MB of f16 written), join 5, GEMM with the expand 320
-//                           (without it 292): the matrix cores
+//                           (without it 297): the matrix cores
 #include <type_traits>
 
 #include "common.hpp"
@@ -325,8 +326,8 @@ __global__ __launch_bounds__(NT) void lora_shrink_kernel(LoraParams p, int tiles
 }
 
 // ---------------------------------------------------------------------------
-// Rows by adapter. One work-group counts, scans and places (7 us at 4093 rows,
-// 16 to 20 at 16384); the rows of one adapter come in no particular order (a
+// Rows by adapter. One work-group counts, scans and places, about 1 us per thousand
+// rows (7 us at 4093, 14 to 17 at 16384, 120 to 130 at 131072); the rows of one adapter come in no particular order (a
 // row's result does not depend on its place). Where at least 16 lanes of a wave share an adapter, as in runs of
 // rows, one of them counts for all: an LDS atomic takes one address at a time.
 constexpr int ST = 1024;
@@ -549,7 +550,7 @@ struct Expand {
 };
 
 // K chunks: out = bf16(alpha * (their sum, in order) + adapters), for one tile
-// of 64 listed rows and 32 columns. 10.3 us at 256 x 6144 and 5 chunks (31 MB of
+// of 64 listed rows and 32 columns. 10.5 us at 256 x 6144 and 5 chunks (31 MB of
 // sums, held by the caches; the sum alone takes 6.6).
 constexpr int RT = 256;
 __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles, const float* __restrict__ partial,
@@ -622,7 +623,7 @@ __global__ __launch_bounds__(RT) void lora_reduce_kernel(LoraParams p, int tiles
 // sums meet in LDS (added in wave order), where the expand's are too. The other
 // waves do the expand meanwhile (loads return in order: in a wave that streams,
 // the adapters' operands would arrive after its weights). 9.5 us for one row of
-// 6144 x 7168 (24.8 MB of weights: 2.6 TB/s, most of it start and end), 18.5 us
+// 6144 x 7168 (24.8 MB of weights: 2.6 TB/s, most of it start and end), 19 us
 // for 61 rows; the tiled form with its two further kernels took 49 us there.
 template <int MT, int CB>
 __global__ __launch_bounds__(MT == 4 ? NT + 256 : NT) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : MT == 4 ? 3 : 2)))
