@@ -40,7 +40,7 @@
 //   T 301        the caches: every stage of a tile is 24 KB for 1/2 us of matrix
 //                work; 26 us + 6 us for the chunks' sums
 //   T 4096       the matrix cores at the clock that they get under load, 2.0 GHz:
-//                forward 192 to 198 us in calls back to back (1.2 PFLOP/s; no LDS
+//                forward 192 to 202 us in calls back to back (1.2 PFLOP/s; no LDS
 //                bank conflicts, the matrix pipes busy 59 % of the cycles), both
 //                products of the backward 405 to 414 us (1.17 PFLOP/s)
 //   1001 rows, H 4112, I 1360   the ends: 499 tiles of unequal lengths on 256 CUs,
