@@ -431,7 +431,9 @@ int nvfp4_route_topk(const float* logits, int64_t T, int64_t E, int64_t topk,
  *   with a = adapter_ids[m]; rows whose id is outside [0, L) get the first
  *   term alone. One rounding; the sums are float32, and the shrunk row
  *   scale * x A^T enters the second product in float32 or as the sum of two
- *   bf16 values (within 2^-17 relative, or 2^-134 where that is more).
+ *   bf16 values (within 2^-17 relative, or 2^-134 where that is more). Sums
+ *   over ranges of K are scaled before they are added: a scale that takes one of
+ *   them out of float32's range takes the row out of it.
  *
  *   aq, asf, a_gs, bq, bsf, b_alpha, M, N, K, out   as nvfp4_gemm
  *   x            (M, K) bf16, what aq was quantized from
@@ -452,7 +454,8 @@ int nvfp4_route_topk(const float* logits, int64_t T, int64_t E, int64_t topk,
  *
  * Workspace: nvfp4_gemm_lora_workspace(M, N, K, L, R) bytes, 256-byte
  * aligned (the shrunk rows, and A in the form that the kernels of the batch
- * size take); 0 for invalid sizes. M == 0 enqueues nothing.
+ * size take); 0 for invalid sizes. A smaller M may need more (its few tiles
+ * have K cut into chunks). M == 0 enqueues nothing.
  * ------------------------------------------------------------------------ */
 size_t nvfp4_gemm_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
 int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs,
@@ -485,8 +488,8 @@ int nvfp4_gemm_lora(const uint8_t* aq, const uint8_t* asf, const float* a_gs,
  * alone. A row of x affects no other row of the outputs, whatever its values.
  *
  * Workspace: nvfp4_gated_workspace(T, H, I) bytes, 256-byte aligned: partial
- * sums of small batches, whose few tiles have H cut into chunks. It returns 0
- * for invalid sizes.
+ * sums of small batches, whose few tiles have H cut into chunks; a smaller T
+ * may need more. It returns 0 for invalid sizes.
  * ------------------------------------------------------------------------ */
 size_t nvfp4_gated_workspace(int64_t T, int64_t H, int64_t I);
 int nvfp4_gated_forward(const uint16_t* x, const uint16_t* w13, int64_t T, int64_t H, int64_t I,
@@ -511,8 +514,8 @@ int nvfp4_gated_forward(const uint16_t* x, const uint16_t* w13, int64_t T, int64
  * T == 0, dw13 is zero. Both outputs NULL: NVFP4_EINVAL.
  *
  * Workspace: nvfp4_gated_backward_workspace(T, H, I) bytes, 256-byte aligned
- * ([dgate | dup], and partial sums where the tiles are few); 0 for invalid
- * sizes.
+ * ([dgate | dup], and partial sums where the tiles are few: a smaller T may
+ * need more); 0 for invalid sizes.
  * ------------------------------------------------------------------------ */
 size_t nvfp4_gated_backward_workspace(int64_t T, int64_t H, int64_t I);
 int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_t* w13,
