@@ -523,6 +523,149 @@ int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_
                          uint16_t* dx, uint16_t* dw13,
                          void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------ *
+ * Operators around the experts: tokens sorted by expert and back, with
+ * gradients, the router's gradient, products of a few rows with 4-bit weights,
+ * and dropout. They need no workspace but for the sort.
+ *
+ * dtype names the type of the tensors declared void*. Those are aligned to their
+ * elements (2 or 4 bytes), rows to nothing more, unless stated otherwise. Values
+ * enter every sum in float32 and each result is rounded once, to nearest-even;
+ * NaN and infinities give what the formulas give.
+ * ------------------------------------------------------------------------ */
+typedef enum nvfp4_dtype { NVFP4_BF16 = 0, NVFP4_F16 = 1, NVFP4_F32 = 2 } nvfp4_dtype;
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_sort_tokens - the expert layer's permutation on rows of any type: one
+ * slot per (t, j) whose id topk_ids[t][j] is in [0, E), sorted by expert and
+ * among equal experts by t * topk + j.
+ *
+ *   x         (T, H)
+ *   topk_ids  (T, topk) int32; ids outside [0, E) (experts that other GPUs hold)
+ *             have no row; a token may name an expert more than once
+ *   rows      (T * topk, H) out: rows[slot_row[t][j]] = x[t]. Rows from
+ *             offsets[E] on are left as they were.
+ *   offsets   (E + 1) int32 out: expert e has rows offsets[e] .. offsets[e + 1]
+ *   slot_row  (T, topk) int32 out: the row of each slot, -1 if it has none
+ *   E <= 512, topk <= 512, T <= 2^24, H <= 2^20, T * topk <= 2^30, else
+ *   NVFP4_ESHAPE. Outputs overlap no input and each other. T == 0 writes offsets.
+ *
+ * Workspace: nvfp4_sort_tokens_workspace(T, E, topk) bytes, 256-byte aligned; 0
+ * for invalid sizes.
+ *
+ * nvfp4_sort_tokens_backward: dx[t] = sum_j d_rows[slot_row[t][j]], in the order
+ * of j. d_rows (R, H), entries of slot_row outside [0, R) contribute nothing.
+ * ------------------------------------------------------------------------ */
+size_t nvfp4_sort_tokens_workspace(int64_t T, int64_t E, int64_t topk);
+int nvfp4_sort_tokens(const void* x, int dtype, const int32_t* topk_ids,
+                      int64_t T, int64_t H, int64_t E, int64_t topk,
+                      void* rows, int32_t* offsets, int32_t* slot_row,
+                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+int nvfp4_sort_tokens_backward(const void* d_rows, int dtype, const int32_t* slot_row,
+                               int64_t T, int64_t H, int64_t topk, int64_t R,
+                               void* dx, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_unsort_tokens - expert rows back to their tokens, weights applied (the
+ * layer's combine on rows of any type):
+ *
+ *   y[t] = sum_j topk_weights[t][j] * rows[slot_row[t][j]], in the order of j
+ *
+ *   rows          (R, H)
+ *   slot_row      (T, topk) int32; entries outside [0, R) contribute nothing,
+ *                 whatever their weight
+ *   topk_weights  (T, topk) float32, used as given
+ *   y             (T, H) out; sizes as in nvfp4_sort_tokens, R <= 2^30
+ *
+ * nvfp4_unsort_tokens_backward: its gradients,
+ *   d_rows[slot_row[t][j]] = topk_weights[t][j] * dy[t]
+ *   d_weights[t][j] = sum_h dy[t][h] * rows[slot_row[t][j]][h]
+ *   d_rows     (R, H) out, or NULL (not computed; topk_weights may then be NULL).
+ *              Rows that slot_row does not name are left as they were; one that
+ *              it names twice holds one of the two products.
+ *   d_weights  (T, topk) float32 out, or NULL (not computed; rows may then be
+ *              NULL); 0 for slots without a row
+ * Both outputs NULL: NVFP4_EINVAL (unless there is nothing to write). Outputs
+ * overlap no input and each other.
+ * ------------------------------------------------------------------------ */
+int nvfp4_unsort_tokens(const void* rows, int dtype, const int32_t* slot_row, const float* topk_weights,
+                        int64_t T, int64_t H, int64_t topk, int64_t R, void* y, hipStream_t stream);
+int nvfp4_unsort_tokens_backward(const void* dy, const void* rows, int dtype, const int32_t* slot_row,
+                                 const float* topk_weights, int64_t T, int64_t H, int64_t topk, int64_t R,
+                                 void* d_rows, float* d_weights, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_route_topk_backward - the gradient of nvfp4_route_topk's weights with
+ * respect to its logits:
+ *
+ *   d_logits[t][e] = sum over j with topk_ids[t][j] = e of
+ *                    w_j * (d_weights[t][j] - sum_i w_i * d_weights[t][i]),
+ *   w = topk_weights[t], and 0 for experts that were not chosen
+ *
+ *   d_weights, topk_ids, topk_weights  (T, topk) float32, int32, float32
+ *   d_logits  (T, E) float32 out
+ *   Sizes as in nvfp4_route_topk. Ids outside [0, E) name no logit; their weights
+ *   count in the inner sum.
+ * ------------------------------------------------------------------------ */
+int nvfp4_route_topk_backward(const float* d_weights, const int32_t* topk_ids, const float* topk_weights,
+                              int64_t T, int64_t E, int64_t topk, float* d_logits, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_matvec - a few rows times 4-bit weights with group scales (nvfp4_gemm's
+ * weights, the activation not quantized):
+ *
+ *   out[m][n] = b_alpha[e] * sum_k x[m][k] * deqB_e[k][n]
+ *   with NVFP4_MATVEC_GATED: columns [gate | up], out (M, N / 2) =
+ *   silu(gate) * up of the float32 sums, silu(z) = z / (1 + exp(-z)) (exp(-|z|)
+ *   below 2^-126 counts as zero)
+ *
+ *   x        (M, K) bf16 or f16 (dtype), 16-byte aligned
+ *   bq, bsf  E packed matrices of K x N (nvfp4_prepack_weights), bq 16-byte and
+ *            bsf 8-byte aligned
+ *   b_alpha  (E) float32; with NVFP4_MATVEC_ALPHA_PER_HALF (gated only) (E, 2):
+ *            [e][0] for gate, [e][1] for up
+ *   offsets  NULL: E is 1, its matrix for all rows; or (E + 1) int32, not
+ *            decreasing: rows offsets[e] .. offsets[e + 1] take matrix e
+ *            (nvfp4_sort_tokens). Rows outside all of these are not written;
+ *            what lies beyond M is ignored.
+ *   out      (M, N) of x's type; overlaps no input
+ *   K % 16 == 0, N % 16 == 0 (gated: 32), E <= 512, K <= 2^20, M <= 2^24,
+ *   N * pitch_q(K) below 2^31, else NVFP4_ESHAPE (also where the work-groups,
+ *   (M / 16 + E) * N / 16 at most, reach 2^31).
+ * Made for up to about 16 rows of a matrix, which read it once; each 16 more read
+ * it again (many rows: nvfp4_gemm). A row's result depends on its own values,
+ * its matrix and the sizes alone.
+ * ------------------------------------------------------------------------ */
+enum { NVFP4_MATVEC_GATED = 1, NVFP4_MATVEC_ALPHA_PER_HALF = 2 };
+int nvfp4_matvec(const void* x, int dtype, const uint8_t* bq, const uint8_t* bsf, const float* b_alpha,
+                 const int32_t* offsets, int64_t M, int64_t N, int64_t K, int64_t E, int flags,
+                 void* out, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * nvfp4_dropout - dropout whose mask is a function of the element's index:
+ *
+ *   y[i] = (residual ? residual[i] : 0) + (kept(i) ? x[i] * scale : 0),
+ *   scale = 1 / (1 - p) rounded to float32
+ *   kept(i): word i % 4 of Philox4x32 in seven rounds (Salmon, Moraes, Dror,
+ *   Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011) of the counter
+ *   rng[1] + i / 4 (64 bits, wrapping; the upper 64 are zero) under the key rng[0]
+ *   is at least p * 2^32, rounded half up. p = 1 keeps nothing.
+ *
+ *   x, residual (or NULL), y   n elements
+ *   rng   (2) int64 on the device: seed and offset, read when the call runs (a
+ *         captured call follows their changes). A call uses the counters
+ *         offset .. offset + (n + 3) / 4: a program moves the offset on by as many.
+ *   0 <= p <= 1, n <= 2^48. y may be x or residual itself, and overlaps neither in
+ *   part. What is not kept enters nothing, NaN and infinities included.
+ *
+ * nvfp4_dropout_backward: dx[i] = kept(i) ? dy[i] * scale : 0, with the forward's
+ * p and rng (the gradient of residual is dy).
+ * ------------------------------------------------------------------------ */
+int nvfp4_dropout(const void* x, const void* residual, int dtype, int64_t n, double p, const int64_t* rng,
+                  void* y, hipStream_t stream);
+int nvfp4_dropout_backward(const void* dy, int dtype, int64_t n, double p, const int64_t* rng,
+                           void* dx, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,14 @@ mirror the C ABI in include/nvfp4moe.h:
               adapter_ids)           -> out (bf16)        gemm + per-row adapters
     gated_forward(x, w13)            -> act               bf16 gated feed-forward block
     gated_backward(d_act, x, w13, gate_up) -> (dx, dw13)  its gradients
+    sort_tokens(x, topk_ids, num_experts) -> (rows, offsets, slot_row)
+    sort_tokens_backward(d_rows, slot_row) -> dx
+    unsort_tokens(rows, slot_row, topk_weights) -> y
+    unsort_tokens_backward(dy, rows, slot_row, topk_weights) -> (d_rows, d_weights)
+    route_topk_backward(d_weights, topk_ids, topk_weights, num_experts) -> d_logits
+    matvec(x, bq, bsf, b_alpha, offsets=None, gated=False) -> out   x not quantized
+    dropout(x, p, rng, residual=None) -> y      counter-based, no mask stored
+    dropout_backward(dy, p, rng)     -> dx
 
 The library must be built in-tree first (``python -m
 nvfp4_block_scaled_quant_amd.build``); importing this package without it
@@ -68,6 +76,15 @@ _SIGS = {
     "nvfp4_gated_forward": ([_vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp], _int),
     "nvfp4_gated_backward_workspace": ([_i64, _i64, _i64], _sz),
     "nvfp4_gated_backward": ([_vp] * 4 + [_i64] * 3 + [_vp, _vp, _vp, _sz, _vp], _int),
+    "nvfp4_sort_tokens_workspace": ([_i64] * 3, _sz),
+    "nvfp4_sort_tokens": ([_vp, _int, _vp] + [_i64] * 4 + [_vp] * 4 + [_sz, _vp], _int),
+    "nvfp4_sort_tokens_backward": ([_vp, _int, _vp] + [_i64] * 4 + [_vp, _vp], _int),
+    "nvfp4_unsort_tokens": ([_vp, _int, _vp, _vp] + [_i64] * 4 + [_vp, _vp], _int),
+    "nvfp4_unsort_tokens_backward": ([_vp, _vp, _int, _vp, _vp] + [_i64] * 4 + [_vp, _vp, _vp], _int),
+    "nvfp4_route_topk_backward": ([_vp] * 3 + [_i64] * 3 + [_vp, _vp], _int),
+    "nvfp4_matvec": ([_vp, _int] + [_vp] * 4 + [_i64] * 4 + [_int, _vp, _vp], _int),
+    "nvfp4_dropout": ([_vp, _vp, _int, _i64, ctypes.c_double, _vp, _vp, _vp], _int),
+    "nvfp4_dropout_backward": ([_vp, _int, _i64, ctypes.c_double, _vp, _vp, _vp], _int),
     "nvfp4_moe_forward_noalloc": ([_vp] * 9 + [_i64] * 5 + [_vp, _vp, _vp, _vp], _int),
 }
 
@@ -597,6 +614,227 @@ def gated_backward(d_act, x, w13, gate_up, dx=None, dw13=None, need_dx=True, nee
                                      ws_ptr, ws_bytes, torch._C._cuda_getCurrentRawStream(index)),
            "nvfp4_gated_backward")
     return dx, dw13
+
+
+# element types of the operators that take several (enum nvfp4_dtype)
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_MATVEC_GATED, _MATVEC_ALPHA_PER_HALF = 1, 2
+
+
+def _typed(t, name, dim=None):
+    """The dtype code of a contiguous tensor on the GPU in one of _DTYPES."""
+    if isinstance(t, torch.Tensor) and t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    _need(t, t.dtype if isinstance(t, torch.Tensor) else None, name, dim)
+    return _DTYPES[t.dtype]
+
+
+def _slots(slot_row, index):
+    """T, topk and address of a (T, topk) int32 tensor on device `index`."""
+    if not isinstance(slot_row, torch.Tensor) or slot_row.dim() != 2 or slot_row.shape[1] < 1:
+        _need(slot_row, torch.int32, "slot_row", 2)
+        raise ValueError("slot_row must be (T, topk) with topk at least 1")
+    return (*slot_row.shape, _operands(index, (slot_row, torch.int32, slot_row.shape, "slot_row"))[0])
+
+
+def sort_tokens(x, topk_ids, num_experts, rows=None, workspace=None):
+    """Tokens sorted by expert: x (T, H) bf16, f16 or f32, topk_ids int32 (T,
+    topk) -> (rows (T * topk, H), offsets int32 (num_experts + 1), slot_row int32
+    (T, topk)). Slots whose id is in [0, num_experts) in order of expert, then of
+    t * topk + j; rows[slot_row[t, j]] = x[t], slot_row is -1 where there is no row,
+    and expert e has the rows from offsets[e] to offsets[e + 1]. Rows from
+    offsets[num_experts] on are not written (uninitialized unless `rows` is given).
+    No graph: see gated_forward."""
+    _refuse_recording("sort_tokens", x=x)
+    code = _typed(x, "x", 2)
+    index = x.get_device()
+    if index != torch._C._cuda_getDevice():                 # the library launches on the current device
+        with torch.cuda.device(index):
+            return sort_tokens(x, topk_ids, num_experts, rows, workspace)
+    T, H = x.shape
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2 or topk_ids.shape[1] < 1:
+        _need(topk_ids, torch.int32, "topk_ids", 2)
+        raise ValueError("topk_ids must be (T, topk) with topk at least 1")
+    k = topk_ids.shape[1]
+    ids = _operands(index, (topk_ids, torch.int32, (T, k), "topk_ids"))[0]
+    rows = _result(rows, x, (T * k, H), "rows", index)
+    offsets, slot_row = topk_ids.new_empty(num_experts + 1), topk_ids.new_empty((T, k))
+    ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.nvfp4_sort_tokens_workspace(T, num_experts, k), index)
+    _check(_lib.nvfp4_sort_tokens(x.data_ptr(), code, ids, T, H, num_experts, k, rows.data_ptr(), offsets.data_ptr(),
+                                  slot_row.data_ptr(), ws_ptr, ws_bytes, torch._C._cuda_getCurrentRawStream(index)),
+           "nvfp4_sort_tokens")
+    return rows, offsets, slot_row
+
+
+def sort_tokens_backward(d_rows, slot_row, dx=None):
+    """Gradient of sort_tokens: dx[t] = sum_j d_rows[slot_row[t, j]] over the slots
+    that have a row; d_rows (R, H) -> dx (T, H) of its type. No graph of its own."""
+    _refuse_recording("sort_tokens_backward", d_rows=d_rows)
+    code = _typed(d_rows, "d_rows", 2)
+    index = d_rows.get_device()
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return sort_tokens_backward(d_rows, slot_row, dx)
+    R, H = d_rows.shape
+    T, k, at = _slots(slot_row, index)
+    dx = _result(dx, d_rows, (T, H), "dx", index)
+    _check(_lib.nvfp4_sort_tokens_backward(d_rows.data_ptr(), code, at, T, H, k, R, dx.data_ptr(),
+                                           torch._C._cuda_getCurrentRawStream(index)), "nvfp4_sort_tokens_backward")
+    return dx
+
+
+def unsort_tokens(rows, slot_row, topk_weights, y=None):
+    """Expert rows back to their tokens: y[t] = sum_j topk_weights[t, j] *
+    rows[slot_row[t, j]] over the slots that have a row, float32 sums, rounded
+    once; rows (R, H), topk_weights float32 (T, topk) -> y (T, H) of rows' type.
+    No graph: see gated_forward."""
+    _refuse_recording("unsort_tokens", rows=rows, topk_weights=topk_weights)
+    code = _typed(rows, "rows", 2)
+    index = rows.get_device()
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return unsort_tokens(rows, slot_row, topk_weights, y)
+    R, H = rows.shape
+    T, k, at = _slots(slot_row, index)
+    w = _operands(index, (topk_weights, torch.float32, (T, k), "topk_weights"))[0]
+    y = _result(y, rows, (T, H), "y", index)
+    _check(_lib.nvfp4_unsort_tokens(rows.data_ptr(), code, at, w, T, H, k, R, y.data_ptr(),
+                                    torch._C._cuda_getCurrentRawStream(index)), "nvfp4_unsort_tokens")
+    return y
+
+
+def unsort_tokens_backward(dy, rows, slot_row, topk_weights, d_rows=None, d_weights=None, need_d_rows=True,
+                           need_d_weights=True):
+    """Gradients of unsort_tokens: dy (T, H), rows (R, H) -> (d_rows (R, H),
+    d_weights float32 (T, topk)). d_rows[slot_row[t, j]] = topk_weights[t, j] * dy[t];
+    rows that slot_row does not name are not written (uninitialized unless d_rows
+    is given). need_d_rows / need_d_weights = False: None in that place. No graph
+    of its own."""
+    _refuse_recording("unsort_tokens_backward", dy=dy, rows=rows, topk_weights=topk_weights)
+    code = _typed(dy, "dy", 2)
+    index = dy.get_device()
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return unsort_tokens_backward(dy, rows, slot_row, topk_weights, d_rows, d_weights, need_d_rows,
+                                          need_d_weights)
+    T, k, at = _slots(slot_row, index)
+    _need(rows, dy.dtype, "rows", 2, dy.device)
+    R, H = rows.shape
+    p_dy, w = _operands(index, (dy, dy.dtype, (T, H), "dy"), (topk_weights, torch.float32, (T, k), "topk_weights"))
+    if not (need_d_rows or need_d_weights):
+        raise ValueError("unsort_tokens_backward: nothing to compute")
+    if (d_rows is not None and not need_d_rows) or (d_weights is not None and not need_d_weights):
+        raise ValueError("unsort_tokens_backward: an output is given for a gradient that is not computed")
+    if need_d_rows:
+        d_rows = _result(d_rows, dy, (R, H), "d_rows", index)
+    if need_d_weights:
+        d_weights = _result(d_weights, topk_weights, (T, k), "d_weights", index)
+    _check(_lib.nvfp4_unsort_tokens_backward(p_dy, rows.data_ptr(), code, at, w, T, H, k, R,
+                                             d_rows.data_ptr() if need_d_rows else None,
+                                             d_weights.data_ptr() if need_d_weights else None,
+                                             torch._C._cuda_getCurrentRawStream(index)),
+           "nvfp4_unsort_tokens_backward")
+    return d_rows, d_weights
+
+
+def route_topk_backward(d_weights, topk_ids, topk_weights, num_experts, d_logits=None):
+    """Gradient of route_topk's weights: d_weights float32 (T, topk), the ids and
+    weights that route_topk gave -> d_logits float32 (T, num_experts), zero for
+    experts that were not chosen. No graph of its own."""
+    _refuse_recording("route_topk_backward", d_weights=d_weights, topk_weights=topk_weights)
+    _need(d_weights, torch.float32, "d_weights", 2)
+    index = d_weights.get_device()
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return route_topk_backward(d_weights, topk_ids, topk_weights, num_experts, d_logits)
+    T, k = d_weights.shape
+    ids, w = _operands(index, (topk_ids, torch.int32, (T, k), "topk_ids"),
+                       (topk_weights, torch.float32, (T, k), "topk_weights"))
+    d_logits = _result(d_logits, d_weights, (T, num_experts), "d_logits", index)
+    _check(_lib.nvfp4_route_topk_backward(d_weights.data_ptr(), ids, w, T, num_experts, k, d_logits.data_ptr(),
+                                          torch._C._cuda_getCurrentRawStream(index)), "nvfp4_route_topk_backward")
+    return d_logits
+
+
+def matvec(x, bq, bsf, b_alpha, offsets=None, gated=False, out=None):
+    """A few rows times packed NVFP4 weights, x (M, K) bf16 or f16 not quantized:
+    out[m] = b_alpha * x[m] @ W, of x's type. One matrix: bq (N/16, halves, 16, 32),
+    bsf (N/16, quads, 16, 32), b_alpha with one float32 (gemm's). With offsets
+    (int32 (E + 1), sort_tokens'): E matrices (packed_shapes), b_alpha (E,); rows
+    offsets[e] .. offsets[e + 1] take matrix e, other rows are not written
+    (uninitialized unless out is given). gated: N columns [gate | up], out (M,
+    N / 2) = silu(gate) * up of the float32 sums; b_alpha may be per half, (2,) or
+    (E, 2). K % 16 == 0. No graph: see gated_forward."""
+    if torch.is_grad_enabled():
+        _refuse_recording("matvec", x=x, b_alpha=b_alpha)
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("x must be a bfloat16 or float16 CUDA (HIP) tensor")
+    _need(x, x.dtype, "x", 2)
+    index = x.get_device()
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return matvec(x, bq, bsf, b_alpha, offsets, gated, out)
+    M, K = x.shape
+    _need(bq, torch.uint8, "bq", 4 if offsets is None else 5, x.device)
+    if K % 16 or K == 0:
+        raise ValueError("matvec: K must be a positive multiple of 16")
+    lead = () if offsets is None else (bq.shape[0],)
+    E, blocks, steps = bq.shape[0] if lead else 1, bq.shape[len(lead)], (K + 127) // 128
+    N = 16 * blocks
+    if E == 0 or N == 0 or (gated and blocks % 2):
+        raise ValueError("matvec: the weights must have columns (gated: a multiple of 32)")
+    p_q, p_sf = _operands(index, (bq, torch.uint8, lead + (blocks, 2 * steps, 16, 32), "bq"),     # packed_shapes
+                          (bsf, torch.uint8, lead + (blocks, (steps + 3) // 4, 16, 32), "bsf"))
+    alpha = _scalar(b_alpha, "b_alpha", index)
+    flags = _MATVEC_GATED if gated else 0
+    if b_alpha.numel() != E:
+        if not gated or b_alpha.shape != lead + (2,):
+            raise ValueError(f"matvec: b_alpha must hold one float32 per matrix (gated: or two), got "
+                             f"{tuple(b_alpha.shape)}")
+        flags |= _MATVEC_ALPHA_PER_HALF
+    p_off = None if offsets is None else _operands(index, (offsets, torch.int32, (E + 1,), "offsets"))[0]
+    out = _result(out, x, (M, N // 2 if gated else N), "out", index)
+    _check(_lib.nvfp4_matvec(x.data_ptr(), _DTYPES[x.dtype], p_q, p_sf, alpha, p_off, M, N, K, E, flags,
+                             out.data_ptr(), torch._C._cuda_getCurrentRawStream(index)), "nvfp4_matvec")
+    return out
+
+
+def _dropout(where, x, p, rng, residual, y, name, out_name):
+    _refuse_recording(where, **{name: x, "residual": residual})
+    code = _typed(x, name)
+    index = x.get_device()
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _dropout(where, x, p, rng, residual, y, name, out_name)
+    state = _operands(index, (rng, torch.int64, (2,), "rng"))[0]
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"{where}: p must be from 0 to 1, got {p}")
+    y = _result(y, x, x.shape, out_name, index)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if where == "dropout_backward":
+        _check(_lib.nvfp4_dropout_backward(x.data_ptr(), code, x.numel(), p, state, y.data_ptr(), stream),
+               "nvfp4_dropout_backward")
+        return y
+    r = None if residual is None else _operands(index, (residual, x.dtype, x.shape, "residual"))[0]
+    _check(_lib.nvfp4_dropout(x.data_ptr(), r, code, x.numel(), p, state, y.data_ptr(), stream), "nvfp4_dropout")
+    return y
+
+
+def dropout(x, p, rng, residual=None, y=None):
+    """y = x / (1 - p) where an element is kept, else 0, plus residual if one is
+    given: x bf16, f16 or f32 of any shape, rng int64 (2,) on the device, [seed,
+    offset]. Element i (in memory order) is kept if word i % 4 of the generator's
+    counter offset + i // 4 is at least p * 2**32: the same for every type, and for
+    dropout_backward. Move the offset on by (x.numel() + 3) // 4 for the next call;
+    rng is read on the GPU, so a captured call follows its changes. y may be x or
+    residual. No graph: see gated_forward."""
+    return _dropout("dropout", x, p, rng, residual, y, "x", "y")
+
+
+def dropout_backward(dy, p, rng, dx=None):
+    """Gradient of dropout with the forward's p and rng: dx = dy / (1 - p) where
+    the element was kept, else 0 (residual's gradient is dy)."""
+    return _dropout("dropout_backward", dy, p, rng, None, dx, "dy", "dx")
 
 
 class _Hip:

@@ -19,7 +19,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libnvfp4moe.so")
-SOURCES = ["api.hip", "quantize.hip", "route.hip", "gemm.hip", "skinny.hip", "gated.hip", "lora.hip"]
+SOURCES = ["api.hip", "quantize.hip", "route.hip", "gemm.hip", "skinny.hip", "gated.hip", "lora.hip",
+           "tokens.hip", "matvec.hip", "dropout.hip"]
 ARCH = "gfx950"
 
 

@@ -784,4 +784,185 @@ int nvfp4_gated_backward(const uint16_t* d_act, const uint16_t* x, const uint16_
     return NVFP4_OK;
 }
 
+// ---------------------------------------------------------------------------
+namespace {
+
+bool dtype_ok(int dtype) { return dtype == NVFP4_BF16 || dtype == NVFP4_F16 || dtype == NVFP4_F32; }
+size_t dtype_bytes(int dtype) { return dtype == NVFP4_F32 ? 4 : 2; }
+
+constexpr int64_t kMaxSlots = (int64_t)1 << 30;
+
+bool tokens_shape_ok(int64_t T, int64_t H, int64_t topk, int64_t R) {
+    return T <= (int64_t)1 << 24 && H <= (int64_t)1 << 20 && topk <= kMaxExperts && T * topk <= kMaxSlots &&
+           R <= kMaxSlots;
+}
+
+// What the routing kernels write beside offsets and slot_row.
+struct SortLayout {
+    size_t counts, sorted, tiles, num_tiles, wg_counts, total;
+};
+SortLayout sort_layout(int64_t T, int64_t E, int64_t topk) {
+    SortLayout w;
+    w.counts = 0;
+    w.sorted = align_up((size_t)E * 4);
+    w.tiles = w.sorted + align_up((size_t)(T * topk) * 4);
+    w.num_tiles = w.tiles + align_up((size_t)E * sizeof(Tile));
+    w.wg_counts = w.num_tiles + kAlign;
+    w.total = w.wg_counts + align_up((size_t)kRouteMaxChunks * (size_t)E * 4);
+    return w;
+}
+
+}  // namespace
+
+size_t nvfp4_sort_tokens_workspace(int64_t T, int64_t E, int64_t topk) {
+    if (T < 0 || E <= 0 || E > kMaxExperts || topk <= 0 || !tokens_shape_ok(T, 1, topk, 0)) return 0;
+    return sort_layout(T, E, topk).total;
+}
+
+int nvfp4_sort_tokens(const void* x, int dtype, const int32_t* topk_ids, int64_t T, int64_t H, int64_t E, int64_t topk,
+                      void* rows, int32_t* offsets, int32_t* slot_row, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+    if (T < 0 || H <= 0 || E <= 0 || topk <= 0 || !dtype_ok(dtype)) return NVFP4_EINVAL;
+    if (E > kMaxExperts || !tokens_shape_ok(T, H, topk, 0)) return NVFP4_ESHAPE;
+    if (!offsets || (T > 0 && (!x || !topk_ids || !rows || !slot_row))) return NVFP4_EINVAL;
+    const size_t size = dtype_bytes(dtype);
+    if (!aligned(x, size) || !aligned(rows, size) || !aligned(topk_ids, 4) || !aligned(offsets, 4) ||
+        !aligned(slot_row, 4))
+        return NVFP4_EINVAL;
+    if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < nvfp4_sort_tokens_workspace(T, E, topk))
+        return NVFP4_EWORKSPACE;
+    int dv = check_device();
+    if (dv) return dv;
+    const SortLayout w = sort_layout(T, E, topk);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int64_t S = T * topk;
+    int32_t* wg_counts = reinterpret_cast<int32_t*>(ws + w.wg_counts);
+    NVFP4_TRY(launch_route_prepass(nullptr, 0, nullptr, topk_ids, S, (int)E, wg_counts, stream));
+    NVFP4_TRY(launch_route(topk_ids, S, (int)topk, (int)E, (int)kMaxSlots, wg_counts,
+                           reinterpret_cast<int32_t*>(ws + w.counts), offsets,
+                           reinterpret_cast<int32_t*>(ws + w.sorted), slot_row,
+                           reinterpret_cast<Tile*>(ws + w.tiles), reinterpret_cast<int32_t*>(ws + w.num_tiles),
+                           nullptr, 0, nullptr, stream));
+    if (T > 0) NVFP4_TRY(launch_sort_rows(dtype, x, slot_row, T, H, (int)topk, rows, stream));
+    return NVFP4_OK;
+}
+
+namespace {
+
+// sort_tokens_backward (weights null and not wanted) and unsort_tokens
+int gather_rows(const void* rows, int dtype, const int32_t* slot_row, const float* weights, bool weighted, int64_t T,
+                int64_t H, int64_t topk, int64_t R, void* y, hipStream_t stream) {
+    if (T < 0 || H <= 0 || topk <= 0 || R < 0 || !dtype_ok(dtype)) return NVFP4_EINVAL;
+    if (!tokens_shape_ok(T, H, topk, R)) return NVFP4_ESHAPE;
+    if (T == 0) return NVFP4_OK;
+    if ((R > 0 && !rows) || !slot_row || (weighted && !weights) || !y) return NVFP4_EINVAL;
+    const size_t size = dtype_bytes(dtype);
+    if (!aligned(rows, size) || !aligned(y, size) || !aligned(slot_row, 4) || !aligned(weights, 4))
+        return NVFP4_EINVAL;
+    int dv = check_device();
+    if (dv) return dv;
+    NVFP4_TRY(launch_gather_rows(dtype, rows, slot_row, weights, T, H, (int)topk, R, y, stream));
+    return NVFP4_OK;
+}
+
+}  // namespace
+
+int nvfp4_sort_tokens_backward(const void* d_rows, int dtype, const int32_t* slot_row, int64_t T, int64_t H,
+                               int64_t topk, int64_t R, void* dx, hipStream_t stream) {
+    return gather_rows(d_rows, dtype, slot_row, nullptr, false, T, H, topk, R, dx, stream);
+}
+
+int nvfp4_unsort_tokens(const void* rows, int dtype, const int32_t* slot_row, const float* topk_weights, int64_t T,
+                        int64_t H, int64_t topk, int64_t R, void* y, hipStream_t stream) {
+    return gather_rows(rows, dtype, slot_row, topk_weights, true, T, H, topk, R, y, stream);
+}
+
+int nvfp4_unsort_tokens_backward(const void* dy, const void* rows, int dtype, const int32_t* slot_row,
+                                 const float* topk_weights, int64_t T, int64_t H, int64_t topk, int64_t R,
+                                 void* d_rows, float* d_weights, hipStream_t stream) {
+    if (T < 0 || H <= 0 || topk <= 0 || R < 0 || !dtype_ok(dtype)) return NVFP4_EINVAL;
+    if (!tokens_shape_ok(T, H, topk, R)) return NVFP4_ESHAPE;
+    if (T == 0 || (R == 0 && !d_weights)) return NVFP4_OK;
+    if (!d_rows && !d_weights) return NVFP4_EINVAL;
+    if (!dy || !slot_row || (d_rows && !topk_weights) || (d_weights && R > 0 && !rows)) return NVFP4_EINVAL;
+    const size_t size = dtype_bytes(dtype);
+    if (!aligned(dy, size) || !aligned(rows, size) || !aligned(d_rows, size) || !aligned(slot_row, 4) ||
+        !aligned(topk_weights, 4) || !aligned(d_weights, 4))
+        return NVFP4_EINVAL;
+    int dv = check_device();
+    if (dv) return dv;
+    NVFP4_TRY(launch_unsort_backward(dtype, dy, rows, slot_row, topk_weights, T, H, (int)topk, R, d_rows, d_weights,
+                                     stream));
+    return NVFP4_OK;
+}
+
+int nvfp4_route_topk_backward(const float* d_weights, const int32_t* topk_ids, const float* topk_weights, int64_t T,
+                              int64_t E, int64_t topk, float* d_logits, hipStream_t stream) {
+    if (T < 0 || E <= 0 || topk <= 0) return NVFP4_EINVAL;
+    if (topk > E || E > kMaxExperts || T * E >= ((int64_t)1 << 31)) return NVFP4_ESHAPE;
+    if (T == 0) return NVFP4_OK;
+    if (!d_weights || !topk_ids || !topk_weights || !d_logits) return NVFP4_EINVAL;
+    if (!aligned(d_weights, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(d_logits, 4))
+        return NVFP4_EINVAL;
+    int dv = check_device();
+    if (dv) return dv;
+    NVFP4_TRY(launch_route_topk_backward(d_weights, topk_ids, topk_weights, T, (int)E, (int)topk, d_logits, stream));
+    return NVFP4_OK;
+}
+
+// ---------------------------------------------------------------------------
+int nvfp4_matvec(const void* x, int dtype, const uint8_t* bq, const uint8_t* bsf, const float* b_alpha,
+                 const int32_t* offsets, int64_t M, int64_t N, int64_t K, int64_t E, int flags, void* out,
+                 hipStream_t stream) {
+    if (M < 0 || N <= 0 || K <= 0 || E <= 0 || (dtype != NVFP4_BF16 && dtype != NVFP4_F16)) return NVFP4_EINVAL;
+    if (flags & ~(NVFP4_MATVEC_GATED | NVFP4_MATVEC_ALPHA_PER_HALF)) return NVFP4_EINVAL;
+    const bool gated = flags & NVFP4_MATVEC_GATED, halves = flags & NVFP4_MATVEC_ALPHA_PER_HALF;
+    if (halves && !gated) return NVFP4_EINVAL;
+    if (K % 16 || N % (gated ? 32 : 16) || E > kMaxExperts || (!offsets && E != 1)) return NVFP4_ESHAPE;
+    if (K > (int64_t)1 << 20 || N * pitch_q(K) >= 0x7FFFFFFF || M > (int64_t)1 << 24) return NVFP4_ESHAPE;
+    if (matvec_tiles(M, offsets ? E : 0) * (N / 16) >= (int64_t)1 << 31) return NVFP4_ESHAPE;
+    if (M == 0) return NVFP4_OK;
+    if (!x || !bq || !bsf || !b_alpha || !out) return NVFP4_EINVAL;
+    if (!aligned(x, 16) || !aligned(bq, 16) || !aligned(bsf, 8) || !aligned(b_alpha, 4) || !aligned(offsets, 4) ||
+        !aligned(out, 2))
+        return NVFP4_EINVAL;
+    int dv = check_device();
+    if (dv) return dv;
+    MatvecParams p = {};
+    p.x = x;
+    p.bq = bq;
+    p.bsf = bsf;
+    p.alpha = b_alpha;
+    p.alpha_stride = halves ? 2 : 1;
+    p.offsets = offsets;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.E = (int)E;
+    p.gated = gated;
+    p.out = out;
+    NVFP4_TRY(launch_matvec(p, dtype, stream));
+    return NVFP4_OK;
+}
+
+// ---------------------------------------------------------------------------
+int nvfp4_dropout(const void* x, const void* residual, int dtype, int64_t n, double p, const int64_t* rng, void* y,
+                  hipStream_t stream) {
+    if (n < 0 || !(p >= 0.0 && p <= 1.0) || !dtype_ok(dtype)) return NVFP4_EINVAL;
+    if (n > (int64_t)1 << 48) return NVFP4_ESHAPE;
+    if (n == 0) return NVFP4_OK;
+    if (!x || !rng || !y) return NVFP4_EINVAL;
+    const size_t size = dtype_bytes(dtype);
+    if (!aligned(x, size) || !aligned(residual, size) || !aligned(y, size) || !aligned(rng, 8)) return NVFP4_EINVAL;
+    int dv = check_device();
+    if (dv) return dv;
+    NVFP4_TRY(launch_dropout(dtype, x, residual, n, p, rng, y, stream));
+    return NVFP4_OK;
+}
+
+int nvfp4_dropout_backward(const void* dy, int dtype, int64_t n, double p, const int64_t* rng, void* dx,
+                           hipStream_t stream) {
+    return nvfp4_dropout(dy, nullptr, dtype, n, p, rng, dx, stream);
+}
+
 }  // extern "C"

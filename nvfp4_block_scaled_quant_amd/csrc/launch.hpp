@@ -368,4 +368,41 @@ hipError_t launch_gated_dgu(const uint16_t* d_act, const uint16_t* gate_up, int6
 // zero `bytes` bytes (a multiple of 16, 16-byte aligned)
 hipError_t launch_zero_bytes(void* p, int64_t bytes, hipStream_t s);
 
+// Element types (enum nvfp4_dtype).
+enum Dtype { kBf16 = 0, kF16 = 1, kF32 = 2 };
+
+// Tokens sorted by expert and back (tokens.hip). slot_row (T, k): the sorted row of
+// each slot; entries outside [0, R) (sort_rows: below 0) have none.
+hipError_t launch_sort_rows(int dtype, const void* x, const int32_t* slot_row, int64_t T, int64_t H, int k, void* rows,
+                            hipStream_t s);
+// y[t] = sum over j of w[t][j] (null: 1) rows[slot_row[t][j]]
+hipError_t launch_gather_rows(int dtype, const void* rows, const int32_t* slot_row, const float* w, int64_t T,
+                              int64_t H, int k, int64_t R, void* y, hipStream_t s);
+// d_rows and dw, or one of them (the other null)
+hipError_t launch_unsort_backward(int dtype, const void* dy, const void* rows, const int32_t* slot_row, const float* w,
+                                  int64_t T, int64_t H, int k, int64_t R, void* d_rows, float* dw, hipStream_t s);
+hipError_t launch_route_topk_backward(const float* dw, const int32_t* ids, const float* w, int64_t T, int E, int k,
+                                      float* dl, hipStream_t s);
+
+// A few rows times packed weights (matvec.hip).
+struct MatvecParams {
+    const void* x;             // (M, K) bf16 or f16
+    const uint8_t* bq;         // E matrices of N columns, packed
+    const uint8_t* bsf;
+    const float* alpha;        // E, or 2 E (gate, up)
+    int alpha_stride;
+    const int32_t* offsets;    // (E + 1), or null: one matrix
+    int64_t M, N, K;
+    int E;
+    bool gated;
+    void* out;                 // (M, N), gated (M, N / 2)
+};
+// tiles of 16 rows: all there can be (E = 0: one matrix)
+inline int64_t matvec_tiles(int64_t M, int64_t E) { return E ? M / 16 + (E < M ? E : M) : (M + 15) / 16; }
+hipError_t launch_matvec(const MatvecParams& p, int dtype, hipStream_t s);
+
+// Dropout of n elements (dropout.hip); residual may be null; rng: seed, offset.
+hipError_t launch_dropout(int dtype, const void* x, const void* residual, int64_t n, double p, const int64_t* rng,
+                          void* y, hipStream_t s);
+
 }  // namespace nvfp4
