@@ -397,8 +397,15 @@ struct MatvecParams {
     bool gated;
     void* out;                 // (M, N), gated (M, N / 2)
 };
-// tiles of 16 rows: all there can be (E = 0: one matrix)
-inline int64_t matvec_tiles(int64_t M, int64_t E) { return E ? M / 16 + (E < M ? E : M) : (M + 15) / 16; }
+// Rows of a tile: 4, 8 or 16, by the rows that a matrix has in the mean (48 experts,
+// gated 4096 x 7168, tiles of 4, 8, 16 rows: mean 2.7 125, 141, 201 us; 4.0 146,
+// 137, 201; 5.3 184, 155, 208; 8.0 245, 196, 216; 10.7 303, 243, 232).
+inline int matvec_tile_rows(int64_t M, int64_t E) { return M <= 4 * E ? 4 : M <= 8 * E ? 8 : 16; }
+// tiles: all there can be (E = 0: one matrix)
+inline int64_t matvec_tiles(int64_t M, int64_t E) {
+    const int64_t tm = matvec_tile_rows(M, E ? E : 1);
+    return E ? M / tm + (E < M ? E : M) : (M + tm - 1) / tm;
+}
 hipError_t launch_matvec(const MatvecParams& p, int dtype, hipStream_t s);
 
 // Dropout of n elements (dropout.hip); residual may be null; rng: seed, offset.
