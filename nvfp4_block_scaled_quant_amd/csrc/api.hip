@@ -1,5 +1,6 @@
 // C ABI of the NVFP4 expert-layer library: argument validation, workspace
 // carving and the launch sequence. Declarations and contracts: include/nvfp4moe.h.
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 #include <mutex>
@@ -797,15 +798,20 @@ bool tokens_shape_ok(int64_t T, int64_t H, int64_t topk, int64_t R) {
            R <= kMaxSlots;
 }
 
-// What the routing kernels write beside offsets and slot_row.
+// The chunks' counts, or (large batches of many experts) what the layer's routing
+// kernels write beside offsets and slot_row.
 struct SortLayout {
     size_t counts, sorted, tiles, num_tiles, wg_counts, total;
 };
 SortLayout sort_layout(int64_t T, int64_t E, int64_t topk) {
-    SortLayout w;
-    w.counts = 0;
+    SortLayout w = {};
+    const int64_t S = T * topk;
+    if (sort_small(S, E) || sort_by_counts(S, E, topk)) {
+        w.total = sort_small(S, E) ? kAlign : align_up((size_t)sort_counts_bytes(S, E));
+        return w;
+    }
     w.sorted = align_up((size_t)E * 4);
-    w.tiles = w.sorted + align_up((size_t)(T * topk) * 4);
+    w.tiles = w.sorted + align_up((size_t)S * 4);
     w.num_tiles = w.tiles + align_up((size_t)E * sizeof(Tile));
     w.wg_counts = w.num_tiles + kAlign;
     w.total = w.wg_counts + align_up((size_t)kRouteMaxChunks * (size_t)E * 4);
@@ -833,17 +839,36 @@ int nvfp4_sort_tokens(const void* x, int dtype, const int32_t* topk_ids, int64_t
         return NVFP4_EWORKSPACE;
     int dv = check_device();
     if (dv) return dv;
+    if (T == 0) {
+        NVFP4_TRY(launch_zero_u32(reinterpret_cast<uint32_t*>(offsets), (int)E + 1, stream));
+        return NVFP4_OK;
+    }
     const SortLayout w = sort_layout(T, E, topk);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int64_t S = T * topk;
+    if (sort_small(S, E) || sort_by_counts(S, E, topk)) {
+        SortParams p = {};
+        p.x = x;
+        p.ids = topk_ids;
+        p.T = T;
+        p.H = H;
+        p.E = (int)E;
+        p.k = (int)topk;
+        p.rows = rows;
+        p.offsets = offsets;
+        p.slot_row = slot_row;
+        NVFP4_TRY(launch_sort_tokens(dtype, p, reinterpret_cast<int32_t*>(ws), stream));
+        return NVFP4_OK;
+    }
     int32_t* wg_counts = reinterpret_cast<int32_t*>(ws + w.wg_counts);
     NVFP4_TRY(launch_route_prepass(nullptr, 0, nullptr, topk_ids, S, (int)E, wg_counts, stream));
+    // (one tile per expert: the tile list is not used)
     NVFP4_TRY(launch_route(topk_ids, S, (int)topk, (int)E, (int)kMaxSlots, wg_counts,
                            reinterpret_cast<int32_t*>(ws + w.counts), offsets,
                            reinterpret_cast<int32_t*>(ws + w.sorted), slot_row,
                            reinterpret_cast<Tile*>(ws + w.tiles), reinterpret_cast<int32_t*>(ws + w.num_tiles),
                            nullptr, 0, nullptr, stream));
-    if (T > 0) NVFP4_TRY(launch_sort_rows(dtype, x, slot_row, T, H, (int)topk, rows, stream));
+    NVFP4_TRY(launch_place_rows(dtype, x, slot_row, T, H, (int)topk, rows, stream));
     return NVFP4_OK;
 }
 

@@ -23,22 +23,27 @@ __device__ __forceinline__ T from_f32(float v) {
 }
 
 // The first n elements (at most a piece) at p, which is aligned to its element
-// alone; the others are zero.
-template <typename T>
+// alone; the others are zero. STREAM: read or written once, past the caches.
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ Vec<T> load_vec(const T* __restrict__ p, int n) {
+    struct __attribute__((packed, aligned(sizeof(T)))) Raw { u32x4 v; };
     Vec<T> r;
     if (n >= kVec<T>) {
-        __builtin_memcpy(&r, p, 16);
+        const Raw* q = reinterpret_cast<const Raw*>(p);
+        r = __builtin_bit_cast(Vec<T>, STREAM ? __builtin_nontemporal_load(&q->v) : q->v);
     } else {
 #pragma unroll
         for (int i = 0; i < kVec<T>; ++i) r.v[i] = i < n ? p[i] : (T)0.0f;
     }
     return r;
 }
-template <typename T>
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ void store_vec(T* __restrict__ p, const Vec<T>& r, int n) {
+    struct __attribute__((packed, aligned(sizeof(T)))) Raw { u32x4 v; };
     if (n >= kVec<T>) {
-        __builtin_memcpy(p, &r, 16);
+        Raw* q = reinterpret_cast<Raw*>(p);
+        if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, r), &q->v);
+        else q->v = __builtin_bit_cast(u32x4, r);
     } else {
 #pragma unroll
         for (int i = 0; i < kVec<T>; ++i)

@@ -1,0 +1,47 @@
+"""The token sort's ranks in each of the ways that it counts them (small batches, chunk
+counts, the layer's routing kernels) and at their borders, and tokens with many
+choices: integers exactly."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+# (T, k, E): 6144 and 16384 slots are the last of small batches, 12288 chunk counts
+# the last that are added up; chunks of 256 slots that end inside a token
+@pytest.mark.parametrize("T,k,E", [(1, 512, 40), (2, 300, 512), (9, 512, 3), (767, 8, 96), (768, 8, 96), (769, 8, 96),
+                                   (2048, 8, 97), (2049, 8, 97), (1366, 9, 48), (8192, 8, 48), (8193, 8, 48),
+                                   (50, 256, 16), (30, 257, 16), (100, 100, 1), (4001, 7, 11), (70001, 3, 2),
+                                   (131072, 8, 24), (200003, 5, 512)])
+def test_ranks(nv, T, k, E):
+    import torch
+    g = np.random.RandomState(T + k + E)
+    ids = g.randint(-1, E + 1, (T, k)).astype(np.int32)
+    flat = ids.reshape(-1)
+    ok = (flat >= 0) & (flat < E)
+    order = np.argsort(np.where(ok, flat, E), kind="stable")[:ok.sum()]
+    row = np.full(T * k, -1, np.int32)
+    row[order] = np.arange(len(order), dtype=np.int32)
+    x = torch.arange(T, device="cuda", dtype=torch.float32).view(T, 1)
+    rows = torch.full((T * k, 1), -5.0, device="cuda")
+    _, off, got = nv.sort_tokens(x, torch.from_numpy(ids).cuda(), E, rows=rows)
+    assert (got.cpu().numpy().reshape(-1) == row).all()
+    counts = np.bincount(flat[ok], minlength=E)
+    assert (off.cpu().numpy() == np.concatenate([[0], np.cumsum(counts)])).all()
+    want = np.full(T * k, -5.0, np.float32)
+    want[:len(order)] = order // k
+    assert (rows.cpu().numpy().reshape(-1) == want).all()
+
+
+def test_a_workspace_of_the_asked_size(nv):
+    """Nothing is written before or behind it."""
+    import torch
+    for T, k, E in ((8, 8, 48), (4096, 8, 48), (8193, 8, 48)):
+        ids = torch.randint(0, E, (T, k), dtype=torch.int32, device="cuda")
+        x = torch.randn((T, 8), device="cuda")
+        n = nv._lib.nvfp4_sort_tokens_workspace(T, E, k)
+        buf = torch.full((n + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+        a = nv.sort_tokens(x, ids, E, workspace=buf[256:256 + n])
+        assert bool((buf[:256] == 0x5A).all()) and bool((buf[256 + n:] == 0x5A).all())
+        b = nv.sort_tokens(x, ids, E)
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
