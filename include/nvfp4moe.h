@@ -550,8 +550,9 @@ typedef enum nvfp4_dtype { NVFP4_BF16 = 0, NVFP4_F16 = 1, NVFP4_F32 = 2 } nvfp4_
  *   E <= 512, topk <= 512, T <= 2^24, H <= 2^20, T * topk <= 2^30, else
  *   NVFP4_ESHAPE. Outputs overlap no input and each other. T == 0 writes offsets.
  *
- * Workspace: nvfp4_sort_tokens_workspace(T, E, topk) bytes, 256-byte aligned; 0
- * for invalid sizes.
+ * Workspace: nvfp4_sort_tokens_workspace(T, E, topk) bytes, 256-byte aligned. 0
+ * for small batches, which need none (workspace may be NULL), and for invalid
+ * sizes.
  *
  * nvfp4_sort_tokens_backward: dx[t] = sum_j d_rows[slot_row[t][j]], in the order
  * of j. d_rows (R, H), entries of slot_row outside [0, R) contribute nothing.

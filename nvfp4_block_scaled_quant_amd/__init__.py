@@ -619,22 +619,42 @@ def gated_backward(d_act, x, w13, gate_up, dx=None, dw13=None, need_dx=True, nee
 # element types of the operators that take several (enum nvfp4_dtype)
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _MATVEC_GATED, _MATVEC_ALPHA_PER_HALF = 1, 2
+_MALFORMED = (AttributeError, KeyError, TypeError, ValueError, IndexError)
+
+# The operators below run for a few microseconds on small batches, about as long as
+# checks one by one: each first asks in one expression whether all is well, and only
+# if not has the checks say what is wrong.
 
 
 def _typed(t, name, dim=None):
-    """The dtype code of a contiguous tensor on the GPU in one of _DTYPES."""
+    """A contiguous tensor on the GPU in one of _DTYPES, or what is wrong with it."""
     if isinstance(t, torch.Tensor) and t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
     _need(t, t.dtype if isinstance(t, torch.Tensor) else None, name, dim)
-    return _DTYPES[t.dtype]
 
 
-def _slots(slot_row, index):
-    """T, topk and address of a (T, topk) int32 tensor on device `index`."""
-    if not isinstance(slot_row, torch.Tensor) or slot_row.dim() != 2 or slot_row.shape[1] < 1:
-        _need(slot_row, torch.int32, "slot_row", 2)
-        raise ValueError("slot_row must be (T, topk) with topk at least 1")
-    return (*slot_row.shape, _operands(index, (slot_row, torch.int32, slot_row.shape, "slot_row"))[0])
+def _table(t, name, index):
+    """A (T, topk) int32 tensor on device `index`, or what is wrong with it."""
+    _need(t, torch.int32, name, 2, torch.device("cuda", index))
+    if t.shape[1] < 1:
+        raise ValueError(f"{name} must be (T, topk) with topk at least 1")
+
+
+def _rows_and_table(where, rows, table, rows_name, table_name):
+    """Checks of a typed (R, H) tensor and a (T, topk) int32 one beside it: the
+    type's code, the device, R, H, T, topk."""
+    try:
+        code, index = _DTYPES[rows.dtype], rows.get_device()
+        (R, H), (T, k) = rows.shape, table.shape
+        good = (index >= 0 and k > 0 and rows.is_contiguous() and table.dtype is torch.int32
+                and table.get_device() == index and table.is_contiguous())
+    except _MALFORMED:
+        good = False
+    if not good:
+        _typed(rows, rows_name, 2)
+        _table(table, table_name, rows.get_device())
+        raise ValueError(f"{where}: inconsistent arguments")
+    return code, index, R, H, T, k
 
 
 def sort_tokens(x, topk_ids, num_experts, rows=None, workspace=None):
@@ -645,40 +665,35 @@ def sort_tokens(x, topk_ids, num_experts, rows=None, workspace=None):
     and expert e has the rows from offsets[e] to offsets[e + 1]. Rows from
     offsets[num_experts] on are not written (uninitialized unless `rows` is given).
     No graph: see gated_forward."""
-    _refuse_recording("sort_tokens", x=x)
-    code = _typed(x, "x", 2)
-    index = x.get_device()
+    if getattr(x, "requires_grad", False):
+        _refuse_recording("sort_tokens", x=x)
+    code, index, T, H, T_ids, k = _rows_and_table("sort_tokens", x, topk_ids, "x", "topk_ids")
+    if T_ids != T:
+        raise ValueError(f"topk_ids must have shape {(T, k)}, got {tuple(topk_ids.shape)}")
     if index != torch._C._cuda_getDevice():                 # the library launches on the current device
         with torch.cuda.device(index):
             return sort_tokens(x, topk_ids, num_experts, rows, workspace)
-    T, H = x.shape
-    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2 or topk_ids.shape[1] < 1:
-        _need(topk_ids, torch.int32, "topk_ids", 2)
-        raise ValueError("topk_ids must be (T, topk) with topk at least 1")
-    k = topk_ids.shape[1]
-    ids = _operands(index, (topk_ids, torch.int32, (T, k), "topk_ids"))[0]
     rows = _result(rows, x, (T * k, H), "rows", index)
-    offsets, slot_row = topk_ids.new_empty(num_experts + 1), topk_ids.new_empty((T, k))
-    ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.nvfp4_sort_tokens_workspace(T, num_experts, k), index)
-    _check(_lib.nvfp4_sort_tokens(x.data_ptr(), code, ids, T, H, num_experts, k, rows.data_ptr(), offsets.data_ptr(),
-                                  slot_row.data_ptr(), ws_ptr, ws_bytes, torch._C._cuda_getCurrentRawStream(index)),
-           "nvfp4_sort_tokens")
+    offsets, slot_row = topk_ids.new_empty(max(num_experts, 0) + 1), topk_ids.new_empty((T, k))
+    nbytes = _lib.nvfp4_sort_tokens_workspace(T, num_experts, k)
+    ws, ws_ptr, ws_bytes = (None, None, 0) if nbytes == 0 and workspace is None else _scratch(workspace, nbytes, index)
+    _check(_lib.nvfp4_sort_tokens(x.data_ptr(), code, topk_ids.data_ptr(), T, H, num_experts, k, rows.data_ptr(),
+                                  offsets.data_ptr(), slot_row.data_ptr(), ws_ptr, ws_bytes,
+                                  torch._C._cuda_getCurrentRawStream(index)), "nvfp4_sort_tokens")
     return rows, offsets, slot_row
 
 
 def sort_tokens_backward(d_rows, slot_row, dx=None):
     """Gradient of sort_tokens: dx[t] = sum_j d_rows[slot_row[t, j]] over the slots
     that have a row; d_rows (R, H) -> dx (T, H) of its type. No graph of its own."""
-    _refuse_recording("sort_tokens_backward", d_rows=d_rows)
-    code = _typed(d_rows, "d_rows", 2)
-    index = d_rows.get_device()
+    if getattr(d_rows, "requires_grad", False):
+        _refuse_recording("sort_tokens_backward", d_rows=d_rows)
+    code, index, R, H, T, k = _rows_and_table("sort_tokens_backward", d_rows, slot_row, "d_rows", "slot_row")
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return sort_tokens_backward(d_rows, slot_row, dx)
-    R, H = d_rows.shape
-    T, k, at = _slots(slot_row, index)
     dx = _result(dx, d_rows, (T, H), "dx", index)
-    _check(_lib.nvfp4_sort_tokens_backward(d_rows.data_ptr(), code, at, T, H, k, R, dx.data_ptr(),
+    _check(_lib.nvfp4_sort_tokens_backward(d_rows.data_ptr(), code, slot_row.data_ptr(), T, H, k, R, dx.data_ptr(),
                                            torch._C._cuda_getCurrentRawStream(index)), "nvfp4_sort_tokens_backward")
     return dx
 
@@ -688,17 +703,15 @@ def unsort_tokens(rows, slot_row, topk_weights, y=None):
     rows[slot_row[t, j]] over the slots that have a row, float32 sums, rounded
     once; rows (R, H), topk_weights float32 (T, topk) -> y (T, H) of rows' type.
     No graph: see gated_forward."""
-    _refuse_recording("unsort_tokens", rows=rows, topk_weights=topk_weights)
-    code = _typed(rows, "rows", 2)
-    index = rows.get_device()
+    if getattr(rows, "requires_grad", False) or getattr(topk_weights, "requires_grad", False):
+        _refuse_recording("unsort_tokens", rows=rows, topk_weights=topk_weights)
+    code, index, R, H, T, k = _rows_and_table("unsort_tokens", rows, slot_row, "rows", "slot_row")
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return unsort_tokens(rows, slot_row, topk_weights, y)
-    R, H = rows.shape
-    T, k, at = _slots(slot_row, index)
-    w = _operands(index, (topk_weights, torch.float32, (T, k), "topk_weights"))[0]
+    w, = _operands(index, (topk_weights, torch.float32, slot_row.shape, "topk_weights"))
     y = _result(y, rows, (T, H), "y", index)
-    _check(_lib.nvfp4_unsort_tokens(rows.data_ptr(), code, at, w, T, H, k, R, y.data_ptr(),
+    _check(_lib.nvfp4_unsort_tokens(rows.data_ptr(), code, slot_row.data_ptr(), w, T, H, k, R, y.data_ptr(),
                                     torch._C._cuda_getCurrentRawStream(index)), "nvfp4_unsort_tokens")
     return y
 
@@ -710,26 +723,25 @@ def unsort_tokens_backward(dy, rows, slot_row, topk_weights, d_rows=None, d_weig
     rows that slot_row does not name are not written (uninitialized unless d_rows
     is given). need_d_rows / need_d_weights = False: None in that place. No graph
     of its own."""
-    _refuse_recording("unsort_tokens_backward", dy=dy, rows=rows, topk_weights=topk_weights)
-    code = _typed(dy, "dy", 2)
-    index = dy.get_device()
+    if (getattr(dy, "requires_grad", False) or getattr(rows, "requires_grad", False)
+            or getattr(topk_weights, "requires_grad", False)):
+        _refuse_recording("unsort_tokens_backward", dy=dy, rows=rows, topk_weights=topk_weights)
+    code, index, R, H, T, k = _rows_and_table("unsort_tokens_backward", rows, slot_row, "rows", "slot_row")
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return unsort_tokens_backward(dy, rows, slot_row, topk_weights, d_rows, d_weights, need_d_rows,
                                           need_d_weights)
-    T, k, at = _slots(slot_row, index)
-    _need(rows, dy.dtype, "rows", 2, dy.device)
-    R, H = rows.shape
-    p_dy, w = _operands(index, (dy, dy.dtype, (T, H), "dy"), (topk_weights, torch.float32, (T, k), "topk_weights"))
+    p_dy, w = _operands(index, (dy, rows.dtype, (T, H), "dy"),
+                        (topk_weights, torch.float32, slot_row.shape, "topk_weights"))
     if not (need_d_rows or need_d_weights):
         raise ValueError("unsort_tokens_backward: nothing to compute")
     if (d_rows is not None and not need_d_rows) or (d_weights is not None and not need_d_weights):
         raise ValueError("unsort_tokens_backward: an output is given for a gradient that is not computed")
     if need_d_rows:
-        d_rows = _result(d_rows, dy, (R, H), "d_rows", index)
+        d_rows = _result(d_rows, rows, rows.shape, "d_rows", index)
     if need_d_weights:
-        d_weights = _result(d_weights, topk_weights, (T, k), "d_weights", index)
-    _check(_lib.nvfp4_unsort_tokens_backward(p_dy, rows.data_ptr(), code, at, w, T, H, k, R,
+        d_weights = _result(d_weights, topk_weights, slot_row.shape, "d_weights", index)
+    _check(_lib.nvfp4_unsort_tokens_backward(p_dy, rows.data_ptr(), code, slot_row.data_ptr(), w, T, H, k, R,
                                              d_rows.data_ptr() if need_d_rows else None,
                                              d_weights.data_ptr() if need_d_weights else None,
                                              torch._C._cuda_getCurrentRawStream(index)),
@@ -741,17 +753,30 @@ def route_topk_backward(d_weights, topk_ids, topk_weights, num_experts, d_logits
     """Gradient of route_topk's weights: d_weights float32 (T, topk), the ids and
     weights that route_topk gave -> d_logits float32 (T, num_experts), zero for
     experts that were not chosen. No graph of its own."""
-    _refuse_recording("route_topk_backward", d_weights=d_weights, topk_weights=topk_weights)
-    _need(d_weights, torch.float32, "d_weights", 2)
-    index = d_weights.get_device()
+    if getattr(d_weights, "requires_grad", False) or getattr(topk_weights, "requires_grad", False):
+        _refuse_recording("route_topk_backward", d_weights=d_weights, topk_weights=topk_weights)
+    f32 = torch.float32
+    try:
+        index, shape = d_weights.get_device(), d_weights.shape
+        T, k = shape
+        good = (index >= 0 and d_weights.dtype is f32 and d_weights.is_contiguous()
+                and topk_ids.dtype is torch.int32 and topk_ids.shape == shape and topk_ids.get_device() == index
+                and topk_ids.is_contiguous()
+                and topk_weights.dtype is f32 and topk_weights.shape == shape
+                and topk_weights.get_device() == index and topk_weights.is_contiguous())
+    except _MALFORMED:
+        good = False
+    if not good:
+        _need(d_weights, f32, "d_weights", 2)
+        _operands(d_weights.get_device(), (topk_ids, torch.int32, d_weights.shape, "topk_ids"),
+                  (topk_weights, f32, d_weights.shape, "topk_weights"))
+        raise ValueError("route_topk_backward: inconsistent arguments")
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return route_topk_backward(d_weights, topk_ids, topk_weights, num_experts, d_logits)
-    T, k = d_weights.shape
-    ids, w = _operands(index, (topk_ids, torch.int32, (T, k), "topk_ids"),
-                       (topk_weights, torch.float32, (T, k), "topk_weights"))
-    d_logits = _result(d_logits, d_weights, (T, num_experts), "d_logits", index)
-    _check(_lib.nvfp4_route_topk_backward(d_weights.data_ptr(), ids, w, T, num_experts, k, d_logits.data_ptr(),
+    d_logits = _result(d_logits, d_weights, (T, max(num_experts, 0)), "d_logits", index)
+    _check(_lib.nvfp4_route_topk_backward(d_weights.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), T,
+                                          num_experts, k, d_logits.data_ptr(),
                                           torch._C._cuda_getCurrentRawStream(index)), "nvfp4_route_topk_backward")
     return d_logits
 
@@ -765,59 +790,76 @@ def matvec(x, bq, bsf, b_alpha, offsets=None, gated=False, out=None):
     (uninitialized unless out is given). gated: N columns [gate | up], out (M,
     N / 2) = silu(gate) * up of the float32 sums; b_alpha may be per half, (2,) or
     (E, 2). K % 16 == 0. No graph: see gated_forward."""
-    if torch.is_grad_enabled():
+    if getattr(x, "requires_grad", False) or getattr(b_alpha, "requires_grad", False):
         _refuse_recording("matvec", x=x, b_alpha=b_alpha)
-    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError("x must be a bfloat16 or float16 CUDA (HIP) tensor")
-    _need(x, x.dtype, "x", 2)
-    index = x.get_device()
+    u8 = torch.uint8
+    try:
+        code, index = _DTYPES[x.dtype], x.get_device()
+        M, K = x.shape
+        steps = (K + 127) // 128
+        if offsets is None:
+            (blocks, *rest), E, lead = bq.shape, 1, ()
+            good = True
+        else:
+            E, blocks, *rest = bq.shape
+            lead = (E,)
+            good = (offsets.dtype is torch.int32 and offsets.shape == (E + 1,) and offsets.get_device() == index
+                    and offsets.is_contiguous())
+        n_alpha = b_alpha.numel()
+        # packed_shapes
+        good = (good and code < 2 and index >= 0 and x.is_contiguous() and K > 0 and K % 16 == 0
+                and bq.dtype is u8 and rest == [2 * steps, 16, 32] and bq.get_device() == index and bq.is_contiguous()
+                and bsf.dtype is u8 and bsf.shape == (*lead, blocks, (steps + 3) // 4, 16, 32)
+                and bsf.get_device() == index and bsf.is_contiguous()
+                and b_alpha.dtype is torch.float32 and b_alpha.get_device() == index and b_alpha.is_contiguous()
+                and (n_alpha == E or (gated and b_alpha.shape == (*lead, 2)))
+                and E > 0 and blocks > 0 and not (gated and blocks % 2))
+    except _MALFORMED:
+        good = False
+    if not good:
+        if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("x must be a bfloat16 or float16 CUDA (HIP) tensor")
+        _need(x, x.dtype, "x", 2)
+        index, (M, K) = x.get_device(), x.shape
+        _need(bq, u8, "bq", 4 if offsets is None else 5, x.device)
+        if K % 16 or K == 0:
+            raise ValueError("matvec: K must be a positive multiple of 16")
+        lead = () if offsets is None else (bq.shape[0],)
+        E, blocks, steps = bq.shape[0] if lead else 1, bq.shape[len(lead)], (K + 127) // 128
+        if E == 0 or blocks == 0 or (gated and blocks % 2):
+            raise ValueError("matvec: the weights must have columns (gated: a multiple of 32)")
+        _operands(index, (bq, u8, lead + (blocks, 2 * steps, 16, 32), "bq"),
+                  (bsf, u8, lead + (blocks, (steps + 3) // 4, 16, 32), "bsf"))
+        _scalar(b_alpha, "b_alpha", index)
+        if offsets is not None:
+            _operands(index, (offsets, torch.int32, (E + 1,), "offsets"))
+        raise ValueError(f"matvec: b_alpha must hold one float32 per matrix (gated: or two), got {tuple(b_alpha.shape)}")
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return matvec(x, bq, bsf, b_alpha, offsets, gated, out)
-    M, K = x.shape
-    _need(bq, torch.uint8, "bq", 4 if offsets is None else 5, x.device)
-    if K % 16 or K == 0:
-        raise ValueError("matvec: K must be a positive multiple of 16")
-    lead = () if offsets is None else (bq.shape[0],)
-    E, blocks, steps = bq.shape[0] if lead else 1, bq.shape[len(lead)], (K + 127) // 128
-    N = 16 * blocks
-    if E == 0 or N == 0 or (gated and blocks % 2):
-        raise ValueError("matvec: the weights must have columns (gated: a multiple of 32)")
-    p_q, p_sf = _operands(index, (bq, torch.uint8, lead + (blocks, 2 * steps, 16, 32), "bq"),     # packed_shapes
-                          (bsf, torch.uint8, lead + (blocks, (steps + 3) // 4, 16, 32), "bsf"))
-    alpha = _scalar(b_alpha, "b_alpha", index)
     flags = _MATVEC_GATED if gated else 0
-    if b_alpha.numel() != E:
-        if not gated or b_alpha.shape != lead + (2,):
-            raise ValueError(f"matvec: b_alpha must hold one float32 per matrix (gated: or two), got "
-                             f"{tuple(b_alpha.shape)}")
+    if n_alpha != E:
         flags |= _MATVEC_ALPHA_PER_HALF
-    p_off = None if offsets is None else _operands(index, (offsets, torch.int32, (E + 1,), "offsets"))[0]
-    out = _result(out, x, (M, N // 2 if gated else N), "out", index)
-    _check(_lib.nvfp4_matvec(x.data_ptr(), _DTYPES[x.dtype], p_q, p_sf, alpha, p_off, M, N, K, E, flags,
+    out = _result(out, x, (M, 8 * blocks if gated else 16 * blocks), "out", index)
+    _check(_lib.nvfp4_matvec(x.data_ptr(), code, bq.data_ptr(), bsf.data_ptr(), b_alpha.data_ptr(),
+                             None if offsets is None else offsets.data_ptr(), M, 16 * blocks, K, E, flags,
                              out.data_ptr(), torch._C._cuda_getCurrentRawStream(index)), "nvfp4_matvec")
     return out
 
 
-def _dropout(where, x, p, rng, residual, y, name, out_name):
-    _refuse_recording(where, **{name: x, "residual": residual})
-    code = _typed(x, name)
-    index = x.get_device()
-    if index != torch._C._cuda_getDevice():
-        with torch.cuda.device(index):
-            return _dropout(where, x, p, rng, residual, y, name, out_name)
-    state = _operands(index, (rng, torch.int64, (2,), "rng"))[0]
-    if not 0.0 <= p <= 1.0:
-        raise ValueError(f"{where}: p must be from 0 to 1, got {p}")
-    y = _result(y, x, x.shape, out_name, index)
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if where == "dropout_backward":
-        _check(_lib.nvfp4_dropout_backward(x.data_ptr(), code, x.numel(), p, state, y.data_ptr(), stream),
-               "nvfp4_dropout_backward")
-        return y
-    r = None if residual is None else _operands(index, (residual, x.dtype, x.shape, "residual"))[0]
-    _check(_lib.nvfp4_dropout(x.data_ptr(), r, code, x.numel(), p, state, y.data_ptr(), stream), "nvfp4_dropout")
-    return y
+def _dropout_args(x, p, rng, name):
+    """The type's code and device of a dropout's x and rng, or what is wrong."""
+    try:
+        code, index = _DTYPES[x.dtype], x.get_device()
+        good = (index >= 0 and x.is_contiguous() and rng.dtype is torch.int64 and rng.shape == (2,)
+                and rng.get_device() == index and rng.is_contiguous() and 0.0 <= p <= 1.0)
+    except _MALFORMED:
+        good = False
+    if not good:
+        _typed(x, name)
+        _operands(x.get_device(), (rng, torch.int64, (2,), "rng"))
+        raise ValueError(f"dropout: p must be from 0 to 1, got {p}")
+    return code, index
 
 
 def dropout(x, p, rng, residual=None, y=None):
@@ -828,13 +870,32 @@ def dropout(x, p, rng, residual=None, y=None):
     dropout_backward. Move the offset on by (x.numel() + 3) // 4 for the next call;
     rng is read on the GPU, so a captured call follows its changes. y may be x or
     residual. No graph: see gated_forward."""
-    return _dropout("dropout", x, p, rng, residual, y, "x", "y")
+    if getattr(x, "requires_grad", False) or getattr(residual, "requires_grad", False):
+        _refuse_recording("dropout", x=x, residual=residual)
+    code, index = _dropout_args(x, p, rng, "x")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return dropout(x, p, rng, residual, y)
+    r = None if residual is None else _operands(index, (residual, x.dtype, x.shape, "residual"))[0]
+    y = _result(y, x, x.shape, "y", index)
+    _check(_lib.nvfp4_dropout(x.data_ptr(), r, code, x.numel(), p, rng.data_ptr(), y.data_ptr(),
+                              torch._C._cuda_getCurrentRawStream(index)), "nvfp4_dropout")
+    return y
 
 
 def dropout_backward(dy, p, rng, dx=None):
     """Gradient of dropout with the forward's p and rng: dx = dy / (1 - p) where
     the element was kept, else 0 (residual's gradient is dy)."""
-    return _dropout("dropout_backward", dy, p, rng, None, dx, "dy", "dx")
+    if getattr(dy, "requires_grad", False):
+        _refuse_recording("dropout_backward", dy=dy)
+    code, index = _dropout_args(dy, p, rng, "dy")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return dropout_backward(dy, p, rng, dx)
+    dx = _result(dx, dy, dy.shape, "dx", index)
+    _check(_lib.nvfp4_dropout_backward(dy.data_ptr(), code, dy.numel(), p, rng.data_ptr(), dx.data_ptr(),
+                                       torch._C._cuda_getCurrentRawStream(index)), "nvfp4_dropout_backward")
+    return dx
 
 
 class _Hip:

@@ -807,7 +807,7 @@ SortLayout sort_layout(int64_t T, int64_t E, int64_t topk) {
     SortLayout w = {};
     const int64_t S = T * topk;
     if (sort_small(S, E) || sort_by_counts(S, E, topk)) {
-        w.total = sort_small(S, E) ? kAlign : align_up((size_t)sort_counts_bytes(S, E));
+        w.total = sort_small(S, E) ? 0 : align_up((size_t)sort_counts_bytes(S, E));
         return w;
     }
     w.sorted = align_up((size_t)E * 4);
@@ -835,8 +835,8 @@ int nvfp4_sort_tokens(const void* x, int dtype, const int32_t* topk_ids, int64_t
     if (!aligned(x, size) || !aligned(rows, size) || !aligned(topk_ids, 4) || !aligned(offsets, 4) ||
         !aligned(slot_row, 4))
         return NVFP4_EINVAL;
-    if (!workspace || !aligned(workspace, kAlign) || workspace_bytes < nvfp4_sort_tokens_workspace(T, E, topk))
-        return NVFP4_EWORKSPACE;
+    const size_t need = nvfp4_sort_tokens_workspace(T, E, topk);
+    if (need > 0 && (!workspace || !aligned(workspace, kAlign) || workspace_bytes < need)) return NVFP4_EWORKSPACE;
     int dv = check_device();
     if (dv) return dv;
     if (T == 0) {

@@ -342,8 +342,8 @@ def test_refusals(nv):
            (ValueError, lambda: nv.sort_tokens(x, ids, 3, rows=rows[:7])),
            (nv.Nvfp4Error, lambda: nv.sort_tokens(x, ids, 0)),
            (nv.Nvfp4Error, lambda: nv.sort_tokens(x, ids, 513)),
-           (nv.Nvfp4Error, lambda: nv.sort_tokens(x, ids, 3, workspace=torch.empty(8, dtype=torch.uint8,
-                                                                                   device="cuda"))),
+           (nv.Nvfp4Error, lambda: nv.sort_tokens(x.repeat(4096, 1), ids.repeat(4096, 1), 3,
+                                                  workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))),
            (ValueError, lambda: nv.sort_tokens_backward(rows, row[:, :0])),
            (TypeError, lambda: nv.sort_tokens_backward(rows, row.float())),
            (ValueError, lambda: nv.sort_tokens_backward(rows, row, dx=x[:2])),

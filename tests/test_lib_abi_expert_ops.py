@@ -39,11 +39,14 @@ def test_sort_tokens_argument_errors(lib):
         assert call(**{name: 0}) == 1 and call(**{name: A16 + 1}) == 1, name
     assert call(T=0, x=0, ids=0, rows=0, row=0, off=0) == 1
     assert call(x=A16 + 2, dtype=2) == 1 and call(rows=A16 + 2, dtype=2) == 1
-    need = ws(4, 5, 2)
-    assert need > 0 and call(nbytes=need - 1) == 3 and call(wsp=0) == 3 and call(wsp=A16 + 64) == 3
-    assert call(x=A16 + 2, rows=A16 + 6, nbytes=need - 1) == 3           # any element's alignment
-    assert ws(4, 513, 2) == 0 and ws(-1, 5, 2) == 0 and ws(4, 5, 0) == 0 and ws(1 << 24, 5, 512) == 0
-    assert ws(0, 5, 2) > 0
+    # small batches need no workspace, larger ones and invalid sizes see to it
+    assert ws(0, 5, 2) == 0 and ws(4, 5, 2) == 0 and ws(4, 513, 2) == 0 and ws(-1, 5, 2) == 0
+    for T, E, k in ((4096, 48, 8), (1 << 16, 256, 8)):
+        need = ws(T, E, k)
+        assert need > 0 and need % 256 == 0
+        big = dict(T=T, E=E, k=k)
+        assert call(nbytes=need - 1, **big) == 3 and call(wsp=0, **big) == 3 and call(wsp=A16 + 64, **big) == 3
+        assert call(x=A16 + 2, rows=A16 + 6, nbytes=need - 1, **big) == 3           # any element's alignment
 
 
 def test_gather_argument_errors(lib):
