@@ -798,16 +798,18 @@ bool tokens_shape_ok(int64_t T, int64_t H, int64_t topk, int64_t R) {
            R <= kMaxSlots;
 }
 
-// The chunks' counts, or (large batches of many experts) what the layer's routing
-// kernels write beside offsets and slot_row.
+// The chunks' counts and the slots' ranks (in `sorted`), or (large batches of many
+// experts) what the layer's routing kernels write beside offsets and slot_row.
 struct SortLayout {
     size_t counts, sorted, tiles, num_tiles, wg_counts, total;
 };
 SortLayout sort_layout(int64_t T, int64_t E, int64_t topk) {
     SortLayout w = {};
     const int64_t S = T * topk;
-    if (sort_small(S, E) || sort_by_counts(S, E, topk)) {
-        w.total = sort_small(S, E) ? 0 : align_up((size_t)sort_counts_bytes(S, E));
+    if (sort_small(S, E)) return w;
+    if (sort_by_counts(S, E, topk)) {
+        w.sorted = align_up((size_t)sort_counts_bytes(S, E));
+        w.total = w.sorted + align_up((size_t)S * 4);
         return w;
     }
     w.sorted = align_up((size_t)E * 4);
@@ -857,7 +859,8 @@ int nvfp4_sort_tokens(const void* x, int dtype, const int32_t* topk_ids, int64_t
         p.rows = rows;
         p.offsets = offsets;
         p.slot_row = slot_row;
-        NVFP4_TRY(launch_sort_tokens(dtype, p, reinterpret_cast<int32_t*>(ws), stream));
+        NVFP4_TRY(launch_sort_tokens(dtype, p, reinterpret_cast<int32_t*>(ws), reinterpret_cast<int32_t*>(ws + w.sorted),
+                                     stream));
         return NVFP4_OK;
     }
     int32_t* wg_counts = reinterpret_cast<int32_t*>(ws + w.wg_counts);
@@ -945,7 +948,8 @@ int nvfp4_matvec(const void* x, int dtype, const uint8_t* bq, const uint8_t* bsf
     if (halves && !gated) return NVFP4_EINVAL;
     if (K % 16 || N % (gated ? 32 : 16) || E > kMaxExperts || (!offsets && E != 1)) return NVFP4_ESHAPE;
     if (K > (int64_t)1 << 20 || N * pitch_q(K) >= 0x7FFFFFFF || M > (int64_t)1 << 24) return NVFP4_ESHAPE;
-    if (matvec_tiles(M, offsets ? E : 0) * (N / 16) >= (int64_t)1 << 31) return NVFP4_ESHAPE;
+    // (a launch has fewer than 2^32 threads, a work-group up to 512)
+    if (matvec_tiles(M, offsets ? E : 0) * (N / 16) >= (int64_t)1 << 23) return NVFP4_ESHAPE;
     if (M == 0) return NVFP4_OK;
     if (!x || !bq || !bsf || !b_alpha || !out) return NVFP4_EINVAL;
     if (!aligned(x, 16) || !aligned(bq, 16) || !aligned(bsf, 8) || !aligned(b_alpha, 4) || !aligned(offsets, 4) ||

@@ -75,7 +75,7 @@ hipError_t launch_dropout(int dtype, const void* x, const void* residual, int64_
     return with_type(dtype, [&](auto zero) {
         using V = decltype(zero);
         const int64_t nblk = (n + NT * kVec<V> - 1) / (NT * kVec<V>);
-        const int64_t grid = nblk < (1 << 30) ? nblk : 1 << 30;
+        const int64_t grid = nblk < (1 << 22) ? nblk : 1 << 22;
         dropout_kernel<V><<<(unsigned)grid, NT, 0, s>>>(static_cast<const V*>(x), static_cast<const V*>(residual), n,
                                                         least, none, scale, rng, static_cast<V*>(y));
     });

@@ -383,6 +383,7 @@ struct SortParams {
     int32_t* slot_row;         // (T, k)
     // set by launch_sort_tokens
     const int32_t* counts;     // (chunks, E)
+    const int32_t* ranks;      // (T, k)
     int chunks, C, TW, parts;
 };
 // How the slots are ranked. Small batches: every work-group counts all ids by itself.
@@ -396,8 +397,9 @@ inline bool sort_by_counts(int64_t S, int64_t E, int64_t k) {
     return !sort_small(S, E) && k <= 256 && (S + 255) / 256 * E <= 12288;
 }
 inline int64_t sort_counts_bytes(int64_t S, int64_t E) { return (S + 255) / 256 * E * 4; }
-// sort_small or sort_by_counts (counts: the chunks' counts)
-hipError_t launch_sort_tokens(int dtype, SortParams p, int32_t* counts, hipStream_t s);
+// sort_small, or sort_by_counts (which takes memory for the chunks' counts, and for
+// the slots' ranks: S values)
+hipError_t launch_sort_tokens(int dtype, SortParams p, int32_t* counts, int32_t* ranks, hipStream_t s);
 // rows[slot_row[t][j]] = x[t] for entries from 0 on
 hipError_t launch_place_rows(int dtype, const void* x, const int32_t* slot_row, int64_t T, int64_t H, int k, void* rows,
                              hipStream_t s);

@@ -59,10 +59,10 @@ __global__ __launch_bounds__(NT) void place_rows_kernel(const T* __restrict__ x,
     }
 }
 
-// Ranks of a chunk of NT slots: slot_row[s] = the slots of the chunk before s with its
-// expert (-1: no expert's), counts[chunk][e] = all that have expert e.
+// Ranks of a chunk of NT slots: ranks[s] = the slots of the chunk before s with its
+// expert, counts[chunk][e] = all that have expert e.
 __global__ __launch_bounds__(NT) void sort_count_kernel(const int32_t* __restrict__ ids, int64_t S, int E, int nbits,
-                                                        int32_t* __restrict__ slot_row, int32_t* __restrict__ counts) {
+                                                        int32_t* __restrict__ ranks, int32_t* __restrict__ counts) {
     extern __shared__ int32_t wave_count[];               // [NT / 64][E]
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t s = (int64_t)blockIdx.x * NT + tid;
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(NT) void sort_count_kernel(const int32_t* __restric
     __syncthreads();
     for (int v = 0; v < wave; ++v)
         if (valid) rank += wave_count[v * E + e];
-    if (s < S) slot_row[s] = valid ? rank : -1;
+    if (s < S) ranks[s] = rank;
     for (int i = tid; i < E; i += NT) {
         int sum = 0;
 #pragma unroll
@@ -159,13 +159,13 @@ __global__ __launch_bounds__(NT) void sort_rows_kernel(SortParams p) {
             if (SMALL) {
                 for (int u = 0; u < i; ++u) r += id[u] == e;
             } else {
-                r += p.slot_row[s0 + i];
+                r += p.ranks[s0 + i];
                 if ((s0 + i) / NT > g0) r += p.counts[g0 * E + e];
             }
         }
         row[i] = r;
     }
-    __syncthreads();                                      // (every rank of its slots has been read)
+    __syncthreads();
     if (part == 0)
         for (int i = tid; i < slots; i += NT) p.slot_row[s0 + i] = row[i];
     if (blockIdx.x == 0)
@@ -261,61 +261,63 @@ __device__ __forceinline__ float wave_sum8(const float (&d)[8], int lane) {
 template <typename T, bool STREAM, int TB>
 __global__ __launch_bounds__(TB) void unsort_backward_kernel(const T* __restrict__ dy, const T* __restrict__ rows,
                                                              const int32_t* __restrict__ slot_row,
-                                                             const float* __restrict__ w, int64_t H, int k, int64_t R,
-                                                             int C, T* __restrict__ d_rows, float* __restrict__ dw) {
+                                                             const float* __restrict__ w, int64_t T_, int64_t H, int k,
+                                                             int64_t R, int C, T* __restrict__ d_rows,
+                                                             float* __restrict__ dw) {
     constexpr int V = kVec<T>, J = 8;                     // choices at a time
     __shared__ float red[TB / 64][J];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t t = blockIdx.x;
-    for (int j0 = 0; j0 < k; j0 += J) {
-        int32_t row[J];
-        float wj[J], dot[J];
+    for (int64_t t = blockIdx.x; t < T_; t += gridDim.x) {
+        for (int j0 = 0; j0 < k; j0 += J) {
+            int32_t row[J];
+            float wj[J], dot[J];
 #pragma unroll
-        for (int u = 0; u < J; ++u) {
-            const int32_t r = j0 + u < k ? __builtin_amdgcn_readfirstlane(slot_row[t * k + j0 + u]) : -1;
-            row[u] = r < R ? r : -1;
-            wj[u] = d_rows && j0 + u < k ? w[t * k + j0 + u] : 0.0f;
-            dot[u] = 0.0f;
-        }
-        for (int c = tid; c < C; c += TB) {
-            const int n = (int)min((int64_t)V, H - (int64_t)c * V);
-            const Vec<T> g = load_vec(dy + t * H + (int64_t)c * V, n);
-            Vec<T> v[J];
-            if (dw) {
-#pragma unroll
-                for (int u = 0; u < J; ++u)
-                    if (row[u] >= 0) v[u] = load_vec<T, STREAM>(rows + (int64_t)row[u] * H + (int64_t)c * V, n);
+            for (int u = 0; u < J; ++u) {
+                const int32_t r = j0 + u < k ? __builtin_amdgcn_readfirstlane(slot_row[t * k + j0 + u]) : -1;
+                row[u] = r < R ? r : -1;
+                wj[u] = d_rows && j0 + u < k ? w[t * k + j0 + u] : 0.0f;
+                dot[u] = 0.0f;
             }
-            if (d_rows) {
+            for (int c = tid; c < C; c += TB) {
+                const int n = (int)min((int64_t)V, H - (int64_t)c * V);
+                const Vec<T> g = load_vec(dy + t * H + (int64_t)c * V, n);
+                Vec<T> v[J];
+                if (dw) {
 #pragma unroll
-                for (int u = 0; u < J; ++u) {
-                    if (row[u] < 0) continue;
-                    Vec<T> o;
+                    for (int u = 0; u < J; ++u)
+                        if (row[u] >= 0) v[u] = load_vec<T, STREAM>(rows + (int64_t)row[u] * H + (int64_t)c * V, n);
+                }
+                if (d_rows) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o.v[i] = from_f32<T>(wj[u] * to_f32(g.v[i]));
-                    store_vec<T, STREAM>(d_rows + (int64_t)row[u] * H + (int64_t)c * V, o, n);
+                    for (int u = 0; u < J; ++u) {
+                        if (row[u] < 0) continue;
+                        Vec<T> o;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) o.v[i] = from_f32<T>(wj[u] * to_f32(g.v[i]));
+                        store_vec<T, STREAM>(d_rows + (int64_t)row[u] * H + (int64_t)c * V, o, n);
+                    }
+                }
+                if (dw) {
+#pragma unroll
+                    for (int u = 0; u < J; ++u) {
+                        if (row[u] < 0) continue;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) dot[u] = __builtin_fmaf(to_f32(g.v[i]), to_f32(v[u].v[i]), dot[u]);
+                    }
                 }
             }
             if (dw) {
+                const float mine = wave_sum8(dot, lane);
+                if ((lane & 7) == 0) red[wave][lane >> 3] = mine;
+                __syncthreads();
+                if (tid < J && j0 + tid < k) {
+                    float s = red[0][tid];
 #pragma unroll
-                for (int u = 0; u < J; ++u) {
-                    if (row[u] < 0) continue;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) dot[u] = __builtin_fmaf(to_f32(g.v[i]), to_f32(v[u].v[i]), dot[u]);
+                    for (int v = 1; v < TB / 64; ++v) s += red[v][tid];
+                    dw[t * k + j0 + tid] = s;
                 }
+                __syncthreads();
             }
-        }
-        if (dw) {
-            const float mine = wave_sum8(dot, lane);
-            if ((lane & 7) == 0) red[wave][lane >> 3] = mine;
-            __syncthreads();
-            if (tid < J && j0 + tid < k) {
-                float s = red[0][tid];
-#pragma unroll
-                for (int v = 1; v < TB / 64; ++v) s += red[v][tid];
-                dw[t * k + j0 + tid] = s;
-            }
-            __syncthreads();
         }
     }
 }
@@ -365,7 +367,7 @@ __global__ __launch_bounds__(NT) void route_topk_backward_kernel(const float* __
     }
 }
 
-constexpr int64_t kMaxGrid = (int64_t)1 << 30;
+constexpr int64_t kMaxGrid = (int64_t)1 << 22;             // work-groups (a launch has fewer than 2^32 threads)
 
 template <typename T>
 struct Pieces {
@@ -406,16 +408,17 @@ void with_flag(bool on, F&& f) {
 
 }  // namespace
 
-hipError_t launch_sort_tokens(int dtype, SortParams p, int32_t* counts, hipStream_t s) {
+hipError_t launch_sort_tokens(int dtype, SortParams p, int32_t* counts, int32_t* ranks, hipStream_t s) {
     const int64_t S = p.T * p.k;
     const bool small = sort_small(S, p.E);
     p.chunks = (int)((S + NT - 1) / NT);
     p.counts = counts;
+    p.ranks = ranks;
     if (!small) {
         int nbits = 1;
         while ((1 << nbits) < p.E) ++nbits;
         sort_count_kernel<<<(unsigned)p.chunks, NT, sizeof(int32_t) * (NT / 64) * p.E, s>>>(p.ids, S, p.E, nbits,
-                                                                                         p.slot_row, counts);
+                                                                                         ranks, counts);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -469,8 +472,9 @@ hipError_t launch_unsort_backward(int dtype, const void* dy, const void* rows, c
             auto run = [&](auto threads) {
                 constexpr int TB = decltype(threads)::value;
                 unsort_backward_kernel<V, decltype(stream)::value, TB>
-                    <<<(unsigned)T, TB, 0, s>>>(static_cast<const V*>(dy), static_cast<const V*>(rows), slot_row, w, H,
-                                                k, R, p.C, static_cast<V*>(d_rows), dw);
+                    <<<(unsigned)std::min(T, kMaxGrid / 4), TB, 0, s>>>(static_cast<const V*>(dy),
+                                                                        static_cast<const V*>(rows), slot_row, w, T, H,
+                                                                        k, R, p.C, static_cast<V*>(d_rows), dw);
             };
             if (p.C <= 64) run(std::integral_constant<int, 64>());
             else if (p.C <= 512 || T > 256) run(std::integral_constant<int, 512>());

@@ -45,3 +45,35 @@ def test_a_workspace_of_the_asked_size(nv):
         assert bool((buf[:256] == 0x5A).all()) and bool((buf[256 + n:] == 0x5A).all())
         b = nv.sort_tokens(x, ids, E)
         assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("T,k,H", [(200, 40, 8192), (401, 17, 5000), (30, 250, 4100)])
+def test_work_groups_that_share_tokens(nv, T, k, H):
+    """Few tokens of many choices: several work-groups move a token's row and rank its
+    slots, each by itself."""
+    import torch
+    E = 48
+    g = np.random.RandomState(T)
+    ids = torch.from_numpy(g.randint(0, E, (T, k)).astype(np.int32)).cuda()
+    x = torch.randn((T, H), device="cuda").to(torch.bfloat16)
+    order = torch.sort(ids.view(-1).long(), stable=True).indices
+    for _ in range(20):
+        rows, _, row = nv.sort_tokens(x, ids, E)
+        assert torch.equal(rows, x[order // k])
+        assert torch.equal(row.view(-1)[order], torch.arange(T * k, device="cuda", dtype=torch.int32))
+
+
+def test_more_tokens_than_work_groups(nv):
+    """2^22 tokens and a few: every one is reached."""
+    import torch
+    T, H = (1 << 22) + 5, 8
+    ids = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    x = torch.randint(-100, 100, (T, H), device="cuda").to(torch.bfloat16)
+    rows, off, row = nv.sort_tokens(x, ids, 1)
+    assert off.tolist() == [0, T] and torch.equal(rows, x)
+    w = torch.full((T, 1), 2.0, device="cuda")
+    assert torch.equal(nv.unsort_tokens(rows, row, w), 2 * x) and torch.equal(nv.sort_tokens_backward(rows, row), x)
+    d_rows, dw = nv.unsort_tokens_backward(x, rows, row, w)
+    assert torch.equal(d_rows, 2 * x) and torch.equal(dw[:, 0], (x.float() ** 2).sum(1))
+    d = nv.route_topk_backward(w, ids, torch.full((T, 1), 0.5, device="cuda"), 1)
+    assert bool((d == 0.5).all())                    # 0.5 * (2 - 0.5 * 2)
