@@ -8,6 +8,8 @@
 // authors found to pass all of their statistical tests: element i takes word i % 4
 // of the counter offset + i / 4 under the key `seed`, and is kept where that word
 // is at least p 2^32.
+#include <type_traits>
+
 #include "elements.hpp"
 
 namespace nvfp4 {
@@ -45,22 +47,28 @@ __global__ __launch_bounds__(NT) void dropout_kernel(const T* x, const T* residu
     const uint64_t seed = (uint64_t)rng[0], offset = (uint64_t)rng[1];
     for (int64_t i = ((int64_t)blockIdx.x * NT + threadIdx.x) * V; i < n; i += (int64_t)gridDim.x * NT * V) {
         const int m = (int)min((int64_t)V, n - i);
-        const Vec<T> v = load_vec(x + i, m);
-        Vec<T> r, out;
-        if (residual) r = load_vec<T>(residual + i, m);
+        auto piece = [&](auto whole) {
+            constexpr bool W = decltype(whole)::value;
+            const Vec<T> v = W ? load_vec(x + i) : load_part(x + i, m);
+            Vec<T> r, out;
+            if (residual) r = W ? load_vec(residual + i) : load_part(residual + i, m);
 #pragma unroll
-        for (int h = 0; h < V / 4; ++h) {
-            uint32_t w[4];
-            philox(offset + (uint64_t)(i / 4 + h), seed, w);
+            for (int h = 0; h < V / 4; ++h) {
+                uint32_t w[4];
+                philox(offset + (uint64_t)(i / 4 + h), seed, w);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool keep = w[u] >= least && !none;
-                float f = keep ? to_f32(v.v[4 * h + u]) * scale : 0.0f;
-                if (residual) f = to_f32(r.v[4 * h + u]) + f;
-                out.v[4 * h + u] = from_f32<T>(f);
+                for (int u = 0; u < 4; ++u) {
+                    const bool keep = w[u] >= least && !none;
+                    float f = keep ? to_f32(v.v[4 * h + u]) * scale : 0.0f;
+                    if (residual) f = to_f32(r.v[4 * h + u]) + f;
+                    out.v[4 * h + u] = from_f32<T>(f);
+                }
             }
-        }
-        store_vec<T>(y + i, out, m);
+            if (W) store_vec(y + i, out);
+            else store_part(y + i, out, m);
+        };
+        if (m == V) piece(std::true_type());
+        else piece(std::false_type());
     }
 }
 

@@ -14,9 +14,14 @@
 // atomics, so results do not depend on scheduling.
 //
 // All of it moves memory: a thread holds 16 bytes of one token's row, so that a
-// token is read once and its copies are written from registers. Rows start at
-// any element (odd H): the loads and stores are declared at the element's
-// alignment, which global memory instructions of 16 bytes allow.
+// token is read once and its copies are written from registers, and all loads of a
+// thread are in flight together. Measured, top 8 of 48 experts, H 7168 in bf16 (in
+// a captured graph; floor: the bytes at the 4.9 TB/s of a copy):
+//   8 tokens       sort 5.0 us, way back 3.9, both gradients 6.5 (latency)
+//   1024 tokens    sort 26, way back 21, gradients 40 (partly from the last cache)
+//   4096 tokens    sort 101 (108), way back 91 (108), gradients 187 (203): the
+//                  memory's rate, which is higher for reads than for a copy
+// Rows start at any element (odd H).
 #include <algorithm>
 #include <type_traits>
 
@@ -38,23 +43,23 @@ __device__ __forceinline__ Piece piece_of(int64_t blk, int C) {
 }
 
 // A thread a piece of one token, written to each of its rows.
-template <typename T, bool STREAM>
+template <typename T, bool STREAM, bool WHOLE>
 __global__ __launch_bounds__(NT) void place_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ slot_row,
                                                         int64_t T_, int64_t H, int k, int C, int64_t nblk,
                                                         T* __restrict__ rows) {
-    constexpr int V = kVec<T>;
+    const RowPieces<T, WHOLE> rp{H};
     for (int64_t b = blockIdx.x; b < nblk; b += gridDim.x) {
         const Piece p = piece_of(b, C);
         if (p.t >= T_) return;
-        const int n = (int)min((int64_t)V, H - (int64_t)p.c * V);
-        const Vec<T> v = load_vec(x + p.t * H + (int64_t)p.c * V, n);
+        const int64_t at = rp.start(p.c);
+        const Vec<T> v = __builtin_bit_cast(Vec<T>, rp.load(x + p.t * H + at));
         for (int j0 = 0; j0 < k; j0 += 8) {
             int32_t row[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) row[u] = j0 + u < k ? slot_row[p.t * k + j0 + u] : -1;
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (row[u] >= 0) store_vec<T, STREAM>(rows + (int64_t)row[u] * H + (int64_t)p.c * V, v, n);
+                if (row[u] >= 0) rp.template store<STREAM>(rows + (int64_t)row[u] * H + at, v);
         }
     }
 }
@@ -95,9 +100,8 @@ __global__ __launch_bounds__(NT) void sort_count_kernel(const int32_t* __restric
 // experts' totals, and of each expert the slots before its first one, from all ids
 // (SMALL) or from the chunks' counts. The first work-group writes offsets, those of
 // the first range slot_row.
-template <typename T, bool STREAM, bool SMALL>
+template <typename T, bool STREAM, bool SMALL, bool WHOLE>
 __global__ __launch_bounds__(NT) void sort_rows_kernel(SortParams p) {
-    constexpr int V = kVec<T>;
     extern __shared__ int32_t lds[];
     int32_t* first = lds;                                 // [E + 1]: the totals, then each expert's first row
     int32_t* before = first + p.E + 1;                    // [E]
@@ -171,7 +175,8 @@ __global__ __launch_bounds__(NT) void sort_rows_kernel(SortParams p) {
     if (blockIdx.x == 0)
         for (int i = tid; i <= E; i += NT) p.offsets[i] = first[i];
 
-    // pieces, four of them in flight
+    // pieces, four of them in flight (beyond the last: it again, not written)
+    const RowPieces<T, WHOLE> rp{p.H};
     const T* x = static_cast<const T*>(p.x);
     T* rows = static_cast<T*>(p.rows);
     const int per = (p.C + p.parts - 1) / p.parts, c0 = part * per, width = min(per, p.C - c0);
@@ -179,44 +184,46 @@ __global__ __launch_bounds__(NT) void sort_rows_kernel(SortParams p) {
     const int pieces = tokens * width;
     constexpr int P = 4;
     for (int i0 = tid; i0 < pieces; i0 += P * NT) {
-        Vec<T> v[P];
+        u32x4 v[P];
+        int64_t at[P];
+        int token[P];
 #pragma unroll
         for (int u = 0; u < P; ++u) {
-            const int i = i0 + u * NT, tt = i / width;
-            const int64_t c = (int64_t)(c0 + i - tt * width) * V;
-            if (i < pieces) v[u] = load_vec(x + (t0 + tt) * p.H + c, (int)min((int64_t)V, p.H - c));
+            const int i = min(i0 + u * NT, pieces - 1);
+            token[u] = i / width;
+            at[u] = rp.start(c0 + i - token[u] * width);
+            v[u] = rp.load(x + (t0 + token[u]) * p.H + at[u]);
         }
 #pragma unroll
         for (int u = 0; u < P; ++u) {
-            const int i = i0 + u * NT, tt = i / width;
-            const int64_t c = (int64_t)(c0 + i - tt * width) * V;
-            if (i >= pieces) break;
+            if (i0 + u * NT >= pieces) break;
             for (int j = 0; j < p.k; ++j) {
-                const int r = row[tt * p.k + j];
-                if (r >= 0) store_vec<T, STREAM>(rows + (int64_t)r * p.H + c, v[u], (int)min((int64_t)V, p.H - c));
+                const int r = row[token[u] * p.k + j];
+                if (r >= 0) rp.template store<STREAM>(rows + (int64_t)r * p.H + at[u], __builtin_bit_cast(Vec<T>, v[u]));
             }
         }
     }
 }
 
 // The sum over a token's rows, with weights or (w null) without.
-template <typename T, bool STREAM>
+template <typename T, bool STREAM, bool WHOLE>
 __global__ __launch_bounds__(NT) void gather_rows_kernel(const T* __restrict__ rows,
                                                          const int32_t* __restrict__ slot_row,
                                                          const float* __restrict__ w, int64_t T_, int64_t H, int k,
                                                          int64_t R, int C, int64_t nblk, T* __restrict__ y) {
     constexpr int V = kVec<T>;
+    const RowPieces<T, WHOLE> rp{H};
     for (int64_t b = blockIdx.x; b < nblk; b += gridDim.x) {
         const Piece p = piece_of(b, C);
         if (p.t >= T_) return;
-        const int n = (int)min((int64_t)V, H - (int64_t)p.c * V);
+        const int64_t at = rp.start(p.c);
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
         for (int j0 = 0; j0 < k; j0 += 8) {
             int32_t row[8];
             float wj[8];
-            Vec<T> v[8];
+            u32x4 raw[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 row[u] = j0 + u < k ? slot_row[p.t * k + j0 + u] : -1;
@@ -224,18 +231,19 @@ __global__ __launch_bounds__(NT) void gather_rows_kernel(const T* __restrict__ r
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (row[u] >= 0 && row[u] < R) v[u] = load_vec<T, STREAM>(rows + (int64_t)row[u] * H + (int64_t)p.c * V, n);
+                if (row[u] >= 0 && row[u] < R) raw[u] = rp.template load<STREAM>(rows + (int64_t)row[u] * H + at);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
                 if (row[u] >= 0 && row[u] < R) {
+                    const Vec<T> v = __builtin_bit_cast(Vec<T>, raw[u]);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(wj[u], to_f32(v[u].v[i]), acc[i]);
+                    for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(wj[u], to_f32(v.v[i]), acc[i]);
                 }
         }
         Vec<T> out;
 #pragma unroll
         for (int i = 0; i < V; ++i) out.v[i] = from_f32<T>(acc[i]);
-        store_vec(y + p.t * H + (int64_t)p.c * V, out, n);
+        rp.store(y + p.t * H + at, out);
     }
 }
 
@@ -258,7 +266,7 @@ __device__ __forceinline__ float wave_sum8(const float (&d)[8], int lane) {
 // One work-group a token: d_rows (null: not wanted) and dw (null: not wanted). The
 // token's rows are the same for the whole work-group, so their addresses and the
 // branches on them are scalar.
-template <typename T, bool STREAM, int TB>
+template <typename T, bool STREAM, bool WHOLE, int TB>
 __global__ __launch_bounds__(TB) void unsort_backward_kernel(const T* __restrict__ dy, const T* __restrict__ rows,
                                                              const int32_t* __restrict__ slot_row,
                                                              const float* __restrict__ w, int64_t T_, int64_t H, int k,
@@ -266,6 +274,7 @@ __global__ __launch_bounds__(TB) void unsort_backward_kernel(const T* __restrict
                                                              float* __restrict__ dw) {
     constexpr int V = kVec<T>, J = 8;                     // choices at a time
     __shared__ float red[TB / 64][J];
+    const RowPieces<T, WHOLE> rp{H};
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int64_t t = blockIdx.x; t < T_; t += gridDim.x) {
         for (int j0 = 0; j0 < k; j0 += J) {
@@ -279,13 +288,31 @@ __global__ __launch_bounds__(TB) void unsort_backward_kernel(const T* __restrict
                 dot[u] = 0.0f;
             }
             for (int c = tid; c < C; c += TB) {
-                const int n = (int)min((int64_t)V, H - (int64_t)c * V);
-                const Vec<T> g = load_vec(dy + t * H + (int64_t)c * V, n);
-                Vec<T> v[J];
+                const int64_t at = rp.start(c);
+                const u32x4 graw = rp.load(dy + t * H + at);
+                u32x4 raw[J];
                 if (dw) {
 #pragma unroll
                     for (int u = 0; u < J; ++u)
-                        if (row[u] >= 0) v[u] = load_vec<T, STREAM>(rows + (int64_t)row[u] * H + (int64_t)c * V, n);
+                        if (row[u] >= 0) raw[u] = rp.template load<STREAM>(rows + (int64_t)row[u] * H + at);
+                }
+                const Vec<T> g = __builtin_bit_cast(Vec<T>, graw);
+                if (dw) {
+                    // the last piece's first elements, which the piece before counts, do not count
+                    const int skip = WHOLE ? (int)((int64_t)c * V - at) : 0;
+#pragma unroll
+                    for (int u = 0; u < J; ++u) {
+                        if (row[u] < 0) continue;
+                        const Vec<T> v = __builtin_bit_cast(Vec<T>, raw[u]);
+                        if (skip == 0) {
+#pragma unroll
+                            for (int i = 0; i < V; ++i) dot[u] = __builtin_fmaf(to_f32(g.v[i]), to_f32(v.v[i]), dot[u]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < V; ++i)
+                                if (i >= skip) dot[u] = __builtin_fmaf(to_f32(g.v[i]), to_f32(v.v[i]), dot[u]);
+                        }
+                    }
                 }
                 if (d_rows) {
 #pragma unroll
@@ -294,15 +321,7 @@ __global__ __launch_bounds__(TB) void unsort_backward_kernel(const T* __restrict
                         Vec<T> o;
 #pragma unroll
                         for (int i = 0; i < V; ++i) o.v[i] = from_f32<T>(wj[u] * to_f32(g.v[i]));
-                        store_vec<T, STREAM>(d_rows + (int64_t)row[u] * H + (int64_t)c * V, o, n);
-                    }
-                }
-                if (dw) {
-#pragma unroll
-                    for (int u = 0; u < J; ++u) {
-                        if (row[u] < 0) continue;
-#pragma unroll
-                        for (int i = 0; i < V; ++i) dot[u] = __builtin_fmaf(to_f32(g.v[i]), to_f32(v[u].v[i]), dot[u]);
+                        rp.template store<STREAM>(d_rows + (int64_t)row[u] * H + at, o);
                     }
                 }
             }
@@ -363,7 +382,8 @@ __global__ __launch_bounds__(NT) void route_topk_backward_kernel(const float* __
     for (int i = 4 * tid; i < n; i += 4 * NT) {
         Vec<float> v;
         __builtin_memcpy(&v, out + i, 16);
-        store_vec(to + i, v, n - i);
+        if (n - i >= 4) store_vec(to + i, v);
+        else store_part(to + i, v, n - i);
     }
 }
 
@@ -382,21 +402,21 @@ struct Pieces {
 };
 
 // Whether rows of so many bytes in all pass by the caches: those that do not fit the
-// last one (256 MB), where they push out what follows (4096 tokens, 448 MB: sort 104
-// against 115 us, both gradients of the way back 222 against 239). Smaller ones are
-// found there by whoever reads them next (1024 tokens, 112 MB: the four calls one
-// after another 157 against 127 us).
+// last one (256 MB), where they push out what follows (4096 tokens of 7168, top 8, 448
+// MB: sort 101 against 117 us, its way back 90 against 103, both gradients 187 against
+// 201). Smaller ones are found there by whoever reads them next (1024 tokens, 112 MB:
+// the four calls one after another 136 against 106 us).
 bool streams(int64_t bytes) { return bytes >= (int64_t)256 << 20; }
 
-// Tokens of a work-group and ranges of its pieces: about 1024 work-groups, and four
-// pieces a thread.
+// Tokens of a work-group, about 1024 of those; for few tokens ranges of its pieces
+// down to one a thread (8 tokens of 896 pieces: 2 ranges 6.1 us, 4 5.0, 8 5.0).
 void sort_plan(SortParams& p) {
     int64_t tw = (p.T + 1023) / 1024;
     tw = std::min<int64_t>(tw, NT / p.k > 0 ? NT / p.k : 1);
     p.TW = (int)std::max<int64_t>(tw, 1);
     const int64_t groups = (p.T + p.TW - 1) / p.TW;
     int parts = 1;
-    while (groups * parts < 512 && (int64_t)p.TW * p.C / (2 * parts) >= NT) parts *= 2;
+    while (groups * parts < 512 && (int64_t)p.TW * p.C / (2 * parts) >= NT / 2) parts *= 2;
     p.parts = parts;
 }
 
@@ -430,7 +450,10 @@ hipError_t launch_sort_tokens(int dtype, SortParams p, int32_t* counts, int32_t*
         const size_t lds = sizeof(int32_t) * (2 * (size_t)p.E + 1 + 2 * (size_t)p.TW * p.k);
         with_flag(streams(S * p.H * (int64_t)sizeof(V)), [&](auto stream) {
             with_flag(small, [&](auto sm) {
-                sort_rows_kernel<V, decltype(stream)::value, decltype(sm)::value><<<(unsigned)grid, NT, lds, s>>>(p);
+                with_flag(p.H >= kVec<V>, [&](auto whole) {
+                    sort_rows_kernel<V, decltype(stream)::value, decltype(sm)::value, decltype(whole)::value>
+                        <<<(unsigned)grid, NT, lds, s>>>(p);
+                });
             });
         });
     });
@@ -442,8 +465,10 @@ hipError_t launch_place_rows(int dtype, const void* x, const int32_t* slot_row, 
         using V = decltype(zero);
         const Pieces<V> p(T, H);
         with_flag(streams(T * k * H * (int64_t)sizeof(V)), [&](auto stream) {
-            place_rows_kernel<V, decltype(stream)::value>
-                <<<p.grid, NT, 0, s>>>(static_cast<const V*>(x), slot_row, T, H, k, p.C, p.nblk, static_cast<V*>(rows));
+            with_flag(H >= kVec<V>, [&](auto whole) {
+                place_rows_kernel<V, decltype(stream)::value, decltype(whole)::value><<<p.grid, NT, 0, s>>>(
+                    static_cast<const V*>(x), slot_row, T, H, k, p.C, p.nblk, static_cast<V*>(rows));
+            });
         });
     });
 }
@@ -454,8 +479,10 @@ hipError_t launch_gather_rows(int dtype, const void* rows, const int32_t* slot_r
         using V = decltype(zero);
         const Pieces<V> p(T, H);
         with_flag(streams(T * k * H * (int64_t)sizeof(V)), [&](auto stream) {
-            gather_rows_kernel<V, decltype(stream)::value><<<p.grid, NT, 0, s>>>(
-                static_cast<const V*>(rows), slot_row, w, T, H, k, R, p.C, p.nblk, static_cast<V*>(y));
+            with_flag(H >= kVec<V>, [&](auto whole) {
+                gather_rows_kernel<V, decltype(stream)::value, decltype(whole)::value><<<p.grid, NT, 0, s>>>(
+                    static_cast<const V*>(rows), slot_row, w, T, H, k, R, p.C, p.nblk, static_cast<V*>(y));
+            });
         });
     });
 }
@@ -466,19 +493,24 @@ hipError_t launch_unsort_backward(int dtype, const void* dy, const void* rows, c
         using V = decltype(zero);
         const Pieces<V> p(T, H);
         with_flag(streams(T * k * H * (int64_t)sizeof(V) * (d_rows && dw ? 2 : 1)), [&](auto stream) {
-            // a piece a thread while the tokens do not fill the GPU (8 tokens of 7168: 256
-            // threads 17.7 us, 512 12.0, 1024 10.3), then 512 threads (1024 tokens: 44, 47
-            // and 54 us, 4096: 230, 222 and 225)
-            auto run = [&](auto threads) {
+            // A piece a thread for few tokens (8 of 7168 bf16 values, 896 pieces: 256 threads
+            // 9.4 us, 512 6.9, 1024 6.4; of 2048, 256 pieces: 64 threads 8.5, 256 4.9), no
+            // idle ones for short rows (4096 tokens of 512: 64 threads 13.8, 256 16.7, 512
+            // 23.1; of 2048: 70, 55, 55), and more work-groups than 1024 threads leave room
+            // for (1024 tokens of 4096: 512 threads 23.8, 1024 28.3).
+            auto run = [&](auto threads, auto whole) {
                 constexpr int TB = decltype(threads)::value;
-                unsort_backward_kernel<V, decltype(stream)::value, TB>
+                unsort_backward_kernel<V, decltype(stream)::value, decltype(whole)::value, TB>
                     <<<(unsigned)std::min(T, kMaxGrid / 4), TB, 0, s>>>(static_cast<const V*>(dy),
                                                                         static_cast<const V*>(rows), slot_row, w, T, H,
                                                                         k, R, p.C, static_cast<V*>(d_rows), dw);
             };
-            if (p.C <= 64) run(std::integral_constant<int, 64>());
-            else if (p.C <= 512 || T > 256) run(std::integral_constant<int, 512>());
-            else run(std::integral_constant<int, 1024>());
+            const std::true_type whole;
+            if (H < kVec<V>) run(std::integral_constant<int, 64>(), std::false_type());
+            else if (p.C <= 64) run(std::integral_constant<int, 64>(), whole);
+            else if (p.C <= 256) run(std::integral_constant<int, 256>(), whole);
+            else if (p.C <= 512 || T > 256) run(std::integral_constant<int, 512>(), whole);
+            else run(std::integral_constant<int, 1024>(), whole);
         });
     });
 }
