@@ -674,7 +674,7 @@ def sort_tokens(x, topk_ids, num_experts, rows=None, workspace=None):
         with torch.cuda.device(index):
             return sort_tokens(x, topk_ids, num_experts, rows, workspace)
     rows = _result(rows, x, (T * k, H), "rows", index)
-    offsets, slot_row = topk_ids.new_empty(max(num_experts, 0) + 1), topk_ids.new_empty((T, k))
+    offsets, slot_row = topk_ids.new_empty(max(num_experts, 0) + 1), torch.empty_like(topk_ids)
     nbytes = _lib.nvfp4_sort_tokens_workspace(T, num_experts, k)
     ws, ws_ptr, ws_bytes = (None, None, 0) if nbytes == 0 and workspace is None else _scratch(workspace, nbytes, index)
     _check(_lib.nvfp4_sort_tokens(x.data_ptr(), code, topk_ids.data_ptr(), T, H, num_experts, k, rows.data_ptr(),
@@ -738,9 +738,10 @@ def unsort_tokens_backward(dy, rows, slot_row, topk_weights, d_rows=None, d_weig
     if (d_rows is not None and not need_d_rows) or (d_weights is not None and not need_d_weights):
         raise ValueError("unsort_tokens_backward: an output is given for a gradient that is not computed")
     if need_d_rows:
-        d_rows = _result(d_rows, rows, rows.shape, "d_rows", index)
+        d_rows = torch.empty_like(rows) if d_rows is None else _result(d_rows, rows, rows.shape, "d_rows", index)
     if need_d_weights:
-        d_weights = _result(d_weights, topk_weights, slot_row.shape, "d_weights", index)
+        d_weights = (torch.empty_like(topk_weights) if d_weights is None
+                     else _result(d_weights, topk_weights, slot_row.shape, "d_weights", index))
     _check(_lib.nvfp4_unsort_tokens_backward(p_dy, rows.data_ptr(), code, slot_row.data_ptr(), w, T, H, k, R,
                                              d_rows.data_ptr() if need_d_rows else None,
                                              d_weights.data_ptr() if need_d_weights else None,
@@ -877,7 +878,7 @@ def dropout(x, p, rng, residual=None, y=None):
         with torch.cuda.device(index):
             return dropout(x, p, rng, residual, y)
     r = None if residual is None else _operands(index, (residual, x.dtype, x.shape, "residual"))[0]
-    y = _result(y, x, x.shape, "y", index)
+    y = torch.empty_like(x) if y is None else _result(y, x, x.shape, "y", index)
     _check(_lib.nvfp4_dropout(x.data_ptr(), r, code, x.numel(), p, rng.data_ptr(), y.data_ptr(),
                               torch._C._cuda_getCurrentRawStream(index)), "nvfp4_dropout")
     return y
@@ -892,7 +893,7 @@ def dropout_backward(dy, p, rng, dx=None):
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return dropout_backward(dy, p, rng, dx)
-    dx = _result(dx, dy, dy.shape, "dx", index)
+    dx = torch.empty_like(dy) if dx is None else _result(dx, dy, dy.shape, "dx", index)
     _check(_lib.nvfp4_dropout_backward(dy.data_ptr(), code, dy.numel(), p, rng.data_ptr(), dx.data_ptr(),
                                        torch._C._cuda_getCurrentRawStream(index)), "nvfp4_dropout_backward")
     return dx
