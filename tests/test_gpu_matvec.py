@@ -57,7 +57,8 @@ def check(x, w, alpha, out, gated=False):
 # and inside a group of four, of one to all waves and several groups a wave; odd
 # numbers of column blocks
 SIZES = [(1, 16, 16), (1, 6144, 7168), (2, 48, 32), (3, 32, 144), (5, 112, 528), (13, 7168, 2048), (15, 16, 4112),
-         (16, 64, 512), (17, 144, 640), (16, 528, 1040), (1, 2064, 20000), (33, 272, 784), (100, 512, 1024)]
+         (16, 64, 512), (17, 144, 640), (16, 528, 1040), (1, 2064, 20000), (33, 272, 784), (100, 512, 1024),
+         (7, 4112, 272), (16, 4112, 144), (9, 64, 4096), (8, 4096, 2064)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -71,7 +72,7 @@ def test_one_matrix(nv, M, N, K, dtype):
     got = nv.matvec(x, bq[0], bsf[0], alpha, out=out)
     assert got is out
     check(x, w[0], alpha, out)
-    # each row alone gives the same bits
+    # each row alone gives the same bits (at these sizes as many waves share K)
     for m in {0, M // 2, M - 1}:
         assert torch.equal(nv.matvec(x[m:m + 1], bq[0], bsf[0], alpha), out[m:m + 1])
 
@@ -97,7 +98,8 @@ def _offsets(counts):
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("K,N,counts,rest", [
     (16, 32, [1], 0), (272, 64, [0, 0, 3, 0, 1, 0], 5), (512, 96, [16, 17, 0, 15, 33, 1], 0), (1040, 64, [0, 0, 0], 7),
-    (784, 32, [1 if e % 3 else 0 for e in range(130)], 2), (64, 32, [2] * 512, 1), (7168, 512, [1, 2, 0, 4], 1)])
+    (784, 32, [1 if e % 3 else 0 for e in range(130)], 2), (64, 32, [2] * 512, 1), (7168, 512, [1, 2, 0, 4], 1),
+    (528, 96, [8, 5, 0, 9, 7], 1), (1040, 4192, [5, 8, 3, 6], 0)])
 def test_each_expert_has_its_rows(nv, K, N, counts, rest, gated):
     """Empty experts, experts of more than a tile, more than 64 experts; rows behind
     the last are left as they were."""
@@ -268,3 +270,21 @@ def test_refusals(nv):
             call()
             pytest.fail(f"call {i} was not refused")
     assert nv.matvec(x[:0], bq[0], bsf[0], alpha[:1]).shape == (0, 48)
+
+
+def test_subnormal_values(nv):
+    """bf16 rows of subnormal numbers: 2^-133 steps meet weights up to 2688 and an
+    alpha of 2^100, so that neither the sums nor the results are subnormal."""
+    import torch
+    K, N = 272, 48
+    bq, bsf, w, _ = _weights(nv, 1, K, N, 9)
+    g = torch.Generator().manual_seed(1)
+    bits = torch.randint(-127, 128, (4, K), generator=g)
+    x = (bits.double() * 2.0 ** -133).to(torch.bfloat16).cuda()
+    assert bool((x.double().cpu() == bits.double() * 2.0 ** -133).all())
+    alpha = torch.tensor([2.0 ** 100], device="cuda")
+    out = nv.matvec(x, bq[0], bsf[0], alpha)
+    ref, mag = (x.double() @ w[0]) * 2.0 ** 100, (x.double().abs() @ w[0].abs()) * 2.0 ** 100
+    # (a float32 sum that is subnormal on the way is off by 2^-149 an addition)
+    tol = 2.0 ** -8 * ref.abs() + ((K + 2) * F32 * mag + K * 2.0 ** -49) * 1.01
+    assert bool(((out.double() - ref).abs() <= tol).all())
