@@ -257,11 +257,12 @@ def test_router_gradient_of_repeated_and_foreign_ids(nv):
     assert bool(((got.double() - ref).abs() <= tol).all())
 
 
-def test_streams_and_graph(nv):
+@pytest.mark.parametrize("T,E", [(700, 16), (1000, 16), (4000, 200)])     # each way to rank the slots
+def test_streams_and_graph(nv, T, E):
     """A captured run replays into the same bits on new values, beside eager calls;
     calls in flight on two streams do not meet."""
     import torch
-    T, H, E, k = 700, 264, 16, 8                              # several routing work-groups
+    H, k = 264, 8
     dtype = torch.bfloat16
     x, dy = _randn((T, H), 1.0, 1, dtype), _randn((T, H), 1.0, 2, dtype)
     logits, w = _randn((T, E), 1.0, 3, torch.float32), torch.empty((T, k), device="cuda")
