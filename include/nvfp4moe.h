@@ -633,6 +633,8 @@ int nvfp4_route_topk_backward(const float* d_weights, const int32_t* topk_ids, c
  *   K % 16 == 0, N % 16 == 0 (gated: 32), E <= 512, K <= 2^20, M <= 2^24,
  *   N * pitch_q(K) below 2^31, else NVFP4_ESHAPE (also where tiles of 4 to 16
  *   rows times N / 16 reach 2^23).
+ * The 16 products of a scale group are summed before its scale enters: values of x
+ * beyond 2^121 may take that sum out of float32's range.
  * Made for up to about 16 rows of a matrix, which read it once; each 16 more read
  * it again (many rows: nvfp4_gemm). A row's result depends on its own values,
  * its matrix and the sizes alone.
