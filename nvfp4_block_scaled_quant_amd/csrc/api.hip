@@ -927,7 +927,7 @@ int nvfp4_unsort_tokens_backward(const void* dy, const void* rows, int dtype, co
 int nvfp4_route_topk_backward(const float* d_weights, const int32_t* topk_ids, const float* topk_weights, int64_t T,
                               int64_t E, int64_t topk, float* d_logits, hipStream_t stream) {
     if (T < 0 || E <= 0 || topk <= 0) return NVFP4_EINVAL;
-    if (topk > E || E > kMaxExperts || T * E >= ((int64_t)1 << 31)) return NVFP4_ESHAPE;
+    if (topk > E || E > kMaxExperts || T > (((int64_t)1 << 31) - 1) / E) return NVFP4_ESHAPE;
     if (T == 0) return NVFP4_OK;
     if (!d_weights || !topk_ids || !topk_weights || !d_logits) return NVFP4_EINVAL;
     if (!aligned(d_weights, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(d_logits, 4))

@@ -1,0 +1,22 @@
+"""Sizes whose products leave 64 bits are refused like all that are too large, on the
+host, before any device is touched (runs without a GPU)."""
+import ctypes
+
+import pytest
+
+PTR = ctypes.c_void_p(1 << 20)     # a fake, aligned, never-dereferenced address
+BIG = 1 << 44
+ESHAPE = 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import nvfp4_block_scaled_quant_amd as nv
+    return nv._lib
+
+
+# 2^55 * 512 is 0 in 64 bits; the last is the least size that is refused for its product
+@pytest.mark.parametrize("T,E,k", [(1 << 55, 512, 8), ((1 << 55) + 1, 512, 8), (1 << 62, 4, 1), ((1 << 63) - 1, 3, 1),
+                                   (1 << 31, 1, 1), ((1 << 31) // 3 + 1, 3, 1)])
+def test_router_gradient(lib, T, E, k):
+    assert lib.nvfp4_route_topk_backward(PTR, PTR, PTR, T, E, k, PTR, None) == ESHAPE
