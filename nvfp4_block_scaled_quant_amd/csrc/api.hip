@@ -947,7 +947,8 @@ int nvfp4_matvec(const void* x, int dtype, const uint8_t* bq, const uint8_t* bsf
     const bool gated = flags & NVFP4_MATVEC_GATED, halves = flags & NVFP4_MATVEC_ALPHA_PER_HALF;
     if (halves && !gated) return NVFP4_EINVAL;
     if (K % 16 || N % (gated ? 32 : 16) || E > kMaxExperts || (!offsets && E != 1)) return NVFP4_ESHAPE;
-    if (K > (int64_t)1 << 20 || N * pitch_q(K) >= 0x7FFFFFFF || M > (int64_t)1 << 24) return NVFP4_ESHAPE;
+    if (K > (int64_t)1 << 20 || N >= 0x7FFFFFFF || M > (int64_t)1 << 24) return NVFP4_ESHAPE;   // then no product wraps
+    if (N * pitch_q(K) >= 0x7FFFFFFF) return NVFP4_ESHAPE;
     // (a launch has fewer than 2^32 threads, a work-group up to 512)
     if (matvec_tiles(M, offsets ? E : 0) * (N / 16) >= (int64_t)1 << 23) return NVFP4_ESHAPE;
     if (M == 0) return NVFP4_OK;

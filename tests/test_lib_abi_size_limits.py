@@ -20,3 +20,12 @@ def lib():
                                    (1 << 31, 1, 1), ((1 << 31) // 3 + 1, 3, 1)])
 def test_router_gradient(lib, T, E, k):
     assert lib.nvfp4_route_topk_backward(PTR, PTR, PTR, T, E, k, PTR, None) == ESHAPE
+
+
+@pytest.mark.parametrize("M,N,K,offsets", [
+    (1 << 24, 1 << 48, 1 << 17, None),          # N * pitch_q(K) and the tiles' number wrap to 0
+    (0, 1 << 60, 1 << 16, None), (0, 1 << 60, 1 << 16, PTR), (1, 1 << 58, 16, None), (1, 1 << 31, 1 << 20, PTR),
+    (4, (1 << 63) - 32, 16, None)])
+@pytest.mark.parametrize("flags", [0, 1])
+def test_matvec(lib, M, N, K, offsets, flags):
+    assert lib.nvfp4_matvec(PTR, 0, PTR, PTR, PTR, offsets, M, N, K, 1, flags, PTR, None) == ESHAPE
