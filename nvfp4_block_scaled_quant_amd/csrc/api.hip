@@ -238,7 +238,7 @@ int nvfp4_quantize_weights_parts(const uint16_t* w, int64_t E, int64_t K, int64_
                                  uint8_t* q, uint8_t* sf, float* alpha, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream) {
     if (E < 0 || K <= 0 || N <= 0 || parts <= 0) return NVFP4_EINVAL;
-    if (K % 16 || E * parts > 65535 || parts > 16 || N % parts || (N / parts) % 8) return NVFP4_ESHAPE;
+    if (K % 16 || parts > 16 || E > 65535 || E * parts > 65535 || N % parts || (N / parts) % 8) return NVFP4_ESHAPE;
     if (E == 0) return NVFP4_OK;
     if (!w || !q || !sf || !alpha) return NVFP4_EINVAL;
     if (!aligned(w, 16) || !aligned(alpha, 4)) return NVFP4_EINVAL;
@@ -294,6 +294,7 @@ int nvfp4_gemm(const uint8_t* aq, const uint8_t* asf, const float* a_gs, const u
                uint16_t* out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
     if (M < 0 || N <= 0 || K <= 0) return NVFP4_EINVAL;
     if (K % 16 || N % 16) return NVFP4_ESHAPE;
+    if (M >= 0x7FFFFFFF || N >= 0x7FFFFFFF || K >= 0x7FFFFFFF) return NVFP4_ESHAPE;      // then no product wraps
     if (M * pitch_h(K) >= 0x7FFFFFFF || N * pitch_q(K) >= 0x7FFFFFFF) return NVFP4_ESHAPE;
     if (M == 0) return NVFP4_OK;
     if (!aq || !asf || !a_gs || !bq || !bsf || !b_alpha || !out) return NVFP4_EINVAL;
@@ -538,7 +539,7 @@ bool lora_shape_ok(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R) {
     if (M < 0 || N <= 0 || K <= 0 || L <= 0 || R <= 0 || K % 16 || N % 16 || R % 8) return false;
     if (R > kLoraMaxRank || L > kLoraMaxAdapters || M > (int64_t)1 << 22) return false;
     if (K > (int64_t)1 << 24 || 2 * R * K >= 0x7FFFFFFF) return false;      // 32-bit offsets inside an adapter
-    return M * pitch_h(K) < 0x7FFFFFFF && N * pitch_q(K) < 0x7FFFFFFF;
+    return N < 0x7FFFFFFF && M * pitch_h(K) < 0x7FFFFFFF && N * pitch_q(K) < 0x7FFFFFFF;
 }
 
 }  // namespace

@@ -29,3 +29,22 @@ def test_router_gradient(lib, T, E, k):
 @pytest.mark.parametrize("flags", [0, 1])
 def test_matvec(lib, M, N, K, offsets, flags):
     assert lib.nvfp4_matvec(PTR, 0, PTR, PTR, PTR, offsets, M, N, K, 1, flags, PTR, None) == ESHAPE
+
+
+def test_gemm(lib):
+    def f(M, N, K):
+        return lib.nvfp4_gemm(*[PTR] * 6, M, N, K, PTR, PTR, BIG, None)
+
+    assert f(1 << 40, 64, 1 << 24) == ESHAPE and f(4, 1 << 48, 1 << 17) == ESHAPE and f(0, 1 << 60, 1 << 16) == ESHAPE
+    assert f(0, 16, 1 << 62) == ESHAPE and f(1 << 62, 16, 16) == ESHAPE
+
+
+def test_gemm_lora(lib):
+    for M, N, K in ((4, 1 << 48, 1 << 17), (0, 1 << 60, 1 << 16)):
+        assert lib.nvfp4_gemm_lora(*[PTR] * 12, M, N, K, 1, 8, PTR, PTR, BIG, None) == ESHAPE
+        assert lib.nvfp4_gemm_lora_workspace(M, N, K, 1, 8) == 0
+
+
+def test_quantize_weights_parts(lib):
+    for E, parts in ((1 << 62, 4), (1 << 60, 16), (4, 1 << 62)):
+        assert lib.nvfp4_quantize_weights_parts(PTR, E, 16, 128, parts, PTR, PTR, PTR, PTR, BIG, None) == ESHAPE
