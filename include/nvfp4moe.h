@@ -635,9 +635,13 @@ int nvfp4_route_topk_backward(const float* d_weights, const int32_t* topk_ids, c
  *   rows times N / 16 reach 2^23).
  * The 16 products of a scale group are summed before its scale enters: values of x
  * beyond 2^121 may take that sum out of float32's range.
- * Made for up to about 16 rows of a matrix, which read it once; each 16 more read
- * it again (many rows: nvfp4_gemm). A row's result depends on its own values,
- * its matrix and the sizes alone.
+ * Made for a few rows of a matrix. Up to 16 rows of one matrix read it once, each 16
+ * more again. With offsets an expert's matrix is read once for every 4, 8 or 16 of its
+ * rows: 4 where M <= 4 E, 8 where M <= 8 E. M counts rows that no expert has too, so
+ * where most of the rows are such (one GPU's share of the experts) fewer rows given,
+ * if the caller knows their number, may run faster. Many rows: nvfp4_gemm, which
+ * quantizes them. A row's result depends on its own values, its matrix and the sizes
+ * alone; M is one of these: alone and in a batch a row may be summed in another order.
  * ------------------------------------------------------------------------ */
 enum { NVFP4_MATVEC_GATED = 1, NVFP4_MATVEC_ALPHA_PER_HALF = 2 };
 int nvfp4_matvec(const void* x, int dtype, const uint8_t* bq, const uint8_t* bsf, const float* b_alpha,

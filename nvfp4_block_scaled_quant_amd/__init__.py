@@ -790,7 +790,8 @@ def matvec(x, bq, bsf, b_alpha, offsets=None, gated=False, out=None):
     offsets[e] .. offsets[e + 1] take matrix e, other rows are not written
     (uninitialized unless out is given). gated: N columns [gate | up], out (M,
     N / 2) = silu(gate) * up of the float32 sums; b_alpha may be per half, (2,) or
-    (E, 2). K % 16 == 0. No graph: see gated_forward."""
+    (E, 2). K % 16 == 0. The order of a row's sum goes by the sizes, M among them. No
+    graph: see gated_forward."""
     if getattr(x, "requires_grad", False) or getattr(b_alpha, "requires_grad", False):
         _refuse_recording("matvec", x=x, b_alpha=b_alpha)
     u8 = torch.uint8

@@ -392,6 +392,9 @@ struct SortParams {
 // in this order): 48 experts, 4096 slots 6.9 in one launch; 6144 8.8, 8.6, 14.7; 16384
 // 17.5, 12.1, 17.4; 65536 -, 25.1, 29.3; 256 experts, 6144 9.4, 13.0, 16.8; 16384 16.7,
 // 24.1, 19.6; 32768 26.5, 38.0, 24.2; 128 experts, 24576 (12288 counts) 22.1, 20.9, 20.2.
+// At the border in experts, 8192, 12288 and 16384 slots: 97 experts 11.2, 12.7, 17.7 in
+// one launch, 11.3, 12.0, 14.6 in two; 128 experts 11.6, 12.8, 18.0 and 12.1, 12.9, 16.4:
+// the larger border costs 97 to 128 experts up to 3 us at 16384 slots and gives 256 7.
 inline bool sort_small(int64_t S, int64_t E) { return S <= (E > 96 ? 16384 : 6144); }
 inline bool sort_by_counts(int64_t S, int64_t E, int64_t k) {
     return !sort_small(S, E) && k <= 256 && (S + 255) / 256 * E <= 12288;
@@ -427,7 +430,12 @@ struct MatvecParams {
 };
 // Rows of a tile: 4, 8 or 16, by the rows that a matrix has in the mean (48 experts,
 // gated 4096 x 7168, tiles of 4, 8, 16 rows: mean 2.7 125, 141, 201 us; 4.0 146,
-// 137, 201; 5.3 184, 155, 208; 8.0 245, 196, 216; 10.7 303, 243, 232).
+// 137, 201; 5.3 184, 155, 208; 8.0 245, 196, 216; 10.7 303, 243, 232). One matrix and
+// experts share the border of 4, which fills one matrix's tile; experts with just 4
+// rows in the mean would take 6 % less in tiles of 8. The host knows M alone, which
+// counts rows behind the last expert's too: a share of the experts, whose rows are
+// mostly those, gets larger tiles than it fills (16 of 48 experts, top 8, with the
+// rows behind and without them: 16 tokens 50, 53 us; 24 74, 53; 32 81, 63; 64 79, 66).
 inline int matvec_tile_rows(int64_t M, int64_t E) { return M <= 4 * E ? 4 : M <= 8 * E ? 8 : 16; }
 // tiles: all there can be (E = 0: one matrix)
 inline int64_t matvec_tiles(int64_t M, int64_t E) {

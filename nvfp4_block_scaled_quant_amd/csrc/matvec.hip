@@ -34,9 +34,10 @@
 //   16 rows of 6144 x 7168       13.0 us, of 7168 x 2048 6.6 us: issue of the MFMAs
 //                                and of the scales' multiply-adds beside the stream
 //   8 tokens' experts, gated     6.7 TB/s (37 experts of 4096 x 7168: 91 us)
-//   32 tokens' experts, gated    154 us (48 experts, 5.2 TB/s)
+//   32 tokens' experts, gated    154 to 170 us by the routing (47, 48 experts: 5.0, 4.7 TB/s)
 // Scaling the weights before 16x16x32 MFMAs, 16 instructions for 8 of them in bf16,
-// was slower at 1 row (11.3 us) and equal at 13.
+// was slower at 1 row (11.3 us); for tiles of 16 rows alone it took 5 to 15 % less (16 x
+// 28672 x 4096 23.1 against 26.6 us) and is not built in yet.
 #include <type_traits>
 
 #include "elements.hpp"
