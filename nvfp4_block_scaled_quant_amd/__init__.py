@@ -619,6 +619,7 @@ def gated_backward(d_act, x, w13, gate_up, dx=None, dw13=None, need_dx=True, nee
 # element types of the operators that take several (enum nvfp4_dtype)
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _MATVEC_GATED, _MATVEC_ALPHA_PER_HALF = 1, 2
+_MAX_EXPERTS, _ESHAPE = 512, 2
 _MALFORMED = (AttributeError, KeyError, TypeError, ValueError, IndexError)
 
 # The operators below run for a few microseconds on small batches, about as long as
@@ -673,6 +674,8 @@ def sort_tokens(x, topk_ids, num_experts, rows=None, workspace=None):
     if index != torch._C._cuda_getDevice():                 # the library launches on the current device
         with torch.cuda.device(index):
             return sort_tokens(x, topk_ids, num_experts, rows, workspace)
+    if num_experts > _MAX_EXPERTS:                          # before outputs of that size are allocated
+        raise Nvfp4Error(_ESHAPE, "nvfp4_sort_tokens")
     rows = _result(rows, x, (T * k, H), "rows", index)
     offsets, slot_row = topk_ids.new_empty(max(num_experts, 0) + 1), torch.empty_like(topk_ids)
     nbytes = _lib.nvfp4_sort_tokens_workspace(T, num_experts, k)
@@ -775,6 +778,8 @@ def route_topk_backward(d_weights, topk_ids, topk_weights, num_experts, d_logits
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return route_topk_backward(d_weights, topk_ids, topk_weights, num_experts, d_logits)
+    if num_experts > _MAX_EXPERTS:
+        raise Nvfp4Error(_ESHAPE, "nvfp4_route_topk_backward")
     d_logits = _result(d_logits, d_weights, (T, max(num_experts, 0)), "d_logits", index)
     _check(_lib.nvfp4_route_topk_backward(d_weights.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), T,
                                           num_experts, k, d_logits.data_ptr(),

@@ -120,3 +120,18 @@ def test_more_pieces_than_a_launch_has(nv):
     rows.zero_()
     nv.unsort_tokens(x, row, torch.ones((T, 1), device="cuda"), y=rows)
     assert torch.equal(rows, x)
+
+
+def test_too_many_experts_allocate_nothing(nv):
+    """A number of experts that the library refuses is refused before outputs of that
+    size are allocated."""
+    import torch
+    x, w = torch.zeros((4, 32), device="cuda"), torch.zeros((4, 2), device="cuda")
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    for E in (513, 1 << 31, 1 << 42, 1 << 60):
+        for call in (lambda: nv.sort_tokens(x, ids, E), lambda: nv.route_topk_backward(w, ids, w, E)):
+            torch.cuda.reset_peak_memory_stats()
+            before = torch.cuda.memory_allocated()
+            with pytest.raises(nv.Nvfp4Error):
+                call()
+            assert torch.cuda.max_memory_allocated() - before <= 1 << 20
