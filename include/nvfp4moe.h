@@ -582,8 +582,8 @@ int nvfp4_sort_tokens_backward(const void* d_rows, int dtype, const int32_t* slo
  *   d_rows[slot_row[t][j]] = topk_weights[t][j] * dy[t]
  *   d_weights[t][j] = sum_h dy[t][h] * rows[slot_row[t][j]][h]
  *   d_rows     (R, H) out, or NULL (not computed; topk_weights may then be NULL).
- *              Rows that slot_row does not name are left as they were; one that
- *              it names twice holds one of the two products.
+ *              Rows that slot_row does not name are left as they were; in one
+ *              that it names twice each element holds one of the two products.
  *   d_weights  (T, topk) float32 out, or NULL (not computed; rows may then be
  *              NULL); 0 for slots without a row
  * Both outputs NULL: NVFP4_EINVAL (unless there is nothing to write). Outputs
